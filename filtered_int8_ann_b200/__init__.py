@@ -32,7 +32,9 @@ ST_MAX_OR = 7
 EXPORTS = ("st_index_create", "st_search", "st_search_ex", "st_search_host", "st_search_host_async",
            "st_index_check",
            "st_index_set_option", "st_probe_noalloc", "st_merge_topk", "st_merge_check", "st_index_update",
-           "st_index_delete", "st_merge_topk_union", "st_index_insert", "st_index_destroy", "st_status_string")
+           "st_index_delete", "st_merge_topk_union", "st_index_insert", "st_index_destroy", "st_status_string",
+           "st_kv_plan", "st_kv_append", "st_kv_attend", "st_kv_attend_workspace", "st_beam_select",
+           "st_beam_select_workspace", "st_beam_reorder", "st_decode_check")
 
 
 class StError(RuntimeError):
@@ -47,7 +49,42 @@ class _Extras(ctypes.Structure):
                 ("candidates", ctypes.c_void_p), ("or_masks", ctypes.c_void_p), ("n_or", ctypes.c_int32)]
 
 
+class _KvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_blocks", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("block_size", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class _BeamExtras(ctypes.Structure):
+    _fields_ = [("allow", ctypes.c_void_p), ("allow_request_stride", ctypes.c_int64),
+                ("allow_beam_stride", ctypes.c_int64), ("finished", ctypes.c_void_p),
+                ("out_finished", ctypes.c_void_p), ("end_token", ctypes.c_int32)]
+
+
+class _BeamState(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("row_bytes", ctypes.c_int64),
+                ("src_row_stride", ctypes.c_int64), ("dst_row_stride", ctypes.c_int64), ("outer", ctypes.c_int64),
+                ("src_outer_stride", ctypes.c_int64), ("dst_outer_stride", ctypes.c_int64)]
+
+
 _lib: Optional[ctypes.CDLL] = None
+
+
+def _declare_decode(L: ctypes.CDLL):
+    P, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+    cache = ctypes.POINTER(_KvCache)
+    L.st_kv_plan.argtypes = [P, P, P, i32, i32, i32, i32, i64, P, P, P, P, P, P]
+    L.st_kv_append.argtypes = [cache, P, P, i32, i64, i64, i64, i64, i64, P, P, P]
+    L.st_kv_attend.argtypes = [cache, P, i32, i64, i32, i64, i64, P, i32, P, P, i32, i32, i64, ctypes.c_float, i32,
+                               P, i64, i64, P, i64, P]
+    L.st_kv_attend_workspace.argtypes = [cache, i64, i32, i32, i32, i64, ctypes.POINTER(i64)]
+    L.st_beam_select.argtypes = [P, i32, i64, P, i32, i32, i32, i32, P, P, P, ctypes.POINTER(_BeamExtras), P, i64, P]
+    L.st_beam_select_workspace.argtypes = [i32, i32, i32, i32, ctypes.POINTER(i64)]
+    L.st_beam_reorder.argtypes = [ctypes.POINTER(_BeamState), i32, P, i32, i32, i32, P]
+    L.st_decode_check.argtypes = [P]
+    for f in ("st_kv_plan", "st_kv_append", "st_kv_attend", "st_kv_attend_workspace", "st_beam_select",
+              "st_beam_select_workspace", "st_beam_reorder", "st_decode_check"):
+        getattr(L, f).restype = ctypes.c_int
 
 
 def lib() -> ctypes.CDLL:
@@ -77,6 +114,7 @@ def lib() -> ctypes.CDLL:
               "st_index_set_option", "st_probe_noalloc", "st_merge_topk", "st_merge_check", "st_index_update",
               "st_index_delete", "st_merge_topk_union", "st_index_insert"):
         getattr(L, f).restype = ctypes.c_int
+    _declare_decode(L)
     L.st_index_destroy.argtypes = [P]
     L.st_index_destroy.restype = None
     L.st_status_string.argtypes = [ctypes.c_int]
@@ -264,6 +302,10 @@ def st_merge_topk_union(ids: torch.Tensor, scores: torch.Tensor, out_ids: Option
 def st_merge_check(stream=None) -> int:
     """Synchronize and return the merge's device-side status (ST_OK or ST_ERR_DEVICE)."""
     return lib().st_merge_check(_stream(stream))
+
+
+from .decode import (KvCache, st_beam_reorder, st_beam_select, st_decode_check, st_kv_append,  # noqa: E402
+                     st_kv_attend, st_kv_plan)
 
 
 def st_index_destroy(index: Optional[int]):

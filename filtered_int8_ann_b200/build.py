@@ -12,7 +12,7 @@ PEAKS_SRC = os.path.join(HERE, "microbench", "dp4a_peak.cu")
 PEAKS_OUT = os.path.join(HERE, "libst_peaks.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-shared", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
-         "--expt-relaxed-constexpr"]
+         "--expt-relaxed-constexpr", "--threads", "0"]
 
 
 def sources():

@@ -1,0 +1,292 @@
+// Host side of the decode operators declared in include/st.h: argument checks
+// and the device's decode error word.
+#include <cmath>
+#include <mutex>
+
+#include "decode.cuh"
+
+namespace st {
+
+// Kernels record an index outside its array here; st_decode_check reads and clears it.
+static __device__ uint32_t g_decode_err;
+
+cudaError_t decode_error_address(uint32_t** word)
+{
+    constexpr int kDevices = 64;
+    static std::mutex mu;
+    static uint32_t* known[kDevices] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < kDevices && known[dev]) {
+        *word = known[dev];
+        return cudaSuccess;
+    }
+    void* p = nullptr;
+    e = cudaGetSymbolAddress(&p, g_decode_err);
+    if (e != cudaSuccess) return e;
+    *word = static_cast<uint32_t*>(p);
+    if (dev < kDevices) known[dev] = *word;
+    return cudaSuccess;
+}
+
+cudaError_t decode_error_word(uint32_t* value)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(value, g_decode_err, sizeof(uint32_t));
+    if (e == cudaSuccess && *value) {
+        const uint32_t z = 0;
+        e = cudaMemcpyToSymbol(g_decode_err, &z, sizeof(uint32_t));
+    }
+    return e;
+}
+
+}  // namespace st
+
+namespace {
+
+constexpr int64_t kLimit31 = int64_t(1) << 31;
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// Device (or managed) memory that the current device `device` holds, aligned to `a`.
+bool on_device(const void* p, int device, size_t a)
+{
+    if (p == nullptr || !aligned(p, a)) return false;
+    cudaPointerAttributes attr;
+    if (cudaPointerGetAttributes(&attr, p) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    if (attr.type == cudaMemoryTypeManaged) return true;
+    return attr.type == cudaMemoryTypeDevice && attr.device == device;
+}
+
+st_status to_status(cudaError_t e)
+{
+    if (e == cudaSuccess) return ST_OK;
+    cudaGetLastError();
+    return e == cudaErrorMemoryAllocation ? ST_ERR_OOM : ST_ERR_CUDA;
+}
+
+bool block_size_ok(int32_t s) { return s == 16 || s == 32 || s == 64 || s == 128; }
+
+// Sizes of a cache: INVALID_ARG for what no cache has, UNSUPPORTED for what this one cannot be.
+st_status cache_sizes(const st_kv_cache* c)
+{
+    if (c == nullptr || c->num_blocks < 1 || c->kv_heads < 1 || c->block_size < 1 || c->head_dim < 1)
+        return ST_ERR_INVALID_ARG;
+    if (c->num_blocks > ST_KV_MAX_BLOCKS || c->kv_heads > 1024 || !block_size_ok(c->block_size) ||
+        (c->head_dim != 64 && c->head_dim != 128))
+        return ST_ERR_UNSUPPORTED;
+    return ST_OK;
+}
+
+bool cache_arrays(const st_kv_cache* c, int dev)
+{
+    return on_device(c->k, dev, 16) && on_device(c->v, dev, 16) && on_device(c->k_scale, dev, 4) &&
+           on_device(c->v_scale, dev, 4);
+}
+
+// Strides (elements of 16 bits) of an array of 16-byte vectors.
+bool strides_ok(int64_t token, int64_t head) { return token >= 0 && head >= 0 && token % 8 == 0 && head % 8 == 0; }
+
+st_status attend_sizes(const st_kv_cache* c, int64_t T, int32_t q_heads, int32_t R, int32_t max_q, int64_t max_len)
+{
+    const st_status s = cache_sizes(c);
+    if (s == ST_ERR_INVALID_ARG) return s;
+    if (T < 0 || q_heads < 1 || R < 1 || max_q < 1 || max_q > (1 << 20) || max_len < 1) return ST_ERR_INVALID_ARG;
+    if (q_heads % c->kv_heads != 0) return ST_ERR_INVALID_ARG;
+    if (s != ST_OK) return s;
+    if (R > ST_KV_MAX_ROWS || T >= kLimit31 || max_len >= kLimit31 || q_heads > 65535) return ST_ERR_UNSUPPORTED;
+    return ST_OK;
+}
+
+st_status select_sizes(int32_t B, int32_t K, int32_t V, int32_t keep)
+{
+    if (B < 1 || K < 1 || V < 1 || keep < 1) return ST_ERR_INVALID_ARG;
+    if (B > ST_MAX_B || K > ST_BEAM_MAX_BEAMS || V > ST_BEAM_MAX_VOCAB || keep > ST_BEAM_MAX_KEEP)
+        return ST_ERR_UNSUPPORTED;
+    return ST_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+st_status st_kv_plan(int32_t* table, const int32_t* have, const int32_t* add, int32_t R, int32_t max_blocks,
+                     int32_t num_blocks, int32_t block_size, int64_t T, int64_t* slots, int32_t* sources,
+                     int32_t* row_start, int32_t* lens, int32_t* report, cudaStream_t stream)
+{
+    if (R < 1 || max_blocks < 1 || num_blocks < 1 || T < 0 || !block_size_ok(block_size)) return ST_ERR_INVALID_ARG;
+    if (R > ST_KV_MAX_ROWS || num_blocks > ST_KV_MAX_BLOCKS || int64_t(R) * max_blocks >= kLimit31 || T >= kLimit31 - 1 ||
+        int64_t(max_blocks) * block_size >= kLimit31)
+        return ST_ERR_UNSUPPORTED;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return ST_ERR_CUDA;
+    if (!on_device(table, dev, 4) || !on_device(have, dev, 4) || !on_device(add, dev, 4) ||
+        !on_device(row_start, dev, 4) || !on_device(lens, dev, 4) || !on_device(report, dev, 4))
+        return ST_ERR_INVALID_ARG;
+    if (T > 0 && (!on_device(slots, dev, 8) || !on_device(sources, dev, 4))) return ST_ERR_INVALID_ARG;
+    st::PlanArgs a{table, have, add, R, max_blocks, num_blocks, block_size, T, slots, sources, row_start, lens, report, nullptr};
+    cudaError_t e = st::decode_error_address(&a.err);
+    if (e == cudaSuccess) e = st::launch_kv_plan(a, stream);
+    return to_status(e);
+}
+
+st_status st_kv_append(const st_kv_cache* cache, const void* k, const void* v, st_dtype dtype, int64_t T,
+                       int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                       int64_t v_head_stride, const int64_t* slots, const int32_t* sources,
+                       cudaStream_t stream)
+{
+    if (cache_sizes(cache) == ST_ERR_INVALID_ARG || T < 0 || (dtype != ST_BF16 && dtype != ST_F16) ||
+        !strides_ok(k_token_stride, k_head_stride) || !strides_ok(v_token_stride, v_head_stride))
+        return ST_ERR_INVALID_ARG;
+    if (cache_sizes(cache) != ST_OK || T >= kLimit31) return ST_ERR_UNSUPPORTED;
+    if (T == 0) return ST_OK;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return ST_ERR_CUDA;
+    if (!cache_arrays(cache, dev) || !on_device(k, dev, 16) || !on_device(v, dev, 16) || !on_device(slots, dev, 8) ||
+        (sources != nullptr && !on_device(sources, dev, 4)))
+        return ST_ERR_INVALID_ARG;
+    st::AppendArgs a{*cache, k, v, dtype, T, k_token_stride, k_head_stride, v_token_stride, v_head_stride, slots, sources, nullptr};
+    cudaError_t e = st::decode_error_address(&a.err);
+    if (e == cudaSuccess) e = st::launch_kv_append(a, stream);
+    return to_status(e);
+}
+
+st_status st_kv_attend_workspace(const st_kv_cache* cache, int64_t T, int32_t q_heads, int32_t R, int32_t max_q,
+                                 int64_t max_len, int64_t* bytes)
+{
+    if (bytes == nullptr) return ST_ERR_INVALID_ARG;
+    *bytes = 0;
+    const st_status s = attend_sizes(cache, T, q_heads, R, max_q, max_len);
+    if (s == ST_OK) *bytes = st::kv_attend_workspace(*cache, T, q_heads, R, max_q, max_len);
+    return s;
+}
+
+st_status st_kv_attend(const st_kv_cache* cache, const void* q, st_dtype dtype, int64_t T, int32_t q_heads,
+                       int64_t q_token_stride, int64_t q_head_stride, const int32_t* table, int32_t max_blocks,
+                       const int32_t* row_start, const int32_t* lens, int32_t R, int32_t max_q, int64_t max_len,
+                       float scale, int32_t causal, void* out, int64_t out_token_stride,
+                       int64_t out_head_stride, void* workspace, int64_t workspace_bytes, cudaStream_t stream)
+{
+    const st_status s = attend_sizes(cache, T, q_heads, R, max_q, max_len);
+    if (s == ST_ERR_INVALID_ARG) return s;
+    if ((dtype != ST_BF16 && dtype != ST_F16) || max_blocks < 1 || !std::isfinite(scale) ||
+        !strides_ok(q_token_stride, q_head_stride) || !strides_ok(out_token_stride, out_head_stride) ||
+        max_len > int64_t(max_blocks) * cache->block_size)
+        return ST_ERR_INVALID_ARG;
+    if (s != ST_OK) return s;
+    if (int64_t(R) * max_blocks >= kLimit31) return ST_ERR_UNSUPPORTED;
+    if (T == 0) return ST_OK;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return ST_ERR_CUDA;
+    if (!cache_arrays(cache, dev) || !on_device(q, dev, 16) || !on_device(out, dev, 16) || !on_device(table, dev, 4) ||
+        !on_device(row_start, dev, 4) || !on_device(lens, dev, 4))
+        return ST_ERR_INVALID_ARG;
+    const int64_t need = st::kv_attend_workspace(*cache, T, q_heads, R, max_q, max_len);
+    if (need > 0 && (workspace_bytes < need || !on_device(workspace, dev, 16))) return ST_ERR_INVALID_ARG;
+    st::AttendArgs a{*cache, q, dtype, T, q_heads, q_token_stride, q_head_stride, table, max_blocks, row_start, lens,
+                     R, max_q, max_len, scale * 1.44269504088896340736f, causal, out, out_token_stride, out_head_stride,
+                     workspace, nullptr};
+    cudaError_t e = st::decode_error_address(&a.err);
+    if (e == cudaSuccess) e = st::launch_kv_attend(a, stream);
+    return to_status(e);
+}
+
+st_status st_beam_select_workspace(int32_t B, int32_t K, int32_t V, int32_t keep, int64_t* bytes)
+{
+    if (bytes == nullptr) return ST_ERR_INVALID_ARG;
+    *bytes = 0;
+    const st_status s = select_sizes(B, K, V, keep);
+    if (s == ST_OK) *bytes = st::beam_select_workspace(B, K, V, keep);
+    return s;
+}
+
+st_status st_beam_select(const void* logits, st_dtype dtype, int64_t logits_stride, const float* scores,
+                         int32_t B, int32_t K, int32_t V, int32_t keep, float* out_scores, int32_t* out_parents,
+                         int32_t* out_tokens, const st_beam_extras* extras, void* workspace,
+                         int64_t workspace_bytes, cudaStream_t stream)
+{
+    const st_status s = select_sizes(B, K, V, keep);
+    if (s == ST_ERR_INVALID_ARG) return s;
+    if ((dtype != ST_BF16 && dtype != ST_F16 && dtype != ST_F32) || logits_stride < V) return ST_ERR_INVALID_ARG;
+    st::SelectArgs a{logits, dtype, logits_stride, scores, B, K, V, keep, out_scores, out_parents, out_tokens, {}, workspace};
+    if (extras) a.ex = *extras;
+    if (a.ex.allow_request_stride < 0 || a.ex.allow_beam_stride < 0 ||
+        (a.ex.finished == nullptr) != (a.ex.out_finished == nullptr) ||
+        (a.ex.finished && (a.ex.end_token < 0 || a.ex.end_token >= V)))
+        return ST_ERR_INVALID_ARG;
+    if (s != ST_OK) return s;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return ST_ERR_CUDA;
+    if (!on_device(logits, dev, dtype == ST_F32 ? 4 : 2) || !on_device(scores, dev, 4) ||
+        !on_device(out_scores, dev, 4) || !on_device(out_parents, dev, 4) || !on_device(out_tokens, dev, 4) ||
+        (a.ex.allow && !on_device(a.ex.allow, dev, 4)) || (a.ex.finished && !on_device(a.ex.finished, dev, 1)) ||
+        (a.ex.out_finished && !on_device(a.ex.out_finished, dev, 1)))
+        return ST_ERR_INVALID_ARG;
+    const int64_t need = st::beam_select_workspace(B, K, V, keep);
+    if (need > 0 && (workspace_bytes < need || !on_device(workspace, dev, 16))) return ST_ERR_INVALID_ARG;
+    return to_status(st::launch_beam_select(a, stream));
+}
+
+st_status st_beam_reorder(const st_beam_state* states, int32_t n_states, const int32_t* parents, int32_t B,
+                          int32_t K, int32_t keep, cudaStream_t stream)
+{
+    if (states == nullptr || n_states < 1 || B < 1 || K < 1 || keep < 1) return ST_ERR_INVALID_ARG;
+    const int64_t n_src = int64_t(B) * K, n_dst = int64_t(B) * keep;
+    const int64_t far = int64_t(1) << 62;
+    for (int i = 0; i < n_states; ++i) {
+        const st_beam_state& x = states[i];
+        if (x.row_bytes < 0 || x.outer < 0 || x.src_row_stride < 0 || x.dst_row_stride < 0 ||
+            x.src_outer_stride < 0 || x.dst_outer_stride < 0)
+            return ST_ERR_INVALID_ARG;
+    }
+    if (n_states > ST_BEAM_MAX_STATES || n_src >= kLimit31 || n_dst >= kLimit31) return ST_ERR_UNSUPPORTED;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return ST_ERR_CUDA;
+    if (!on_device(parents, dev, 4)) return ST_ERR_INVALID_ARG;
+    // the bytes that each array's rows span, for the overlap checks
+    struct Span {
+        __int128 lo, hi;
+    } src[ST_BEAM_MAX_STATES], dst[ST_BEAM_MAX_STATES];
+    for (int i = 0; i < n_states; ++i) {
+        const st_beam_state& x = states[i];
+        src[i] = dst[i] = Span{0, 0};
+        if (x.row_bytes == 0 || x.outer == 0) continue;
+        if (!on_device(x.src, dev, 1) || !on_device(x.dst, dev, 1)) return ST_ERR_INVALID_ARG;
+        const __int128 ls = __int128(x.outer - 1) * x.src_outer_stride + __int128(n_src - 1) * x.src_row_stride + x.row_bytes;
+        const __int128 ld = __int128(x.outer - 1) * x.dst_outer_stride + __int128(n_dst - 1) * x.dst_row_stride + x.row_bytes;
+        if (ls > far || ld > far) return ST_ERR_INVALID_ARG;
+        // rows of dst apart from each other: rows inside outer parts, or outer parts inside rows
+        const bool rows_inside = (n_dst == 1 || x.dst_row_stride >= x.row_bytes) &&
+                                 (x.outer == 1 || __int128(x.dst_outer_stride) >= __int128(n_dst - 1) * x.dst_row_stride + x.row_bytes);
+        const bool outer_inside = (x.outer == 1 || x.dst_outer_stride >= x.row_bytes) &&
+                                  (n_dst == 1 || __int128(x.dst_row_stride) >= __int128(x.outer - 1) * x.dst_outer_stride + x.row_bytes);
+        if (!rows_inside && !outer_inside) return ST_ERR_INVALID_ARG;
+        src[i].lo = reinterpret_cast<uintptr_t>(x.src);
+        src[i].hi = src[i].lo + ls;
+        dst[i].lo = reinterpret_cast<uintptr_t>(x.dst);
+        dst[i].hi = dst[i].lo + ld;
+    }
+    for (int i = 0; i < n_states; ++i)
+        for (int j = 0; j < n_states; ++j) {
+            if (dst[i].lo < src[j].hi && src[j].lo < dst[i].hi) return ST_ERR_INVALID_ARG;
+            if (i < j && dst[i].lo < dst[j].hi && dst[j].lo < dst[i].hi) return ST_ERR_INVALID_ARG;
+        }
+    uint32_t* err = nullptr;
+    cudaError_t e = st::decode_error_address(&err);
+    if (e == cudaSuccess) e = st::launch_beam_reorder(states, n_states, parents, B, K, keep, err, stream);
+    return to_status(e);
+}
+
+st_status st_decode_check(cudaStream_t stream)
+{
+    if (cudaStreamSynchronize(stream) != cudaSuccess) return ST_ERR_CUDA;
+    uint32_t word = 0;
+    if (st::decode_error_word(&word) != cudaSuccess) return ST_ERR_CUDA;
+    return word ? ST_ERR_DEVICE : ST_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,262 @@
+"""Python side of the decode calls of include/st.h: one step of a beam decode
+over an int8 paged cache. Argument marshalling and checks only, as in the
+package; every step runs in the library's CUDA kernels.
+
+A step, for R rows (beams) with `have` tokens each:
+
+    slots, sources, start, lens, report = st_kv_plan(table, have, add, num_blocks, block_size, T)
+    st_kv_append(cache, k, v, slots, sources)                      # per layer
+    out = st_kv_attend(cache, q, table, start, lens, max_q)        # per layer
+    scores, parents, tokens, finished = st_beam_select(logits, scores, keep)
+    table, lens = (x.flatten(0, 1) for x in st_beam_reorder([table.view(B, K, -1), lens.view(B, K)], parents))
+
+Tensors are on the current CUDA device; work goes to the current stream, or to
+`stream`. Nothing waits. Call each function once before capturing it in a graph.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import Optional, Sequence
+
+import torch
+
+from . import _BeamExtras, _BeamState, _KvCache, _check, _stream, lib
+
+ST_BF16, ST_F16, ST_F32 = 0, 1, 2
+_DTYPES = {torch.bfloat16: ST_BF16, torch.float16: ST_F16, torch.float32: ST_F32}
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _array(x: torch.Tensor, dtype, shape, name: str) -> int:
+    """The address of a dense tensor of this type and shape."""
+    _need(isinstance(x, torch.Tensor) and x.dtype == dtype, f"{name} must be {dtype}")
+    _need(tuple(x.shape) == tuple(shape), f"{name} must have shape {tuple(shape)}, not {tuple(x.shape)}")
+    _need(x.is_contiguous(), f"{name} must be contiguous")
+    return x.data_ptr()
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor, in the allocator's books of the stream that will use it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(s):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+class KvCache:
+    """An int8 paged cache over caller-owned tensors: k, v int8 [num_blocks,
+    kv_heads, block_size, head_dim] and their scales float32 [num_blocks,
+    kv_heads]. KvCache.empty allocates one."""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "_c")
+
+    def __init__(self, k, v, k_scale, v_scale):
+        _need(k.dim() == 4, "k must be [num_blocks, kv_heads, block_size, head_dim]")
+        blocks, heads, size, dim = k.shape
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._c = _KvCache(_array(k, torch.int8, k.shape, "k"), _array(v, torch.int8, k.shape, "v"),
+                           _array(k_scale, torch.float32, (blocks, heads), "k_scale"),
+                           _array(v_scale, torch.float32, (blocks, heads), "v_scale"), blocks, heads, size, dim)
+
+    @classmethod
+    def empty(cls, num_blocks: int, kv_heads: int, block_size: int, head_dim: int, device="cuda"):
+        shape = (num_blocks, kv_heads, block_size, head_dim)
+        return cls(torch.zeros(shape, dtype=torch.int8, device=device), torch.zeros(shape, dtype=torch.int8, device=device),
+                   torch.zeros(shape[:2], device=device), torch.zeros(shape[:2], device=device))
+
+    @property
+    def num_blocks(self):
+        return self._c.num_blocks
+
+    @property
+    def kv_heads(self):
+        return self._c.kv_heads
+
+    @property
+    def block_size(self):
+        return self._c.block_size
+
+    @property
+    def head_dim(self):
+        return self._c.head_dim
+
+
+def _vectors(x: torch.Tensor, heads: Optional[int], dim: int, name: str):
+    """[T, heads, dim] with dense vectors; its address and strides."""
+    _need(isinstance(x, torch.Tensor) and x.dtype in (torch.bfloat16, torch.float16), f"{name} must be bfloat16 or float16")
+    _need(x.dim() == 3 and x.shape[2] == dim and (heads is None or x.shape[1] == heads),
+          f"{name} must be [T, {'heads' if heads is None else heads}, {dim}], not {tuple(x.shape)}")
+    _need(x.stride(2) == 1, f"{name} must have dense vectors")
+    # strides of extents of one say nothing
+    return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else 0, x.stride(1) if x.shape[1] > 1 else 0
+
+
+def st_kv_plan(table: torch.Tensor, have: torch.Tensor, add: torch.Tensor, num_blocks: int, block_size: int, T: int,
+               slots: Optional[torch.Tensor] = None, sources: Optional[torch.Tensor] = None,
+               row_start: Optional[torch.Tensor] = None, lens: Optional[torch.Tensor] = None,
+               report: Optional[torch.Tensor] = None, stream=None):
+    """Blocks for the rows' next tokens: table int32 [R, max_blocks] (written in
+    place), have and add int32 [R], room for T new tokens. Returns (slots int64
+    [T], sources int32 [T], row_start int32 [R + 1], lens int32 [R], report
+    int32 [4]); see st_kv_plan in include/st.h for what they hold."""
+    _need(table.dim() == 2, "table must be [R, max_blocks]")
+    R, width = table.shape
+    dev = table.device
+    new = lambda x, shape, dtype: _empty(shape, dtype, dev, stream) if x is None else x  # noqa: E731
+    slots, sources = new(slots, (T,), torch.int64), new(sources, (T,), torch.int32)
+    row_start, lens, report = new(row_start, (R + 1,), torch.int32), new(lens, (R,), torch.int32), new(report, (4,), torch.int32)
+    i32 = torch.int32
+    _check(lib().st_kv_plan(_array(table, i32, (R, width), "table"), _array(have, i32, (R,), "have"),
+                            _array(add, i32, (R,), "add"), R, width, num_blocks, block_size, T,
+                            _array(slots, torch.int64, (T,), "slots"), _array(sources, i32, (T,), "sources"),
+                            _array(row_start, i32, (R + 1,), "row_start"), _array(lens, i32, (R,), "lens"),
+                            _array(report, i32, (4,), "report"), _stream(stream)), "st_kv_plan")
+    return slots, sources, row_start, lens, report
+
+
+def st_kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+                 sources: Optional[torch.Tensor] = None, stream=None):
+    """Quantise keys and values [T, kv_heads, head_dim] (bfloat16 or float16,
+    any multiple-of-8 strides) into the cache's slots int64 [T]."""
+    c = cache._c
+    pk, kt, kh = _vectors(k, c.kv_heads, c.head_dim, "k")
+    pv, vt, vh = _vectors(v, c.kv_heads, c.head_dim, "v")
+    T = k.shape[0]
+    _need(v.shape[0] == T and v.dtype == k.dtype, "k and v must have the same tokens and type")
+    _check(lib().st_kv_append(ctypes.byref(c), pk, pv, _DTYPES[k.dtype], T, kt, kh, vt, vh,
+                              _array(slots, torch.int64, (T,), "slots"),
+                              None if sources is None else _array(sources, torch.int32, (T,), "sources"),
+                              _stream(stream)), "st_kv_append")
+
+
+def st_kv_attend(cache: KvCache, q: torch.Tensor, table: torch.Tensor, row_start: torch.Tensor, lens: torch.Tensor,
+                 max_q: int, max_len: Optional[int] = None, scale: Optional[float] = None, causal: bool = True,
+                 out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of query tokens q [T, q_heads, head_dim] over the rows' cached
+    tokens (table int32 [R, max_blocks], row_start int32 [R + 1], lens int32 [R]).
+    max_q and max_len bound a row's query and cached tokens; scale defaults to
+    head_dim ** -0.5. `out` rows behind row_start[R] are left as they were (a new `out` holds anything there)."""
+    c = cache._c
+    pq, qt, qh = _vectors(q, None, c.head_dim, "q")
+    T, heads = q.shape[0], q.shape[1]
+    _need(table.dim() == 2, "table must be [R, max_blocks]")
+    R, width = table.shape
+    max_len = width * c.block_size if max_len is None else max_len
+    if out is None:
+        out = _empty(q.shape, q.dtype, q.device, stream)
+    _need(out.shape == q.shape and out.dtype == q.dtype, "out must be like q")
+    po, ot, oh = _vectors(out, heads, c.head_dim, "out")
+    _need(T <= 1 or ot >= c.head_dim, "out's tokens must not overlap")
+    _need(heads <= 1 or oh >= c.head_dim, "out's heads must not overlap")
+    need = ctypes.c_int64(0)
+    L = lib()
+    _check(L.st_kv_attend_workspace(ctypes.byref(c), T, heads, R, max_q, max_len, ctypes.byref(need)),
+           "st_kv_attend_workspace")
+    if need.value and workspace is None:
+        workspace = _empty((need.value,), torch.uint8, q.device, stream)
+    _check(L.st_kv_attend(ctypes.byref(c), pq, _DTYPES[q.dtype], T, heads, qt, qh,
+                          _array(table, torch.int32, (R, width), "table"), width,
+                          _array(row_start, torch.int32, (R + 1,), "row_start"), _array(lens, torch.int32, (R,), "lens"),
+                          R, max_q, max_len, c.head_dim ** -0.5 if scale is None else scale, int(causal), po, ot, oh,
+                          None if workspace is None else workspace.data_ptr(),
+                          0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)),
+           "st_kv_attend")
+    return out
+
+
+def st_beam_select(logits: torch.Tensor, scores: torch.Tensor, keep: int, allow: Optional[torch.Tensor] = None,
+                   finished: Optional[torch.Tensor] = None, end_token: int = 0,
+                   workspace: Optional[torch.Tensor] = None, stream=None):
+    """The `keep` best (beam, token) pairs of each request from logits [B, K, V]
+    (bfloat16, float16 or float32; vocabulary dense, beams evenly spaced) and
+    scores float32 [B, K]. `allow` int32 [B, K, ceil(V / 32)] holds a bit per
+    token (expanded dimensions are read as they are); `finished` bool [B, K]
+    marks beams that only repeat end_token. Returns (scores [B, keep], parents int32, tokens
+    int32, finished bool or None); missing pairs are -inf, -1, -1."""
+    _need(logits.dim() == 3 and logits.dtype in _DTYPES, "logits must be [B, K, V] bfloat16, float16 or float32")
+    B, K, V = logits.shape
+    _need(V <= 1 or logits.stride(2) == 1, "logits must have a dense vocabulary")
+    stride = logits.stride(1) if K > 1 else logits.stride(0) if B > 1 else V
+    _need(B <= 1 or K <= 1 or logits.stride(0) == K * stride, "logits' beams must be evenly spaced")
+    dev = logits.device
+    out_scores = _empty((B, keep), torch.float32, dev, stream)
+    out_parents, out_tokens = _empty((B, keep), torch.int32, dev, stream), _empty((B, keep), torch.int32, dev, stream)
+    ex = _BeamExtras()
+    out_finished = None
+    if allow is not None:
+        _need(allow.dtype in (torch.int32, torch.uint32) and tuple(allow.shape) == (B, K, (V + 31) // 32),
+              "allow must be int32 [B, K, ceil(V / 32)]")
+        _need(allow.shape[2] <= 1 or allow.stride(2) == 1, "allow must have dense words")
+        ex.allow, ex.allow_request_stride, ex.allow_beam_stride = allow.data_ptr(), allow.stride(0), allow.stride(1)
+    if finished is not None:
+        out_finished = _empty((B, keep), torch.bool, dev, stream)
+        ex.finished, ex.out_finished = _array(finished, torch.bool, (B, K), "finished"), out_finished.data_ptr()
+        ex.end_token = end_token
+    L = lib()
+    need = ctypes.c_int64(0)
+    _check(L.st_beam_select_workspace(B, K, V, keep, ctypes.byref(need)), "st_beam_select_workspace")
+    if need.value and workspace is None:
+        workspace = _empty((need.value,), torch.uint8, dev, stream)
+    _check(L.st_beam_select(logits.data_ptr(), _DTYPES[logits.dtype], stride, _array(scores, torch.float32, (B, K), "scores"),
+                            B, K, V, keep, out_scores.data_ptr(), out_parents.data_ptr(), out_tokens.data_ptr(),
+                            ctypes.byref(ex), None if workspace is None else workspace.data_ptr(),
+                            0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)),
+           "st_beam_select")
+    return out_scores, out_parents, out_tokens, out_finished
+
+
+def _dense_from(x: torch.Tensor, dim: int) -> bool:
+    """Are the dimensions from `dim` on one dense run of elements?"""
+    want = 1
+    for n, s in zip(reversed(x.shape[dim:]), reversed(x.stride()[dim:])):
+        if n != 1 and s != want:
+            return False
+        want *= n
+    return True
+
+
+def st_beam_reorder(states: Sequence[torch.Tensor], parents: torch.Tensor, out: Optional[Sequence[torch.Tensor]] = None,
+                    beam_dim: int = 1, stream=None):
+    """The states of the chosen beams: for each tensor, out[b, j] = states[b,
+    parents[b, j]] (zeros where the parent is -1) with parents int32 [B, keep].
+    The request and beam dimensions are beam_dim - 1 and beam_dim; beam_dim = 2
+    takes tensors of several layers [layers, B, K, ...]. Up to 16 tensors go in
+    one launch; `out` must not overlap them."""
+    _need(parents.dim() == 2 and beam_dim in (1, 2), "parents must be [B, keep] and beam_dim 1 or 2")
+    B, keep = parents.shape
+    _need(len(states) > 0, "no states given")
+    K = states[0].shape[beam_dim] if states[0].dim() > beam_dim else -1
+    made = []
+    table = (_BeamState * len(states))()
+    for i, x in enumerate(states):
+        _need(x.dim() > beam_dim and x.shape[beam_dim - 1] == B and x.shape[beam_dim] == K,
+              f"state {i} must have {B} requests of {K} beams at dimension {beam_dim}")
+        shape = x.shape[:beam_dim] + (keep,) + x.shape[beam_dim + 1:]
+        y = _empty(shape, x.dtype, x.device, stream) if out is None else out[i]
+        _need(y.shape == shape and y.dtype == x.dtype, f"out {i} must be {tuple(shape)} {x.dtype}")
+        size = x.element_size()
+        for z, name, n in ((x, "state", K), (y, "out", keep)):
+            _need(_dense_from(z, beam_dim + 1), f"{name} {i} must have dense rows")
+            _need(B <= 1 or n <= 1 or z.stride(beam_dim - 1) == n * z.stride(beam_dim), f"{name} {i}'s beams must be evenly spaced")
+        row = lambda z, n: size * (z.stride(beam_dim) if n > 1 else z.stride(beam_dim - 1) if B > 1 else 0)  # noqa: E731
+        e = table[i]
+        e.src, e.dst = x.data_ptr(), y.data_ptr()
+        e.row_bytes = size * math.prod(x.shape[beam_dim + 1:])
+        e.src_row_stride, e.dst_row_stride = row(x, K), row(y, keep)
+        e.outer = x.shape[0] if beam_dim == 2 else 1
+        e.src_outer_stride, e.dst_outer_stride = (size * x.stride(0), size * y.stride(0)) if beam_dim == 2 else (0, 0)
+        made.append(y)
+    _check(lib().st_beam_reorder(table, len(states), _array(parents, torch.int32, (B, keep), "parents"), B, K, keep,
+                                 _stream(stream)), "st_beam_reorder")
+    return made
+
+
+def st_decode_check(stream=None) -> int:
+    """Synchronize and return the decode calls' device-side status (ST_OK or ST_ERR_DEVICE)."""
+    return lib().st_decode_check(_stream(stream))

@@ -386,6 +386,231 @@ st_status st_index_delete(st_index* idx, const int64_t* ids, int64_t m, cudaStre
 st_status st_index_insert(st_index* idx, const int32_t* lists, const int8_t* items, const uint64_t* sigs,
                           int64_t m, int64_t* out_ids, cudaStream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * One step of a beam decode over an int8 paged cache. A model that writes its
+ * candidates token by token (item codes, or words) runs beside the index on
+ * the same GPU; these calls are the step's work outside its dense layers:
+ *   st_kv_plan      block tables and slot maps of the rows from their lengths
+ *   st_kv_append    new keys and values into the cache, quantised
+ *   st_kv_attend    attention over the cache
+ *   st_beam_select  the best (beam, token) pairs of each request
+ *   st_beam_reorder the states of the chosen beams
+ * They keep no state between calls: every array, workspaces included, is the
+ * caller's, on the device that is current during the call (INVALID_ARG
+ * otherwise), and all work is enqueued on `stream` without waiting, so calls
+ * on different streams that share no array they write may overlap, and all of
+ * them can be captured into graphs. A captured call keeps its workspace: calls
+ * that may overlap need workspaces of their own.
+ *
+ * A kernel that meets an index outside its arrays skips what it names and
+ * sets the device's decode error word (st_decode_check).
+ */
+
+/* Types of the arrays that hold computed numbers. */
+typedef enum { ST_BF16 = 0, ST_F16 = 1, ST_F32 = 2 } st_dtype;
+
+/* Limits of the decode calls (ST_ERR_UNSUPPORTED outside them). */
+#define ST_KV_MAX_BLOCKS 4194304 /* blocks of a cache */
+#define ST_KV_MAX_ROWS 32768     /* rows of a plan or an attention call */
+#define ST_BEAM_MAX_BEAMS 256    /* beams per request (st_beam_select) */
+#define ST_BEAM_MAX_KEEP 512     /* pairs kept per request */
+#define ST_BEAM_MAX_VOCAB 1048576
+#define ST_BEAM_MAX_STATES 16    /* arrays of one st_beam_reorder call */
+
+/*
+ * An int8 cache of keys and values in blocks ("pages") of block_size tokens,
+ * with one scale per block and head: the key of head h of the token at offset
+ * o of block b is k[b][h][o][:] * k_scale[b][h]. Caller-owned device arrays.
+ * block_size is 16, 32, 64 or 128; head_dim 64 or 128; kv_heads 1 to 1024;
+ * k and v 16-byte aligned. A token's slot is block * block_size + offset.
+ */
+typedef struct {
+    int8_t* k;       /* [num_blocks][kv_heads][block_size][head_dim] */
+    int8_t* v;       /* likewise */
+    float* k_scale;  /* [num_blocks][kv_heads] */
+    float* v_scale;
+    int32_t num_blocks, kv_heads, block_size, head_dim;
+} st_kv_cache;
+
+/*
+ * Give the rows' next tokens their slots. Row r holds have[r] tokens in the
+ * blocks table[r][0 .. ceil(have[r] / block_size)) and gets add[r] more.
+ *
+ *   table     device int32 [R][max_blocks]  entries written for new blocks;
+ *                                           entries behind them are left as they were
+ *   have, add device int32 [R]
+ *   T         tokens that slots and sources have room for
+ *   slots     device int64 [T]   the rows' new tokens one row after another:
+ *                                each token's slot; -1 for tokens of rows that were
+ *                                not served and behind the last row's tokens
+ *   sources   device int32 [T]   the block holding the earlier tokens of the
+ *                                token's block: that block itself, or, for a row
+ *                                whose last block other rows share, the shared block
+ *                                (st_kv_append then copies its tokens); -1 likewise
+ *   row_start device int32 [R+1] first token of each row (sums of add), at most T
+ *   lens      device int32 [R]   have + add; -1 for a row that was not served
+ *   report    device int32 [4]   {blocks needed, blocks free, rows not served for
+ *                                want of blocks, of table entries or of T, rows
+ *                                refused}
+ *
+ * Which blocks are free follows from the tables alone: a block that no row's
+ * stored tokens use is free, so rows that ended (have = 0) or were replaced by
+ * other beams' tables (st_beam_reorder) give theirs back without a call. The
+ * free blocks go to the rows in order, the lowest first, and to a row's blocks
+ * in order. A row with add > 0 whose last block is partly filled and used by
+ * another row too (or twice by itself) gets a new block for it, since writing there would
+ * change the other row: full blocks stay shared. Rows are served in order while the
+ * free blocks last: row r is not served when the blocks needed by rows 0 .. r
+ * exceed them (unless it needs none), when have + add exceeds max_blocks *
+ * block_size, or when its tokens end behind T; its table row is left as it was.
+ * A row is refused, and served like those, when have or add is negative, have exceeds
+ * max_blocks * block_size, or a used entry is outside [0, num_blocks) (this sets the
+ * decode error word too).
+ *
+ * Errors: INVALID_ARG (null or non-device pointer, misaligned arrays, R < 1,
+ * max_blocks < 1, T < 0, num_blocks < 1, a block size other than those above),
+ * UNSUPPORTED (R above ST_KV_MAX_ROWS, num_blocks above ST_KV_MAX_BLOCKS,
+ * R * max_blocks or max_blocks * block_size at 2^31 or above, T at 2^31 - 1 or above), CUDA. slots and sources may be NULL when T = 0.
+ */
+st_status st_kv_plan(int32_t* table, const int32_t* have, const int32_t* add, int32_t R, int32_t max_blocks,
+                     int32_t num_blocks, int32_t block_size, int64_t T, int64_t* slots, int32_t* sources,
+                     int32_t* row_start, int32_t* lens, int32_t* report, cudaStream_t stream);
+
+/*
+ * Quantise T tokens' keys and values into their slots.
+ *
+ *   k, v       device bf16 or f16 [T][kv_heads][head_dim], the strides between tokens and
+ *              between heads given in elements (multiples of 8; 16-byte aligned
+ *              base): slices of a fused projection need no copy
+ *   slots      device int64 [T]; a negative slot is skipped
+ *   sources    device int32 [T] or NULL (each token's own block)
+ *
+ * Consecutive tokens with consecutive slots in one block are a run; a block
+ * must not be written by two runs of a call (st_kv_plan never does that).
+ * Per run and head, the block's scale becomes s = max(s0, amax / 127), amax
+ * being the largest finite magnitude of the run and s0 the scale of the
+ * run's source block when the run begins behind offset 0 (else 0); s = 0 when that
+ * is 2^-100 or less. New codes are rint(x * (1 / s)) limited to [-127, 127]
+ * (ties to even; NaN gives 0), 0 where s = 0; the codes of the earlier tokens (offsets before the run) become
+ * rint(code * (s0 / s)), taken from the source block. All of this in fp32. Codes behind
+ * the run are left as they were: they belong to no token.
+ *
+ * Errors: INVALID_ARG (null or non-device pointer, bad strides or alignment, a type other than
+ * those, T < 0), UNSUPPORTED (the cache outside its limits, T at 2^31 or above), CUDA. A slot or
+ * source outside the cache is skipped and sets the decode error word.
+ */
+st_status st_kv_append(const st_kv_cache* cache, const void* k, const void* v, st_dtype dtype, int64_t T,
+                       int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                       int64_t v_head_stride, const int64_t* slots, const int32_t* sources,
+                       cudaStream_t stream);
+
+/*
+ * Attention of each row's query tokens over its cached tokens. For query
+ * token i of the n tokens of row r (row_start[r] .. row_start[r+1]), head h
+ * reading cache head h / (q_heads / kv_heads):
+ *   out = sum_j softmax_j(scale * <q, k_j>) v_j   over the cached tokens j < lens[r]
+ * and, with `causal`, j <= lens[r] - n + i (the query tokens are the row's
+ * last ones). A token that sees nothing (lens[r] <= 0 or fewer cached tokens
+ * than query tokens) gets zeros; a query head holding an infinity or NaN gets
+ * NaN in its output, if it sees anything.
+ *
+ *   q, out     device bf16 or f16 [T][q_heads][head_dim], strides as in st_kv_append;
+ *              out rows behind row_start[R] are left as they were
+ *   table      device int32 [R][max_blocks], row_start device int32 [R+1] (nondecreasing,
+ *              within [0, T]), lens device int32 [R]
+ *   max_q      most query tokens of a row (1 to 2^20); max_len: most cached tokens of a
+ *              row (1 to max_blocks * block_size). They size the launch: a row
+ *              with more of either sets the decode error word, and its tokens get zeros.
+ *   scale      finite
+ *   workspace  device, 16-byte aligned, of at least the bytes that
+ *              st_kv_attend_workspace gives (NULL when that is 0)
+ *
+ * Products are taken in fp16 with fp32 sums: codes are exact there, a query is
+ * scaled by a power of two to its largest element first, and softmax weights
+ * carry 11 bits; maxima, sums and outputs are held in fp32 and rounded once.
+ *
+ * Errors: INVALID_ARG (null or non-device pointer, misaligned arrays or strides,
+ * q_heads not a multiple of kv_heads, sizes outside those above, a workspace that is too small),
+ * UNSUPPORTED (the cache outside its limits, R above ST_KV_MAX_ROWS,
+ * R * max_blocks or T at 2^31 or above, more than 65535 query heads), CUDA. A used table entry outside the cache hides its
+ * tokens and sets the decode error word.
+ */
+st_status st_kv_attend(const st_kv_cache* cache, const void* q, st_dtype dtype, int64_t T, int32_t q_heads,
+                       int64_t q_token_stride, int64_t q_head_stride, const int32_t* table, int32_t max_blocks,
+                       const int32_t* row_start, const int32_t* lens, int32_t R, int32_t max_q, int64_t max_len,
+                       float scale, int32_t causal, void* out, int64_t out_token_stride,
+                       int64_t out_head_stride, void* workspace, int64_t workspace_bytes, cudaStream_t stream);
+/* Bytes of workspace for st_kv_attend with these sizes (same errors for sizes). */
+st_status st_kv_attend_workspace(const st_kv_cache* cache, int64_t T, int32_t q_heads, int32_t R, int32_t max_q,
+                                 int64_t max_len, int64_t* bytes);
+
+/* Optional parts of st_beam_select; any member may be NULL. */
+typedef struct {
+    /* device uint32 words: token v may follow beam i of request b when bit v % 32 of
+       allow[b * allow_request_stride + i * allow_beam_stride + v / 32] is set
+       (strides in words; 0 shares one mask). A token that may not is as if its logit were -inf. */
+    const uint32_t* allow;
+    int64_t allow_request_stride, allow_beam_stride;
+    /* device uint8 [B][K]: a nonzero beam is finished. It has one candidate, end_token
+       at its own score. out_finished, device uint8 [B][keep], then tells which kept pairs
+       are finished: their beam was, or their token is end_token. Both or neither. */
+    const uint8_t* finished;
+    uint8_t* out_finished;
+    int32_t end_token; /* in [0, V) when finished is given */
+} st_beam_extras;
+
+/*
+ * The `keep` best pairs (beam i, token v) of each request by
+ *   score(i, v) = scores[i] + logits[i][v] - ln(sum over allowed u of exp(logits[i][u]))
+ * ordered by score descending, then i * V + v ascending. The order is that of the
+ * numbers as they stand (the sum is taken in 64 bits), not of rounded scores.
+ *
+ *   logits      device bf16, f16 or f32 [B][K][V], consecutive beams logits_stride elements
+ *               apart (at least V); aligned to the element only
+ *   scores      device float [B][K]; a beam whose score is not finite has no candidates
+ *   out_scores  device float [B][keep], out_parents / out_tokens device int32 [B][keep]:
+ *               missing candidates are -inf, -1, -1
+ * A logit that is NaN or +-inf has no candidate and no share of the sum.
+ *
+ * Errors: INVALID_ARG (null or non-device pointer, misaligned arrays, sizes below 1, logits_stride
+ * below V, one of finished and out_finished alone, end_token outside [0, V), negative allow strides, a workspace too
+ * small or not 16-byte aligned), UNSUPPORTED (B above ST_MAX_B, K, keep or V above the limits), CUDA.
+ */
+st_status st_beam_select(const void* logits, st_dtype dtype, int64_t logits_stride, const float* scores,
+                         int32_t B, int32_t K, int32_t V, int32_t keep, float* out_scores, int32_t* out_parents,
+                         int32_t* out_tokens, const st_beam_extras* extras, void* workspace,
+                         int64_t workspace_bytes, cudaStream_t stream);
+st_status st_beam_select_workspace(int32_t B, int32_t K, int32_t V, int32_t keep, int64_t* bytes);
+
+/* One state array of st_beam_reorder: for each o < outer, src holds B * K rows and dst B * keep rows of
+   row_bytes bytes; rows and outer parts lie the given strides (bytes, not negative) apart. */
+typedef struct {
+    const void* src;
+    void* dst;
+    int64_t row_bytes, src_row_stride, dst_row_stride;
+    int64_t outer, src_outer_stride, dst_outer_stride;
+} st_beam_state;
+
+/*
+ * Take the states of the chosen beams: in every array, row (b, j) of dst
+ * becomes row (b, parents[b][j]) of src; zeros where the parent is -1.
+ *   states   HOST array of n_states (1 to ST_BEAM_MAX_STATES)
+ *   parents  device int32 [B][keep]
+ * A parent outside [-1, K) gives zeros and sets the decode error word. src and dst must not
+ * overlap: a beam may be the parent of several (INVALID_ARG where their ranges do, or where dst
+ * rows would overlap). An array with row_bytes = 0 or outer = 0 is skipped.
+ * Errors: INVALID_ARG (null or non-device pointers, negative sizes, overlap), UNSUPPORTED
+ * (more than ST_BEAM_MAX_STATES arrays, B * K or B * keep at 2^31 or above), CUDA.
+ */
+st_status st_beam_reorder(const st_beam_state* states, int32_t n_states, const int32_t* parents, int32_t B,
+                          int32_t K, int32_t keep, cudaStream_t stream);
+
+/* Wait for `stream`, then report and clear the decode error word of the
+   current device: ST_OK, ST_ERR_DEVICE (a call met an index outside its
+   arrays), or ST_ERR_CUDA. */
+st_status st_decode_check(cudaStream_t stream);
+
 /* Free the index (NULL-safe). Waits for the device to finish work that may
    still use it. */
 void st_index_destroy(st_index* idx);

@@ -1,112 +1,487 @@
-// Attention over an int8 paged cache.
-#include "decode.cuh"
+// Attention of a few query tokens per row over an int8 paged cache (a decode step).
+//
+// Bound by the cache's bytes: every code is read once per group of query
+// heads that share it. The work is split along the cache: a CTA takes one row, one cache
+// head, up to 16 "columns" (query token, head) and a stretch of tokens; its four
+// warps take 32 tokens at a time, and the stretches are joined by a second
+// launch when there are several.
+//
+// One pass with a running maximum, in powers of two:
+//   s_j = scale log2(e) ks <q, k_j>, M = max s_j, p_j = 2^(s_j - M), l = sum p_j, O = sum p_j v_j.
+// Products run on mma.sync (m16n8k16, fp16 with fp32 sums): with at most 16 columns a tcgen05 tile
+// of 128 rows would be almost empty, and the codes would have to be converted
+// through shared memory; here they go from global memory to registers in the
+// order the fragments want, so nothing is staged:
+//   S^T = K Q^T    A = 16 tokens x 16 dims: lane (g, t) loads 16 dims of tokens g and g + 8 as
+//                  one vector; which dims stand at which k index is free as long as Q agrees
+//   O^T = V^T P^T  A = 16 dims x 16 tokens: lane (g, t) loads D/8 dims of four tokens and pairs
+//                  the tokens' bytes with byte permutes; B = P^T is S^T's accumulator transposed by movmatrix
+// A code becomes fp16 exactly: with the sign bit flipped it is the low byte of 1024 + 128 + code.
+// A query is scaled by a power of two to below 2 (exact in fp16 down to 2^-24 of
+// its largest element). The weights' V factor is p_j vs_j / max vs, at most 1, so fp16's
+// 11 bits hold it whatever the scales; maxima, sums and O stay in fp32.
+#include "attend.cuh"
 
 namespace st {
 
-constexpr int kAttendBlock = 128;
+constexpr int kDecWarps = 4;
+constexpr int kDecBlock = 32 * kDecWarps;
+constexpr int kDecGroup = 32;             // tokens a warp takes at a time
+constexpr int kDecMaxBlocks = 1024 / 16;  // cache blocks of the longest stretch
 
-template <typename T>
-__device__ __forceinline__ float to_float(T x);
-template <>
-__device__ __forceinline__ float to_float<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <>
-__device__ __forceinline__ float to_float<__half>(__half x) { return __half2float(x); }
-template <typename T>
-__device__ __forceinline__ T from_float(float x);
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
-template <>
-__device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
+template <int D, int NT>
+struct DecShared {
+    int32_t page[kDecMaxBlocks];
+    float ks[kDecMaxBlocks], vs[kDecMaxBlocks];
+    float m[kDecWarps][8 * NT], l[kDecWarps][8 * NT];
+    float o[kDecWarps][8 * NT][D + 4];
+};
 
-// A CTA per query token and head: a key per thread, then an output element per thread.
-template <typename T, int D>
-__global__ void __launch_bounds__(kAttendBlock) kv_attend_kernel(AttendArgs a)
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    __shared__ float s_q[D], s_w[kAttendBlock], s_vs[kAttendBlock], s_red[kAttendBlock / 32];
-    __shared__ int64_t s_at[kAttendBlock];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t t = blockIdx.x;
-    const int h = blockIdx.y, hk = h / (a.q_heads / a.c.kv_heads);
-    int lo = 0, hi = a.R;  // the row holding token t
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (a.row_start[mid + 1] > t) hi = mid;
-        else lo = mid + 1;
-    }
-    if (lo == a.R || a.row_start[lo] > t) return;
-    const int start = a.row_start[lo], n = a.row_start[lo + 1] - start;
-    int64_t len = a.lens[lo];
-    T* out = static_cast<T*>(a.out) + t * a.out_token + h * a.out_head;
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// D bytes of a row's share of a lane: 16 dims (D = 128) or 8 (D = 64) of V
+template <int D>
+struct VecV;
+template <>
+struct VecV<128> { using type = uint4; };
+template <>
+struct VecV<64> { using type = uint2; };
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kDecBlock, NT == 1 ? 4 : 2)
+kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
+{
+    constexpr int KV = D / 64;    // 16-byte vectors of a K row per lane
+    constexpr int MT = D / 16;    // m-tiles of O^T
+    constexpr int VW = D / 32;    // words of a V row per lane
+    constexpr int COLS = 8 * NT;
+    using V = typename VecV<D>::type;
+    extern __shared__ __align__(16) unsigned char raw[];
+    DecShared<D, NT>& sh = *reinterpret_cast<DecShared<D, NT>*>(raw);
+    __shared__ float s_vmax[kDecWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int hk = blockIdx.y, unit = blockIdx.x / splits, split = blockIdx.x - unit * splits;
+    const int row = unit / col_blocks, col0 = (unit - row * col_blocks) * COLS;
+    const int G = a.q_heads / a.c.kv_heads, S = a.c.block_size;
+
+    const int start = min(max(a.row_start[row], 0), int(a.T)), n = min(max(a.row_start[row + 1], start), int(a.T)) - start;
+    int64_t len = max(a.lens[row], 0);
     if (len > a.max_len || n > a.max_q) {
-        if (tid == 0) atomicOr(a.err, kDecErrRow);
+        if (split == 0 && hk == 0 && col0 == 0 && tid == 0) atomicOr(a.err, kDecErrRow);
         len = 0;
+        if (n > a.max_q) {  // more tokens than column blocks: the first writes all its zeros
+            if (split == 0 && col0 == 0) zero_rows<T, D>(a, start, n, hk * G, G);
+            return;
+        }
     }
-    if (a.causal) len = min(len, len - n + (t - start) + 1);
-    const T* q = static_cast<const T*>(a.q) + t * a.q_token + h * a.q_head;
-    for (int d = tid; d < D; d += kAttendBlock) s_q[d] = to_float(q[d]);
-    const int S = a.c.block_size, heads = a.c.kv_heads;
-    __syncthreads();
-    bool finite = true;
-    for (int d = 0; d < D; ++d) finite = finite && fabsf(s_q[d]) < INFINITY;
-    float m = -INFINITY, l = 0.f, o = 0.f;
-    for (int64_t j0 = 0; j0 < len; j0 += kAttendBlock) {
-        __syncthreads();
-        const int64_t j = j0 + tid;
-        float s = -INFINITY;
-        if (j < len) {
-            const int page = a.table[int64_t(lo) * a.max_blocks + j / S];
-            if (page < 0 || page >= a.c.num_blocks) {
-                atomicOr(a.err, kDecErrTable);
-            } else {
-                const int64_t head = int64_t(page) * heads + hk, row = head * S + j % S;
-                const int8_t* k = a.c.k + row * D;
-                float dot = 0.f;
-                for (int d = 0; d < D; d += 16) {
-                    const int4 w = *reinterpret_cast<const int4*>(k + d);
-                    const int8_t* c = reinterpret_cast<const int8_t*>(&w);
-                    for (int u = 0; u < 16; ++u) dot = fmaf(s_q[d + u], float(c[u]), dot);
-                }
-                s = dot * a.c.k_scale[head] * a.scale_log2;
-                s_at[tid] = row * D;
-                s_vs[tid] = a.c.v_scale[head];
+    const int cols = min(COLS, n * G - col0);  // of this block
+    if (cols <= 0) return;
+    const int64_t j0 = int64_t(split) * stretch;
+    if (j0 >= len && split > 0) return;  // the join knows how many stretches a row has
+    const int tokens = int(min(int64_t(stretch), len - j0));
+
+    // blocks of the stretch and their scales
+    const int shift = 31 - __clz(S), pages = (tokens + S - 1) >> shift;
+    const int32_t* table = a.table + int64_t(row) * a.max_blocks + (j0 >> shift);
+    float vmax = 0.f;
+    for (int i = tid; i < pages; i += kDecBlock) {
+        int p = table[i];
+        if (p < 0 || p >= a.c.num_blocks) {
+            atomicOr(a.err, kDecErrTable);
+            p = -1;
+        }
+        const int64_t at = int64_t(p) * a.c.kv_heads + hk;
+        sh.page[i] = p;
+        sh.ks[i] = p < 0 ? 0.f : a.c.k_scale[at];
+        sh.vs[i] = p < 0 ? 0.f : a.c.v_scale[at];
+        vmax = fmaxf(vmax, fabsf(sh.vs[i]));
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
+    if (lane == 0) s_vmax[warp] = vmax;
+
+    // queries: lane (g, t) holds dims 16 t .. 16 t + 15 (and 64 on) of columns g, g + 8, ...
+    uint32_t q[NT][KV][8];
+    float mult[NT][2];  // of columns 8 nt + 2 t and the next: scale log2(e) and the query's power of two
+    int seen[NT][2];    // tokens of the stretch that the column sees
+    float own_mult[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int c = 8 * nt + g, col = col0 + c;
+        float x[KV * 16];
+#pragma unroll
+        for (int i = 0; i < KV * 16; ++i) x[i] = 0.f;
+        if (c < cols) {
+            const T* p = static_cast<const T*>(a.q) + int64_t(start + col / G) * a.q_token +
+                         int64_t(hk * G + col % G) * a.q_head + 16 * t;
+#pragma unroll
+            for (int v = 0; v < KV; ++v) {
+                unpack8<T>(*reinterpret_cast<const uint4*>(p + 64 * v), x + 16 * v);
+                unpack8<T>(*reinterpret_cast<const uint4*>(p + 64 * v + 8), x + 16 * v + 8);
             }
         }
-        float mm = s;
-        for (int off = 16; off > 0; off >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, off));
-        if (lane == 0) s_red[warp] = mm;
-        __syncthreads();
-        mm = m;
-        for (int w = 0; w < kAttendBlock / 32; ++w) mm = fmaxf(mm, s_red[w]);
-        const float shrink = mm > -INFINITY ? exp2f(m - mm) : 1.f;
-        m = mm;
-        s_w[tid] = s > -INFINITY ? exp2f(s - m) : 0.f;
-        __syncthreads();
-        o *= shrink;
-        l *= shrink;
-        const int keys = int(min(int64_t(kAttendBlock), len - j0));
-        for (int u = 0; u < keys; ++u) {
-            const float w = s_w[u];
-            l += w;
-            if (tid < D && w > 0.f) o = fmaf(w * s_vs[u], float(a.c.v[s_at[u] + tid]), o);
+        float big = 0.f;
+        bool finite = true;
+#pragma unroll
+        for (int i = 0; i < KV * 16; ++i) {
+            big = fmaxf(big, fabsf(x[i]));
+            finite = finite && fabsf(x[i]) < INFINITY;
+        }
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        const unsigned ok = __ballot_sync(0xffffffffu, finite) >> (lane & 28) & 15u;
+        const float down = ok == 15u ? pow2_down(big) : 0.f, up = ok == 15u ? pow2_up(big) : NAN;
+#pragma unroll
+        for (int v = 0; v < KV; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                q[nt][v][i] = ok == 15u ? pack_half2(x[16 * v + 2 * i] * down, x[16 * v + 2 * i + 1] * down) : 0u;
+        own_mult[nt] = a.scale_log2 * up;
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int c = 2 * t + i;
+            mult[nt][i] = __shfl_sync(0xffffffffu, own_mult[nt], 4 * c);
+            const int col = col0 + 8 * nt + c;
+            int64_t see = len - j0;
+            if (a.causal) see = len - n + col / G + 1 - j0;
+            seen[nt][i] = 8 * nt + c < cols ? int(max(int64_t(0), min(int64_t(tokens), see))) : 0;
+        }
+    __syncthreads();
+    float vtop = s_vmax[0];
+#pragma unroll
+    for (int w = 1; w < kDecWarps; ++w) vtop = fmaxf(vtop, s_vmax[w]);
+    const float vinv = vtop > 0.f ? 1.f / vtop : 0.f;
+    int least_seen = 0x7fffffff;  // of the whole warp's columns: tiles below it need no mask
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (8 * nt + 2 * t + i < cols) least_seen = min(least_seen, seen[nt][i]);
+    }
+    least_seen = __reduce_min_sync(0xffffffffu, least_seen);
+
+    float o[NT][MT][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        m[nt][0] = m[nt][1] = -INFINITY;
+        l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+    }
+
+    const int64_t head_bytes = int64_t(S) * D;
+    // the codes of the 16 tokens from jj on (a multiple of 16), which lie in one block
+    auto block_of = [&](int jj) { return jj < tokens ? sh.page[jj >> shift] : -1; };
+    auto rows_at = [&](const int8_t* base, int page, int jj) {
+        return base + (int64_t(page) * a.c.kv_heads + hk) * head_bytes + int64_t(jj & (S - 1)) * D;
+    };
+    uint4 kreg[2][2][KV];
+    auto load_k = [&](int jj0) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int jj = jj0 + 16 * h, page = block_of(jj);
+            if (page >= 0) {
+                const int8_t* p = rows_at(a.c.k, page, jj) + g * D + 16 * t;
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int v = 0; v < KV; ++v)
+                        kreg[h][r][v] = ldg_stream(reinterpret_cast<const uint4*>(p + 8 * r * D + 64 * v));
+            }
+        }
+    };
+    load_k(warp * kDecGroup);
+    for (int jj0 = warp * kDecGroup; jj0 < tokens; jj0 += kDecWarps * kDecGroup) {
+        V vreg[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int jj = jj0 + 16 * h, page = block_of(jj);
+            if (page >= 0) {
+                const int8_t* p = rows_at(a.c.v, page, jj) + 2 * t * D + g * (D / 8);
+                vreg[h][0] = ldg_stream(reinterpret_cast<const V*>(p));
+                vreg[h][1] = ldg_stream(reinterpret_cast<const V*>(p + D));
+                vreg[h][2] = ldg_stream(reinterpret_cast<const V*>(p + 8 * D));
+                vreg[h][3] = ldg_stream(reinterpret_cast<const V*>(p + 9 * D));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) vreg[h][i] = V{};
+            }
+        }
+        float s[2][NT][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) s[h][nt][0] = s[h][nt][1] = s[h][nt][2] = s[h][nt][3] = 0.f;
+#pragma unroll
+            for (int v = 0; v < KV; ++v) {
+                const uint32_t w0[4] = {kreg[h][0][v].x, kreg[h][0][v].y, kreg[h][0][v].z, kreg[h][0][v].w};
+                const uint32_t w1[4] = {kreg[h][1][v].x, kreg[h][1][v].y, kreg[h][1][v].z, kreg[h][1][v].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t f[4];
+                    codes_to_half(w0[i], f[0], f[2]);
+                    codes_to_half(w1[i], f[1], f[3]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma16816(s[h][nt], f, q[nt][v][2 * i], q[nt][v][2 * i + 1]);
+                }
+            }
+        }
+        load_k(jj0 + kDecWarps * kDecGroup);
+        // scores, masked; the columns' maxima
+        float f[2];  // V factor of each half
+        float mx[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            mx[nt][0] = m[nt][0];
+            mx[nt][1] = m[nt][1];
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int jj = jj0 + 16 * h, page = block_of(jj);
+            const float ks = page >= 0 ? sh.ks[jj >> shift] : 0.f;
+            f[h] = page >= 0 ? sh.vs[jj >> shift] * vinv : 0.f;
+            const bool whole = page >= 0 && jj + 16 <= least_seen;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s[h][nt][i] *= ks * mult[nt][i & 1];
+                    if (!whole) {
+                        const bool sees = page >= 0 && jj + g + 8 * (i >> 1) < seen[nt][i & 1];
+                        s[h][nt][i] = sees ? s[h][nt][i] : -INFINITY;
+                    }
+                    mx[nt][i & 1] = fmaxf(mx[nt][i & 1], s[h][nt][i]);
+                }
+            }
+        }
+        bool grew = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int off = 4; off <= 16; off <<= 1)
+                    mx[nt][i] = fmaxf(mx[nt][i], __shfl_xor_sync(0xffffffffu, mx[nt][i], off));
+                grew = grew || mx[nt][i] > m[nt][i];
+            }
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float shrink[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    shrink[i] = mx[nt][i] > m[nt][i] ? ex2(m[nt][i] - mx[nt][i]) : 1.f;
+                    m[nt][i] = mx[nt][i];
+                    l[nt][i] *= shrink[i];
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    o[nt][i][0] *= shrink[0];
+                    o[nt][i][1] *= shrink[1];
+                    o[nt][i][2] *= shrink[0];
+                    o[nt][i][3] *= shrink[1];
+                }
+            }
+        }
+        // weights, transposed to the B fragments of 16 tokens x 8 columns
+        uint32_t p[2][NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const float b0 = m[nt][0] > -INFINITY ? m[nt][0] : 0.f, b1 = m[nt][1] > -INFINITY ? m[nt][1] : 0.f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float p0 = ex2(s[h][nt][2 * r] - b0), p1 = ex2(s[h][nt][2 * r + 1] - b1);
+                    l[nt][0] += p0;
+                    l[nt][1] += p1;
+                    p[h][nt][r] = transpose8x8(pack_half2(p0 * f[h], p1 * f[h]));
+                }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t* w[4] = {reinterpret_cast<const uint32_t*>(&vreg[h][0]), reinterpret_cast<const uint32_t*>(&vreg[h][1]),
+                                    reinterpret_cast<const uint32_t*>(&vreg[h][2]), reinterpret_cast<const uint32_t*>(&vreg[h][3])};
+#pragma unroll
+            for (int i = 0; i < VW; ++i) {  // four dims of the four tokens
+                const uint32_t x0 = w[0][i] ^ 0x80808080u, x1 = w[1][i] ^ 0x80808080u, x2 = w[2][i] ^ 0x80808080u,
+                               x3 = w[3][i] ^ 0x80808080u;
+                const uint32_t a01 = __byte_perm(x0, x1, 0x5140), b01 = __byte_perm(x0, x1, 0x7362);
+                const uint32_t a23 = __byte_perm(x2, x3, 0x5140), b23 = __byte_perm(x2, x3, 0x7362);
+                uint32_t f0[4], f1[4];
+                biased_to_half(a01, f0[0], f0[1]);
+                biased_to_half(a23, f0[2], f0[3]);
+                biased_to_half(b01, f1[0], f1[1]);
+                biased_to_half(b23, f1[2], f1[3]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma16816(o[nt][2 * i], f0, p[h][nt][0], p[h][nt][1]);
+                    mma16816(o[nt][2 * i + 1], f1, p[h][nt][0], p[h][nt][1]);
+                }
+            }
         }
     }
-    if (tid < D) out[tid] = from_float<T>(!finite && len > 0 ? NAN : l > 0.f ? o / l : 0.f);
-}
 
-int64_t kv_attend_workspace(const st_kv_cache&, int64_t, int32_t, int32_t, int32_t, int64_t) { return 0; }
-
-cudaError_t launch_kv_attend(const AttendArgs& a, cudaStream_t s)
-{
-    const dim3 grid(unsigned(a.T), unsigned(a.q_heads));
-    const bool bf = a.dtype == ST_BF16;
-    if (a.c.head_dim == 128) {
-        if (bf) kv_attend_kernel<__nv_bfloat16, 128><<<grid, kAttendBlock, 0, s>>>(a);
-        else kv_attend_kernel<__half, 128><<<grid, kAttendBlock, 0, s>>>(a);
-    } else {
-        if (bf) kv_attend_kernel<__nv_bfloat16, 64><<<grid, kAttendBlock, 0, s>>>(a);
-        else kv_attend_kernel<__half, 64><<<grid, kAttendBlock, 0, s>>>(a);
+    // join the warps
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int off = 4; off <= 16; off <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], off);
+            const int c = 8 * nt + 2 * t + i;
+            if (g == 0) {
+                sh.m[warp][c] = m[nt][i];
+                sh.l[warp][c] = l[nt][i];
+            }
+#pragma unroll
+            for (int k = 0; k < MT; ++k) {  // dims g D/8 + 2 k and the next
+                sh.o[warp][c][g * (D / 8) + 2 * k] = o[nt][k][i];
+                sh.o[warp][c][g * (D / 8) + 2 * k + 1] = o[nt][k][2 + i];
+            }
+        }
+    __syncthreads();
+    for (int i = tid; i < cols * D; i += kDecBlock) {
+        const int c = i / D, d = i - c * D, col = col0 + c;
+        float top = sh.m[0][c];
+#pragma unroll
+        for (int w = 1; w < kDecWarps; ++w) top = fmaxf(top, sh.m[w][c]);
+        const float base = top > -INFINITY ? top : 0.f;
+        float sum = 0.f, val = 0.f;
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) {
+            const float z = sh.m[w][c] > -INFINITY ? ex2(sh.m[w][c] - base) : 0.f;
+            sum += sh.l[w][c] * z;
+            val += sh.o[w][c][d] * z;
+        }
+        // a column whose query is not finite has NaN scores, a NaN sum and no maximum
+        const int64_t token = start + col / G, head = hk * G + col % G;
+        if (splits == 1) {
+            static_cast<T*>(a.out)[token * a.out_token + head * a.out_head + d] =
+                from_float<T>(sum == 0.f ? 0.f : val * vtop / sum);
+        } else {
+            const int64_t part = (token * a.q_heads + head) * splits + split;
+            float* po = static_cast<float*>(a.workspace);
+            float* pm = po + a.T * a.q_heads * splits * D;
+            po[part * D + d] = val * vtop;
+            if (d == 0) {
+                pm[2 * part] = top;
+                pm[2 * part + 1] = sum;
+            }
+        }
     }
-    return cudaGetLastError();
 }
+
+// Join a query head's stretches.
+template <typename T, int D>
+__global__ void __launch_bounds__(D) kv_join_kernel(AttendArgs a, int splits, int stretch)
+{
+    dep_enter();
+    const int64_t unit = blockIdx.x;
+    const int64_t token = unit / a.q_heads, head = unit - token * a.q_heads;
+    int lo = 0, hi = a.R;  // the row holding the token
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (a.row_start[mid + 1] > token) hi = mid;
+        else lo = mid + 1;
+    }
+    if (lo == a.R || a.row_start[lo] > token) return;
+    const int n = a.row_start[lo + 1] - a.row_start[lo];
+    int64_t len = max(a.lens[lo], 0);
+    if (n > a.max_q) return;  // written already
+    if (len > a.max_len) len = 0;
+    const int used = int(max(int64_t(1), (len + stretch - 1) / stretch));
+    const float* po = static_cast<const float*>(a.workspace);
+    const float* pm = po + a.T * a.q_heads * splits * D + 2 * unit * splits;
+    po += unit * splits * D + threadIdx.x;
+    float top = -INFINITY;
+    for (int i = 0; i < used; ++i) top = fmaxf(top, pm[2 * i]);
+    const float base = top > -INFINITY ? top : 0.f;
+    float sum = 0.f, val = 0.f;
+    for (int i = 0; i < used; ++i) {
+        const float m = pm[2 * i];
+        const float z = m > -INFINITY ? ex2(m - base) : 0.f;
+        sum += pm[2 * i + 1] * z;
+        val += po[int64_t(i) * D] * z;
+    }
+    static_cast<T*>(a.out)[token * a.out_token + head * a.out_head + threadIdx.x] = from_float<T>(sum == 0.f ? 0.f : val / sum);
+}
+
+struct DecPlan {
+    int splits, stretch, cols, col_blocks;
+};
+
+// Stretches: enough CTAs for the GPU's places (4 per SM), each of 256 to 1024 tokens, in multiples of the
+// longest block; a short row is one stretch, which needs no join.
+static DecPlan dec_plan(const st_kv_cache& c, int32_t q_heads, int32_t R, int32_t max_q, int64_t max_len)
+{
+    DecPlan p;
+    const int64_t cols = int64_t(max_q) * (q_heads / c.kv_heads);
+    p.cols = cols <= 8 ? 8 : 16;
+    p.col_blocks = int((cols + p.cols - 1) / p.cols);
+    const int64_t places = 4 * 148;
+    const int64_t units = int64_t(R) * c.kv_heads * p.col_blocks;
+    int64_t stretch = (max_len * units + places - 1) / places;
+    stretch = stretch < 256 ? 256 : stretch > 1024 ? 1024 : stretch;
+    stretch = (stretch + 127) / 128 * 128;
+    p.splits = int((max_len + stretch - 1) / stretch);
+    if (max_len <= 512) p.splits = 1, stretch = 512;
+    p.stretch = int(stretch);
+    return p;
+}
+
+int64_t kv_decode_workspace(const st_kv_cache& c, int64_t T, int32_t q_heads, int32_t R, int32_t max_q, int64_t max_len)
+{
+    const DecPlan p = dec_plan(c, q_heads, R, max_q, max_len);
+    return p.splits == 1 ? 0 : T * q_heads * p.splits * (int64_t(c.head_dim) + 2) * 4;
+}
+
+template <typename T, int D, int NT>
+static cudaError_t launch_decode(const AttendArgs& a, const DecPlan& p, cudaStream_t s)
+{
+    const int bytes = int(sizeof(DecShared<D, NT>));
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kv_decode_kernel<T, D, NT>), bytes);
+    if (e != cudaSuccess) return e;
+    const int64_t ctas = int64_t(a.R) * p.col_blocks * p.splits;
+    if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    const dim3 grid(unsigned(ctas), unsigned(a.c.kv_heads));
+    kv_decode_kernel<T, D, NT><<<grid, kDecBlock, bytes, s>>>(a, p.splits, p.stretch, p.col_blocks);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || p.splits == 1) return e;
+    return launch_dep(kv_join_kernel<T, D>, dim3(unsigned(a.T * a.q_heads)), dim3(D), 0, s, a, p.splits, p.stretch);
+}
+
+cudaError_t launch_kv_decode(const AttendArgs& a, cudaStream_t s)
+{
+    const DecPlan p = dec_plan(a.c, a.q_heads, a.R, a.max_q, a.max_len);
+    const bool bf = a.dtype == ST_BF16, wide = a.c.head_dim == 128, two = p.cols > 8;
+    if (wide && two) return bf ? launch_decode<__nv_bfloat16, 128, 2>(a, p, s) : launch_decode<__half, 128, 2>(a, p, s);
+    if (wide) return bf ? launch_decode<__nv_bfloat16, 128, 1>(a, p, s) : launch_decode<__half, 128, 1>(a, p, s);
+    if (two) return bf ? launch_decode<__nv_bfloat16, 64, 2>(a, p, s) : launch_decode<__half, 64, 2>(a, p, s);
+    return bf ? launch_decode<__nv_bfloat16, 64, 1>(a, p, s) : launch_decode<__half, 64, 1>(a, p, s);
+}
+
+int64_t kv_attend_workspace(const st_kv_cache& c, int64_t T, int32_t q_heads, int32_t R, int32_t max_q, int64_t max_len)
+{
+    return kv_decode_workspace(c, T, q_heads, R, max_q, max_len);
+}
+
+cudaError_t launch_kv_attend(const AttendArgs& a, cudaStream_t s) { return launch_kv_decode(a, s); }
 
 }  // namespace st

@@ -9,12 +9,13 @@
 // blocks holds j. Everything is whole numbers, so results are the same
 // whatever the order of the atomics.
 //
-// One cluster of 8 CTAs does all of it in one launch: both bitmaps are split
-// over the CTAs' shared memory (2 x 64 KB per CTA for the largest pool of 4M blocks), the marks are
-// distributed-shared-memory atomics, and the cluster barrier orders the steps.
-// The bytes are few (4 per used entry, 12 per token), so the launch and five
-// barriers bound the small calls; spreading over more SMs would need a second
-// launch.
+// A single cluster does all of that in one launch: the bitmaps are split over its
+// CTAs' shared memory (2 x 64 KB in each of 8 CTAs for the largest pool of 4M
+// blocks), the marks are distributed-shared-memory atomics, and the cluster barrier
+// orders the steps. Small pools and tables take one CTA: no remote atomics and cheap barriers.
+// The new tokens' slots (12 bytes each) are written there too, a warp per
+// row, when the rows get few tokens each; prompts' are written by a second
+// launch over the whole GPU, since the cluster's SMs alone store too slowly.
 #include <cooperative_groups.h>
 
 #include "decode.cuh"
@@ -23,8 +24,12 @@ namespace cg = cooperative_groups;
 
 namespace st {
 
-constexpr int kPlanCtas = 8;
+constexpr int kPlanCtas = 8;      // CTAs of the cluster for large calls
 constexpr int kPlanBlock = 1024;
+// Calls up to these sizes take one CTA.
+constexpr int kPlanSmallRows = 1024;
+constexpr int kPlanSmallBlocks = 131072;
+constexpr int64_t kPlanSmallEntries = 32768;
 constexpr int kPlanWarps = kPlanBlock / 32;
 
 struct PlanShared {
@@ -63,8 +68,11 @@ __device__ __forceinline__ unsigned long long block_incl_scan64(unsigned long lo
     return v;
 }
 
-__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanBlock)
-kv_plan_kernel(PlanArgs a, int rows_per, int words_per)
+// CTAS: CTAs of the (only) cluster. all_slots: every token's slot is written
+// here, else only those in the rows' partly filled blocks (whose sources only
+// this kernel knows).
+template <int CTAS>
+__global__ void __launch_bounds__(kPlanBlock) kv_plan_kernel(PlanArgs a, int rows_per, int words_per, bool all_slots)
 {
     extern __shared__ uint32_t smem[];
     __shared__ PlanShared sh;
@@ -181,9 +189,9 @@ kv_plan_kernel(PlanArgs a, int rows_per, int words_per)
     unsigned long long tok_before = 0, tok_all = 0;
     uint32_t need_before = 0, free_before = 0, free_all = 0;
     unsigned long long need_all = 0;
-    uint32_t need_ends[kPlanCtas];  // blocks needed by the rows of CTAs 0..c
+    uint32_t need_ends[CTAS];  // blocks needed by the rows of CTAs 0..c
 #pragma unroll
-    for (int c = 0; c < kPlanCtas; ++c) {
+    for (int c = 0; c < CTAS; ++c) {
         const PlanShared* o = cluster.map_shared_rank(&sh, c);
         if (c < me) {
             tok_before += o->tokens;
@@ -222,10 +230,10 @@ kv_plan_kernel(PlanArgs a, int rows_per, int words_per)
             const uint32_t j = rank++;
             int c = 0;
 #pragma unroll
-            for (int i = 0; i < kPlanCtas - 1; ++i) c += need_ends[i] <= j;
+            for (int i = 0; i < CTAS - 1; ++i) c += need_ends[i] <= j;
             uint32_t before = 0;
 #pragma unroll
-            for (int i = 0; i < kPlanCtas - 1; ++i)
+            for (int i = 0; i < CTAS - 1; ++i)
                 if (i < c) before = need_ends[i];
             const uint32_t* ends = cluster.map_shared_rank(row_end, c);
             int lo = 0, hi = min(a.R, (c + 1) * rows_per) - c * rows_per - 1;  // first row whose end is above j
@@ -246,64 +254,32 @@ kv_plan_kernel(PlanArgs a, int rows_per, int words_per)
     __syncthreads();
     cluster.sync();
 
-    // 5. slots: each warp walks a stretch of tokens, its lanes holding the starts of the next 32 rows
-    const int gw = me * kPlanWarps + warp;
-    const int64_t stretch = ((a.T + kPlanCtas * kPlanWarps - 1) / (kPlanCtas * kPlanWarps) + 31) & ~int64_t(31);
-    const int64_t t0 = gw * stretch, t1 = min(a.T, t0 + stretch);
-    if (t0 < t1) {
-        int lo = 0, hi = a.R;  // first row that ends behind t0 (R: none)
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (__ldcg(a.row_start + mid + 1) > t0) hi = mid;
-            else lo = mid + 1;
-        }
-        int base = lo;  // lane i: the end of row base + i
-        int64_t end = base + lane < a.R ? int64_t(__ldcg(a.row_start + base + lane + 1)) : int64_t(1) << 40;
-        for (int64_t t = t0 + lane; t - lane < t1; t += 32) {
-            int row = 0;
-            bool found = false;
-            while (true) {  // the first row that ends behind t
-                int pos = 0;
-#pragma unroll
-                for (int step = 16; step > 0; step >>= 1) {
-                    const int64_t e = __shfl_sync(0xffffffffu, end, pos + step - 1);
-                    if (e <= t) pos += step;
-                }
-                const int64_t e = __shfl_sync(0xffffffffu, end, pos);
-                if (!found && e > t) {
-                    row = base + pos;
-                    found = true;
-                }
-                if (__all_sync(0xffffffffu, found)) break;
-                base += 32;
-                end = base + lane < a.R ? int64_t(__ldcg(a.row_start + base + lane + 1)) : int64_t(1) << 40;
+    // 5. slots, a warp per row
+    for (int r = r0 + warp; r < r1; r += kPlanWarps) {
+        const int64_t start = __ldcg(a.row_start + r), end = __ldcg(a.row_start + r + 1);
+        const bool served = !(row_need[r - r0] >> 30 & 1u);
+        const int have = a.have[r], into = have % S;
+        const int32_t tail = row_tail[r - r0];
+        const int64_t n = !served || all_slots ? end - start : into ? min(end - start, int64_t(S - into)) : 0;
+        const int32_t* row = a.table + int64_t(r) * a.max_blocks;
+        for (int64_t i = lane; i < n; i += 32) {
+            int64_t slot = -1;
+            int32_t src = -1;
+            if (served) {
+                const int p = have + int(i), c = p / S;
+                src = __ldcg(row + c);
+                slot = int64_t(src) * S + (p - c * S);
+                if (c == have / S && tail >= 0) src = tail;
             }
-            const int last_row = __shfl_sync(0xffffffffu, row, 31);
-            if (t < t1) {
-                int64_t slot = -1;
-                int32_t src = -1;
-                if (row < a.R && __ldcg(a.lens + row) >= 0) {
-                    const int have = a.have[row];
-                    const int start = __ldcg(a.row_start + row);
-                    const int p = have + int(t - start);
-                    const int c = p / S;
-                    src = __ldcg(a.table + int64_t(row) * a.max_blocks + c);
-                    slot = int64_t(src) * S + (p - c * S);
-                    if (c == have / S && have % S != 0) {
-                        const int owner = row / rows_per, i = row - owner * rows_per;
-                        const int32_t tail = cluster.map_shared_rank(row_tail, owner)[i];
-                        if (tail >= 0) src = tail;
-                    }
-                }
-                a.slots[t] = slot;
-                a.sources[t] = src;
-            }
-            if (last_row >= base + 16 && last_row < a.R) {  // keep the window ahead of the walk
-                base = last_row;
-                end = base + lane < a.R ? int64_t(__ldcg(a.row_start + base + lane + 1)) : int64_t(1) << 40;
-            }
+            a.slots[start + i] = slot;
+            a.sources[start + i] = src;
         }
     }
+    if (all_slots)  // behind the last row's tokens
+        for (int64_t t = int64_t(min(tok_all, (unsigned long long)(a.T))) + me * kPlanBlock + tid; t < a.T; t += CTAS * kPlanBlock) {
+            a.slots[t] = -1;
+            a.sources[t] = -1;
+        }
     if (me == 0 && tid == 0) {
         a.report[0] = int32_t(min(need_all, 0x7fffffffull));
         a.report[1] = int32_t(free_all);
@@ -313,18 +289,103 @@ kv_plan_kernel(PlanArgs a, int rows_per, int words_per)
     cluster.sync();  // the CTAs' shared memory stays until all are done with it
 }
 
-cudaError_t launch_kv_plan(const PlanArgs& a, cudaStream_t s)
+// The slots of rows that get many tokens: each warp walks a stretch of tokens,
+// its lanes holding the ends of the next 32 rows.
+constexpr int kSlotBlock = 256;
+constexpr int kSlotStretch = 256;  // tokens per warp
+
+__global__ void __launch_bounds__(kSlotBlock) kv_slots_kernel(PlanArgs a)
 {
-    const int rows_per = (a.R + kPlanCtas - 1) / kPlanCtas;
-    const int words = (a.num_blocks + 31) / 32;
-    const int words_per = (words + kPlanCtas - 1) / kPlanCtas;
-    const size_t bytes = size_t(2 * words_per + 3 * rows_per) * 4;
+    dep_enter();
+    const int lane = threadIdx.x & 31, S = a.block_size;
+    const int64_t t0 = (int64_t(blockIdx.x) * (kSlotBlock / 32) + (threadIdx.x >> 5)) * kSlotStretch;
+    const int64_t t1 = min(a.T, t0 + kSlotStretch);
+    if (t0 >= t1) return;
+    int lo = 0, hi = a.R;  // first row that ends behind t0 (R: none)
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (a.row_start[mid + 1] > t0) hi = mid;
+        else lo = mid + 1;
+    }
+    constexpr int64_t kNever = int64_t(1) << 40;
+    int base = lo;  // lane i: the end of row base + i
+    int64_t end = base + lane < a.R ? int64_t(a.row_start[base + lane + 1]) : kNever;
+    for (int64_t t = t0 + lane; t - lane < t1; t += 32) {
+        int row = 0;
+        bool found = false;
+        while (true) {  // the first row that ends behind t
+            int pos = 0;
+#pragma unroll
+            for (int step = 16; step > 0; step >>= 1) {
+                const int64_t e = __shfl_sync(0xffffffffu, end, pos + step - 1);
+                if (e <= t) pos += step;
+            }
+            const int64_t e = __shfl_sync(0xffffffffu, end, pos);
+            if (!found && e > t) {
+                row = base + pos;
+                found = true;
+            }
+            if (__all_sync(0xffffffffu, found)) break;
+            base += 32;
+            end = base + lane < a.R ? int64_t(a.row_start[base + lane + 1]) : kNever;
+        }
+        const int last_row = __shfl_sync(0xffffffffu, row, 31);
+        if (t < t1) {
+            int64_t slot = -1;
+            int32_t src = -1;
+            bool mine = true;
+            if (row < a.R && a.lens[row] >= 0) {
+                const int have = a.have[row];
+                const int p = have + int(t - a.row_start[row]), c = p / S;
+                mine = have % S == 0 || c != have / S;
+                if (mine) {
+                    src = a.table[int64_t(row) * a.max_blocks + c];
+                    slot = int64_t(src) * S + (p - c * S);
+                }
+            }
+            if (mine) {
+                a.slots[t] = slot;
+                a.sources[t] = src;
+            }
+        }
+        if (last_row >= base + 16 && last_row < a.R) {  // keep the window ahead of the walk
+            base = last_row;
+            end = base + lane < a.R ? int64_t(a.row_start[base + lane + 1]) : kNever;
+        }
+    }
+}
+
+template <int CTAS>
+static cudaError_t launch_plan(const PlanArgs& a, bool all_slots, cudaStream_t s)
+{
+    const int rows_per = (a.R + CTAS - 1) / CTAS;
+    const int words_per = ((a.num_blocks + 31) / 32 + CTAS - 1) / CTAS;
     // the largest: 2 x 16384 words and 3 x 4096 rows
-    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kv_plan_kernel),
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kv_plan_kernel<CTAS>),
                                      (2 * (ST_KV_MAX_BLOCKS / 32 / kPlanCtas) + 3 * (ST_KV_MAX_ROWS / kPlanCtas)) * 4);
     if (e != cudaSuccess) return e;
-    kv_plan_kernel<<<kPlanCtas, kPlanBlock, bytes, s>>>(a, rows_per, words_per);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(CTAS);
+    cfg.blockDim = dim3(kPlanBlock);
+    cfg.dynamicSmemBytes = size_t(2 * words_per + 3 * rows_per) * 4;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {CTAS, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv_plan_kernel<CTAS>, a, rows_per, words_per, all_slots);
+}
+
+cudaError_t launch_kv_plan(const PlanArgs& a, cudaStream_t s)
+{
+    const bool all_slots = a.T <= 4 * int64_t(a.R) + 1024;
+    const bool small = a.R <= kPlanSmallRows && a.num_blocks <= kPlanSmallBlocks &&
+                       int64_t(a.R) * a.max_blocks <= kPlanSmallEntries;
+    cudaError_t e = small ? launch_plan<1>(a, all_slots, s) : launch_plan<kPlanCtas>(a, all_slots, s);
+    if (e != cudaSuccess || all_slots) return e;
+    const int64_t per_cta = int64_t(kSlotBlock / 32) * kSlotStretch;
+    return launch_dep(kv_slots_kernel, dim3(unsigned((a.T + per_cta - 1) / per_cta)), dim3(kSlotBlock), 0, s, a);
 }
 
 }  // namespace st

@@ -16,6 +16,7 @@ Tensors are on the current CUDA device; work goes to the current stream, or to
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import Optional, Sequence
 
@@ -25,6 +26,7 @@ from . import _BeamExtras, _BeamState, _KvCache, _check, _stream, lib
 
 ST_BF16, ST_F16, ST_F32 = 0, 1, 2
 _DTYPES = {torch.bfloat16: ST_BF16, torch.float16: ST_F16, torch.float32: ST_F32}
+_HALVES = (torch.bfloat16, torch.float16)
 
 
 def _need(ok: bool, what: str):
@@ -32,11 +34,16 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
+def _wrong(x, dtype, shape, name: str):
+    _need(isinstance(x, torch.Tensor) and x.dtype == dtype, f"{name} must be a tensor of {dtype}")
+    _need(x.shape == shape, f"{name} must have shape {tuple(shape)}, not {tuple(x.shape)}")
+    _need(False, f"{name} must be contiguous")
+
+
 def _array(x: torch.Tensor, dtype, shape, name: str) -> int:
     """The address of a dense tensor of this type and shape."""
-    _need(isinstance(x, torch.Tensor) and x.dtype == dtype, f"{name} must be {dtype}")
-    _need(tuple(x.shape) == tuple(shape), f"{name} must have shape {tuple(shape)}, not {tuple(x.shape)}")
-    _need(x.is_contiguous(), f"{name} must be contiguous")
+    if not isinstance(x, torch.Tensor) or x.dtype is not dtype or x.shape != shape or not x.is_contiguous():
+        _wrong(x, dtype, shape, name)
     return x.data_ptr()
 
 
@@ -49,6 +56,23 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+@functools.lru_cache(maxsize=256)
+def _select_workspace(B: int, K: int, V: int, keep: int) -> int:
+    need = ctypes.c_int64(0)
+    _check(lib().st_beam_select_workspace(B, K, V, keep, ctypes.byref(need)), "st_beam_select_workspace")
+    return need.value
+
+
+@functools.lru_cache(maxsize=256)
+def _attend_workspace(blocks: int, kv_heads: int, size: int, dim: int, T: int, heads: int, R: int, max_q: int,
+                      max_len: int) -> int:
+    need = ctypes.c_int64(0)
+    c = _KvCache(None, None, None, None, blocks, kv_heads, size, dim)
+    _check(lib().st_kv_attend_workspace(ctypes.byref(c), T, heads, R, max_q, max_len, ctypes.byref(need)),
+           "st_kv_attend_workspace")
+    return need.value
+
+
 class KvCache:
     """An int8 paged cache over caller-owned tensors: k, v int8 [num_blocks,
     kv_heads, block_size, head_dim] and their scales float32 [num_blocks,
@@ -57,12 +81,13 @@ class KvCache:
     __slots__ = ("k", "v", "k_scale", "v_scale", "_c")
 
     def __init__(self, k, v, k_scale, v_scale):
-        _need(k.dim() == 4, "k must be [num_blocks, kv_heads, block_size, head_dim]")
-        blocks, heads, size, dim = k.shape
+        shape = k.shape
+        if len(shape) != 4:
+            raise ValueError("k must be [num_blocks, kv_heads, block_size, head_dim]")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self._c = _KvCache(_array(k, torch.int8, k.shape, "k"), _array(v, torch.int8, k.shape, "v"),
-                           _array(k_scale, torch.float32, (blocks, heads), "k_scale"),
-                           _array(v_scale, torch.float32, (blocks, heads), "v_scale"), blocks, heads, size, dim)
+        self._c = _KvCache(_array(k, torch.int8, shape, "k"), _array(v, torch.int8, shape, "v"),
+                           _array(k_scale, torch.float32, shape[:2], "k_scale"),
+                           _array(v_scale, torch.float32, shape[:2], "v_scale"), *shape)
 
     @classmethod
     def empty(cls, num_blocks: int, kv_heads: int, block_size: int, head_dim: int, device="cuda"):
@@ -88,13 +113,17 @@ class KvCache:
 
 
 def _vectors(x: torch.Tensor, heads: Optional[int], dim: int, name: str):
-    """[T, heads, dim] with dense vectors; its address and strides."""
-    _need(isinstance(x, torch.Tensor) and x.dtype in (torch.bfloat16, torch.float16), f"{name} must be bfloat16 or float16")
-    _need(x.dim() == 3 and x.shape[2] == dim and (heads is None or x.shape[1] == heads),
-          f"{name} must be [T, {'heads' if heads is None else heads}, {dim}], not {tuple(x.shape)}")
-    _need(x.stride(2) == 1, f"{name} must have dense vectors")
+    """[T, heads, dim] of 16-bit floats with dense vectors; its address and strides."""
+    if not isinstance(x, torch.Tensor) or x.dtype not in _HALVES:
+        raise ValueError(f"{name} must be a tensor of bfloat16 or float16")
+    shape = x.shape
+    if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must be [T, {'heads' if heads is None else heads}, {dim}], not {tuple(shape)}")
+    token, head, one = x.stride()
+    if one != 1:
+        raise ValueError(f"{name} must have dense vectors")
     # strides of extents of one say nothing
-    return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else 0, x.stride(1) if x.shape[1] > 1 else 0
+    return x.data_ptr(), token if shape[0] > 1 else 0, head if shape[1] > 1 else 0
 
 
 def st_kv_plan(table: torch.Tensor, have: torch.Tensor, add: torch.Tensor, num_blocks: int, block_size: int, T: int,
@@ -105,13 +134,20 @@ def st_kv_plan(table: torch.Tensor, have: torch.Tensor, add: torch.Tensor, num_b
     place), have and add int32 [R], room for T new tokens. Returns (slots int64
     [T], sources int32 [T], row_start int32 [R + 1], lens int32 [R], report
     int32 [4]); see st_kv_plan in include/st.h for what they hold."""
-    _need(table.dim() == 2, "table must be [R, max_blocks]")
+    if table.dim() != 2:
+        raise ValueError("table must be [R, max_blocks]")
     R, width = table.shape
-    dev = table.device
-    new = lambda x, shape, dtype: _empty(shape, dtype, dev, stream) if x is None else x  # noqa: E731
-    slots, sources = new(slots, (T,), torch.int64), new(sources, (T,), torch.int32)
-    row_start, lens, report = new(row_start, (R + 1,), torch.int32), new(lens, (R,), torch.int32), new(report, (4,), torch.int32)
-    i32 = torch.int32
+    dev, i32 = table.device, torch.int32
+    if slots is None:
+        slots = _empty((T,), torch.int64, dev, stream)
+    if sources is None:
+        sources = _empty((T,), i32, dev, stream)
+    if row_start is None:
+        row_start = _empty((R + 1,), i32, dev, stream)
+    if lens is None:
+        lens = _empty((R,), i32, dev, stream)
+    if report is None:
+        report = _empty((4,), i32, dev, stream)
     _check(lib().st_kv_plan(_array(table, i32, (R, width), "table"), _array(have, i32, (R,), "have"),
                             _array(add, i32, (R,), "add"), R, width, num_blocks, block_size, T,
                             _array(slots, torch.int64, (T,), "slots"), _array(sources, i32, (T,), "sources"),
@@ -128,7 +164,8 @@ def st_kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.
     pk, kt, kh = _vectors(k, c.kv_heads, c.head_dim, "k")
     pv, vt, vh = _vectors(v, c.kv_heads, c.head_dim, "v")
     T = k.shape[0]
-    _need(v.shape[0] == T and v.dtype == k.dtype, "k and v must have the same tokens and type")
+    if v.shape[0] != T or v.dtype is not k.dtype:
+        raise ValueError("k and v must have the same tokens and type")
     _check(lib().st_kv_append(ctypes.byref(c), pk, pv, _DTYPES[k.dtype], T, kt, kh, vt, vh,
                               _array(slots, torch.int64, (T,), "slots"),
                               None if sources is None else _array(sources, torch.int32, (T,), "sources"),
@@ -143,29 +180,35 @@ def st_kv_attend(cache: KvCache, q: torch.Tensor, table: torch.Tensor, row_start
     max_q and max_len bound a row's query and cached tokens; scale defaults to
     head_dim ** -0.5. `out` rows behind row_start[R] are left as they were (a new `out` holds anything there)."""
     c = cache._c
-    pq, qt, qh = _vectors(q, None, c.head_dim, "q")
-    T, heads = q.shape[0], q.shape[1]
-    _need(table.dim() == 2, "table must be [R, max_blocks]")
+    dim = c.head_dim
+    pq, qt, qh = _vectors(q, None, dim, "q")
+    T, heads, _ = q.shape
+    if table.dim() != 2:
+        raise ValueError("table must be [R, max_blocks]")
     R, width = table.shape
-    max_len = width * c.block_size if max_len is None else max_len
+    if max_len is None:
+        max_len = width * c.block_size
     if out is None:
         out = _empty(q.shape, q.dtype, q.device, stream)
-    _need(out.shape == q.shape and out.dtype == q.dtype, "out must be like q")
-    po, ot, oh = _vectors(out, heads, c.head_dim, "out")
-    _need(T <= 1 or ot >= c.head_dim, "out's tokens must not overlap")
-    _need(heads <= 1 or oh >= c.head_dim, "out's heads must not overlap")
-    need = ctypes.c_int64(0)
-    L = lib()
-    _check(L.st_kv_attend_workspace(ctypes.byref(c), T, heads, R, max_q, max_len, ctypes.byref(need)),
-           "st_kv_attend_workspace")
-    if need.value and workspace is None:
-        workspace = _empty((need.value,), torch.uint8, q.device, stream)
-    _check(L.st_kv_attend(ctypes.byref(c), pq, _DTYPES[q.dtype], T, heads, qt, qh,
-                          _array(table, torch.int32, (R, width), "table"), width,
-                          _array(row_start, torch.int32, (R + 1,), "row_start"), _array(lens, torch.int32, (R,), "lens"),
-                          R, max_q, max_len, c.head_dim ** -0.5 if scale is None else scale, int(causal), po, ot, oh,
-                          None if workspace is None else workspace.data_ptr(),
-                          0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)),
+        po, ot, oh = out.data_ptr(), heads * dim, dim
+    else:
+        _need(out.shape == q.shape and out.dtype == q.dtype, "out must be like q")
+        po, ot, oh = _vectors(out, heads, dim, "out")
+        # tokens apart from each other, and heads: one inside the other either way
+        _need((T <= 1 or ot >= dim) and (heads <= 1 or oh >= dim) and
+              (T <= 1 or heads <= 1 or ot >= (heads - 1) * oh + dim or oh >= (T - 1) * ot + dim), "out's vectors must not overlap")
+    need = _attend_workspace(c.num_blocks, c.kv_heads, c.block_size, dim, T, heads, R, max_q, max_len)
+    room = 0
+    if workspace is not None:
+        room = workspace.numel() * workspace.element_size()
+    elif need:
+        workspace, room = _empty((need,), torch.uint8, q.device, stream), need
+    _check(lib().st_kv_attend(ctypes.byref(c), pq, _DTYPES[q.dtype], T, heads, qt, qh,
+                              _array(table, torch.int32, (R, width), "table"), width,
+                              _array(row_start, torch.int32, (R + 1,), "row_start"),
+                              _array(lens, torch.int32, (R,), "lens"), R, max_q, max_len,
+                              dim ** -0.5 if scale is None else scale, int(causal), po, ot, oh,
+                              None if workspace is None else workspace.data_ptr(), room, _stream(stream)),
            "st_kv_attend")
     return out
 
@@ -179,46 +222,58 @@ def st_beam_select(logits: torch.Tensor, scores: torch.Tensor, keep: int, allow:
     token (expanded dimensions are read as they are); `finished` bool [B, K]
     marks beams that only repeat end_token. Returns (scores [B, keep], parents int32, tokens
     int32, finished bool or None); missing pairs are -inf, -1, -1."""
-    _need(logits.dim() == 3 and logits.dtype in _DTYPES, "logits must be [B, K, V] bfloat16, float16 or float32")
+    kind = _DTYPES.get(logits.dtype)
+    if kind is None or logits.dim() != 3:
+        raise ValueError("logits must be [B, K, V] bfloat16, float16 or float32")
     B, K, V = logits.shape
-    _need(V <= 1 or logits.stride(2) == 1, "logits must have a dense vocabulary")
-    stride = logits.stride(1) if K > 1 else logits.stride(0) if B > 1 else V
-    _need(B <= 1 or K <= 1 or logits.stride(0) == K * stride, "logits' beams must be evenly spaced")
+    request, beam, one = logits.stride()
+    if V > 1 and one != 1:
+        raise ValueError("logits must have a dense vocabulary")
+    stride = beam if K > 1 else request if B > 1 else V
+    if B > 1 and K > 1 and request != K * stride:
+        raise ValueError("logits' beams must be evenly spaced")
     dev = logits.device
+    ex = out_finished = None
+    if allow is not None or finished is not None:
+        ex = _BeamExtras()
+        if allow is not None:
+            _need(allow.dtype in (torch.int32, torch.uint32) and tuple(allow.shape) == (B, K, (V + 31) // 32),
+                  "allow must be int32 [B, K, ceil(V / 32)]")
+            _need(allow.shape[2] <= 1 or allow.stride(2) == 1, "allow must have dense words")
+            ex.allow, ex.allow_request_stride, ex.allow_beam_stride = allow.data_ptr(), allow.stride(0), allow.stride(1)
+        if finished is not None:
+            out_finished = _empty((B, keep), torch.bool, dev, stream)
+            ex.finished, ex.out_finished = _array(finished, torch.bool, (B, K), "finished"), out_finished.data_ptr()
+            ex.end_token = end_token
+    need = _select_workspace(B, K, V, keep)
     out_scores = _empty((B, keep), torch.float32, dev, stream)
     out_parents, out_tokens = _empty((B, keep), torch.int32, dev, stream), _empty((B, keep), torch.int32, dev, stream)
-    ex = _BeamExtras()
-    out_finished = None
-    if allow is not None:
-        _need(allow.dtype in (torch.int32, torch.uint32) and tuple(allow.shape) == (B, K, (V + 31) // 32),
-              "allow must be int32 [B, K, ceil(V / 32)]")
-        _need(allow.shape[2] <= 1 or allow.stride(2) == 1, "allow must have dense words")
-        ex.allow, ex.allow_request_stride, ex.allow_beam_stride = allow.data_ptr(), allow.stride(0), allow.stride(1)
-    if finished is not None:
-        out_finished = _empty((B, keep), torch.bool, dev, stream)
-        ex.finished, ex.out_finished = _array(finished, torch.bool, (B, K), "finished"), out_finished.data_ptr()
-        ex.end_token = end_token
-    L = lib()
-    need = ctypes.c_int64(0)
-    _check(L.st_beam_select_workspace(B, K, V, keep, ctypes.byref(need)), "st_beam_select_workspace")
-    if need.value and workspace is None:
-        workspace = _empty((need.value,), torch.uint8, dev, stream)
-    _check(L.st_beam_select(logits.data_ptr(), _DTYPES[logits.dtype], stride, _array(scores, torch.float32, (B, K), "scores"),
-                            B, K, V, keep, out_scores.data_ptr(), out_parents.data_ptr(), out_tokens.data_ptr(),
-                            ctypes.byref(ex), None if workspace is None else workspace.data_ptr(),
-                            0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)),
+    room = 0
+    if workspace is not None:
+        room = workspace.numel() * workspace.element_size()
+    elif need:
+        workspace, room = _empty((need,), torch.uint8, dev, stream), need
+    _check(lib().st_beam_select(logits.data_ptr(), kind, stride, _array(scores, torch.float32, (B, K), "scores"),
+                                B, K, V, keep, out_scores.data_ptr(), out_parents.data_ptr(), out_tokens.data_ptr(),
+                                None if ex is None else ctypes.byref(ex),
+                                None if workspace is None else workspace.data_ptr(), room, _stream(stream)),
            "st_beam_select")
     return out_scores, out_parents, out_tokens, out_finished
 
 
-def _dense_from(x: torch.Tensor, dim: int) -> bool:
-    """Are the dimensions from `dim` on one dense run of elements?"""
-    want = 1
-    for n, s in zip(reversed(x.shape[dim:]), reversed(x.stride()[dim:])):
-        if n != 1 and s != want:
-            return False
-        want *= n
-    return True
+def _rows(x: torch.Tensor, dim: int, what: str):
+    """The stride between the beams of a tensor whose requests and beams are
+    dimensions dim - 1 and dim, evenly spaced, with dense rows behind them."""
+    shape, stride = x.shape, x.stride()
+    if not x.is_contiguous():
+        want = 1
+        for n, s in zip(reversed(shape[dim + 1:]), reversed(stride[dim + 1:])):
+            if n != 1 and s != want:
+                raise ValueError(f"{what} must have dense rows")
+            want *= n
+        if shape[dim - 1] > 1 and shape[dim] > 1 and stride[dim - 1] != shape[dim] * stride[dim]:
+            raise ValueError(f"{what} must have evenly spaced beams")
+    return stride[dim] if shape[dim] > 1 else stride[dim - 1] if shape[dim - 1] > 1 else 0
 
 
 def st_beam_reorder(states: Sequence[torch.Tensor], parents: torch.Tensor, out: Optional[Sequence[torch.Tensor]] = None,
@@ -228,29 +283,24 @@ def st_beam_reorder(states: Sequence[torch.Tensor], parents: torch.Tensor, out: 
     The request and beam dimensions are beam_dim - 1 and beam_dim; beam_dim = 2
     takes tensors of several layers [layers, B, K, ...]. Up to 16 tensors go in
     one launch; `out` must not overlap them."""
-    _need(parents.dim() == 2 and beam_dim in (1, 2), "parents must be [B, keep] and beam_dim 1 or 2")
+    if parents.dim() != 2 or beam_dim not in (1, 2) or not len(states):
+        raise ValueError("parents must be [B, keep], beam_dim 1 or 2, and states not empty")
     B, keep = parents.shape
-    _need(len(states) > 0, "no states given")
     K = states[0].shape[beam_dim] if states[0].dim() > beam_dim else -1
     made = []
     table = (_BeamState * len(states))()
     for i, x in enumerate(states):
-        _need(x.dim() > beam_dim and x.shape[beam_dim - 1] == B and x.shape[beam_dim] == K,
-              f"state {i} must have {B} requests of {K} beams at dimension {beam_dim}")
-        shape = x.shape[:beam_dim] + (keep,) + x.shape[beam_dim + 1:]
-        y = _empty(shape, x.dtype, x.device, stream) if out is None else out[i]
-        _need(y.shape == shape and y.dtype == x.dtype, f"out {i} must be {tuple(shape)} {x.dtype}")
+        shape = x.shape
+        if len(shape) <= beam_dim or shape[beam_dim - 1] != B or shape[beam_dim] != K:
+            raise ValueError(f"state {i} must have {B} requests of {K} beams at dimension {beam_dim}")
+        new = shape[:beam_dim] + (keep,) + shape[beam_dim + 1:]
+        y = _empty(new, x.dtype, x.device, stream) if out is None else out[i]
+        if out is not None and (y.shape != new or y.dtype != x.dtype):
+            raise ValueError(f"out {i} must be {tuple(new)} {x.dtype}")
         size = x.element_size()
-        for z, name, n in ((x, "state", K), (y, "out", keep)):
-            _need(_dense_from(z, beam_dim + 1), f"{name} {i} must have dense rows")
-            _need(B <= 1 or n <= 1 or z.stride(beam_dim - 1) == n * z.stride(beam_dim), f"{name} {i}'s beams must be evenly spaced")
-        row = lambda z, n: size * (z.stride(beam_dim) if n > 1 else z.stride(beam_dim - 1) if B > 1 else 0)  # noqa: E731
-        e = table[i]
-        e.src, e.dst = x.data_ptr(), y.data_ptr()
-        e.row_bytes = size * math.prod(x.shape[beam_dim + 1:])
-        e.src_row_stride, e.dst_row_stride = row(x, K), row(y, keep)
-        e.outer = x.shape[0] if beam_dim == 2 else 1
-        e.src_outer_stride, e.dst_outer_stride = (size * x.stride(0), size * y.stride(0)) if beam_dim == 2 else (0, 0)
+        layers = (shape[0], size * x.stride(0), size * y.stride(0)) if beam_dim == 2 else (1, 0, 0)
+        table[i] = (x.data_ptr(), y.data_ptr(), size * math.prod(shape[beam_dim + 1:]), size * _rows(x, beam_dim, f"state {i}"),
+                    size * _rows(y, beam_dim, f"out {i}"), *layers)
         made.append(y)
     _check(lib().st_beam_reorder(table, len(states), _array(parents, torch.int32, (B, keep), "parents"), B, K, keep,
                                  _stream(stream)), "st_beam_reorder")

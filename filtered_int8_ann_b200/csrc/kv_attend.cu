@@ -9,13 +9,16 @@
 // One pass with a running maximum, in powers of two:
 //   s_j = scale log2(e) ks <q, k_j>, M = max s_j, p_j = 2^(s_j - M), l = sum p_j, O = sum p_j v_j.
 // Products run on mma.sync (m16n8k16, fp16 with fp32 sums): with at most 16 columns a tcgen05 tile
-// of 128 rows would be almost empty, and the codes would have to be converted
-// through shared memory; here they go from global memory to registers in the
-// order the fragments want, so nothing is staged:
+// of 128 rows would be almost empty, and the converted codes would have to go back through
+// shared memory; here they go from there to registers in the order the fragments want:
 //   S^T = K Q^T    A = 16 tokens x 16 dims: lane (g, t) loads 16 dims of tokens g and g + 8 as
 //                  one vector; which dims stand at which k index is free as long as Q agrees
 //   O^T = V^T P^T  A = 16 dims x 16 tokens: lane (g, t) loads D/8 dims of four tokens and pairs
 //                  the tokens' bytes with byte permutes; B = P^T is S^T's accumulator transposed by movmatrix
+// Each warp copies its next 32 tokens (cp.async, 16 bytes a lane) while it works on
+// the last: 12 warps per SM keep 96 KB of codes under way, where loads to registers kept too
+// few (64 rows of up to 16384 tokens: 404 us). The 16-byte pieces of a 128-byte line are permuted
+// by the token so that both kinds of loads are free of bank conflicts.
 // A code becomes fp16 exactly: with the sign bit flipped it is the low byte of 1024 + 128 + code.
 // A query is scaled by a power of two to below 2 (exact in fp16 down to 2^-24 of
 // its largest element). The weights' V factor is p_j vs_j / max vs, at most 1, so fp16's
@@ -27,15 +30,28 @@ namespace st {
 constexpr int kDecWarps = 4;
 constexpr int kDecBlock = 32 * kDecWarps;
 constexpr int kDecGroup = 32;             // tokens a warp takes at a time
-constexpr int kDecMaxBlocks = 1024 / 16;  // cache blocks of the longest stretch
+constexpr int kDecMaxStretch = 4096;      // tokens
+constexpr int kDecMaxBlocks = kDecMaxStretch / 16;
 
 template <int D, int NT>
 struct DecShared {
     int32_t page[kDecMaxBlocks];
     float ks[kDecMaxBlocks], vs[kDecMaxBlocks];
     float m[kDecWarps][8 * NT], l[kDecWarps][8 * NT];
-    float o[kDecWarps][8 * NT][D + 4];
+    union {
+        alignas(128) uint8_t codes[kDecWarps][2][2][kDecGroup * D];  // per warp: two stages of K and V codes
+        float o[kDecWarps][8 * NT][D + 4];              // at the end: the warps' sums
+    };
 };
+
+// Where 16-byte piece `c` of token r stands among its warp's codes: in line r
+// (two tokens per line for D = 64), pieces permuted.
+template <int D>
+__device__ __forceinline__ int piece_at(int r, int c)
+{
+    if (D == 128) return r * 128 + ((c ^ ((r & 1) << 2 | (r >> 1 & 3))) << 4);
+    return (r >> 1) * 128 + ((((r & 1) << 2 | c) ^ (r >> 1 & 3) << 1) << 4);
+}
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
@@ -52,7 +68,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
     return y;
 }
 
-// D bytes of a row's share of a lane: 16 dims (D = 128) or 8 (D = 64) of V
+// A lane's dims of a V row: 16 (D = 128) or 8 (D = 64)
 template <int D>
 struct VecV;
 template <>
@@ -60,8 +76,13 @@ struct VecV<128> { using type = uint4; };
 template <>
 struct VecV<64> { using type = uint2; };
 
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kDecBlock, NT == 1 ? 4 : 2)
+__global__ void __launch_bounds__(kDecBlock, 3)
 kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
 {
     constexpr int KV = D / 64;    // 16-byte vectors of a K row per lane
@@ -185,44 +206,46 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
         for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
     }
 
+    // Codes of 32 tokens from jj0 on into stage `st`: 16 tokens lie in one block and are one run of bytes.
     const int64_t head_bytes = int64_t(S) * D;
-    // the codes of the 16 tokens from jj on (a multiple of 16), which lie in one block
+    uint8_t* codes = sh.codes[warp][0][0];
+    const uint32_t codes_at = smem_u32(codes);
+    constexpr int kStage = 2 * kDecGroup * D, kHalf = 16 * D, kCopies = kHalf / 512;
+    constexpr int kLaneRows = 512 / D;  // tokens that a warp's copy covers
+    uint32_t dst[2];  // of copies with even and odd numbers
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        dst[i] = codes_at + piece_at<D>(i * kLaneRows + lane / (D / 16), lane % (D / 16)) - i * 512;
     auto block_of = [&](int jj) { return jj < tokens ? sh.page[jj >> shift] : -1; };
-    auto rows_at = [&](const int8_t* base, int page, int jj) {
-        return base + (int64_t(page) * a.c.kv_heads + hk) * head_bytes + int64_t(jj & (S - 1)) * D;
-    };
-    uint4 kreg[2][2][KV];
-    auto load_k = [&](int jj0) {
+    auto copy_stage = [&](int jj0, int st) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int jj = jj0 + 16 * h, page = block_of(jj);
             if (page >= 0) {
-                const int8_t* p = rows_at(a.c.k, page, jj) + g * D + 16 * t;
+                const int64_t at = (int64_t(page) * a.c.kv_heads + hk) * head_bytes + (jj & (S - 1)) * D + lane * 16;
+                const int8_t *k = a.c.k + at, *v = a.c.v + at;
+                const uint32_t to = uint32_t(st * kStage + h * kHalf);
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
-#pragma unroll
-                    for (int v = 0; v < KV; ++v)
-                        kreg[h][r][v] = ldg_stream(reinterpret_cast<const uint4*>(p + 8 * r * D + 64 * v));
+                for (int i = 0; i < kCopies; ++i) {
+                    copy_async(dst[i & 1] + to + i * 512, k + i * 512);
+                    copy_async(dst[i & 1] + to + kDecGroup * D + i * 512, v + i * 512);
+                }
             }
         }
+        cp_async_commit();
     };
-    load_k(warp * kDecGroup);
-    for (int jj0 = warp * kDecGroup; jj0 < tokens; jj0 += kDecWarps * kDecGroup) {
-        V vreg[2][4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int jj = jj0 + 16 * h, page = block_of(jj);
-            if (page >= 0) {
-                const int8_t* p = rows_at(a.c.v, page, jj) + 2 * t * D + g * (D / 8);
-                vreg[h][0] = ldg_stream(reinterpret_cast<const V*>(p));
-                vreg[h][1] = ldg_stream(reinterpret_cast<const V*>(p + D));
-                vreg[h][2] = ldg_stream(reinterpret_cast<const V*>(p + 8 * D));
-                vreg[h][3] = ldg_stream(reinterpret_cast<const V*>(p + 9 * D));
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) vreg[h][i] = V{};
-            }
-        }
+    // lane (g, t)'s pieces: K pieces t (and t + 4) of tokens g, g + 8; V dims of tokens 2t, 2t+1 (and + 8)
+    const int vdim = D == 128 ? (g >> 1 | (g & 1) << 2) * 16 : g * 8;  // first of the lane's D/8 dims of V
+    const int k_at[2] = {piece_at<D>(g, t), D == 128 ? piece_at<D>(g, t + 4) : 0};
+    const int v_at[2] = {kDecGroup * D + piece_at<D>(2 * t, vdim / 16) + vdim % 16,
+                         kDecGroup * D + piece_at<D>(2 * t + 1, vdim / 16) + vdim % 16};
+    int stage = 0;
+    copy_stage(warp * kDecGroup, 0);
+    for (int jj0 = warp * kDecGroup; jj0 < tokens; jj0 += kDecWarps * kDecGroup, stage ^= 1) {
+        copy_stage(jj0 + kDecWarps * kDecGroup, stage ^ 1);
+        cp_async_wait_group<1>();
+        __syncwarp();
+        const uint8_t* from = codes + stage * kStage;
         float s[2][NT][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -230,8 +253,9 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
             for (int nt = 0; nt < NT; ++nt) s[h][nt][0] = s[h][nt][1] = s[h][nt][2] = s[h][nt][3] = 0.f;
 #pragma unroll
             for (int v = 0; v < KV; ++v) {
-                const uint32_t w0[4] = {kreg[h][0][v].x, kreg[h][0][v].y, kreg[h][0][v].z, kreg[h][0][v].w};
-                const uint32_t w1[4] = {kreg[h][1][v].x, kreg[h][1][v].y, kreg[h][1][v].z, kreg[h][1][v].w};
+                const uint4 x0 = *reinterpret_cast<const uint4*>(from + h * kHalf + k_at[v]);
+                const uint4 x1 = *reinterpret_cast<const uint4*>(from + h * kHalf + 8 * D + k_at[v]);
+                const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     uint32_t f[4];
@@ -242,7 +266,6 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
                 }
             }
         }
-        load_k(jj0 + kDecWarps * kDecGroup);
         // scores, masked; the columns' maxima
         float f[2];  // V factor of each half
         float mx[NT][2];
@@ -316,8 +339,11 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint32_t* w[4] = {reinterpret_cast<const uint32_t*>(&vreg[h][0]), reinterpret_cast<const uint32_t*>(&vreg[h][1]),
-                                    reinterpret_cast<const uint32_t*>(&vreg[h][2]), reinterpret_cast<const uint32_t*>(&vreg[h][3])};
+            V vreg[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vreg[i] = *reinterpret_cast<const V*>(from + h * kHalf + (i >> 1) * 8 * D + v_at[i & 1]);
+            const uint32_t* w[4] = {reinterpret_cast<const uint32_t*>(&vreg[0]), reinterpret_cast<const uint32_t*>(&vreg[1]),
+                                    reinterpret_cast<const uint32_t*>(&vreg[2]), reinterpret_cast<const uint32_t*>(&vreg[3])};
 #pragma unroll
             for (int i = 0; i < VW; ++i) {  // four dims of the four tokens
                 const uint32_t x0 = w[0][i] ^ 0x80808080u, x1 = w[1][i] ^ 0x80808080u, x2 = w[2][i] ^ 0x80808080u,
@@ -336,9 +362,12 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
                 }
             }
         }
+        __syncwarp();  // the stage is copied into again
     }
 
     // join the warps
+    cp_async_wait_group<0>();
+    __syncthreads();  // the codes' memory is used again
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -351,9 +380,9 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
                 sh.l[warp][c] = l[nt][i];
             }
 #pragma unroll
-            for (int k = 0; k < MT; ++k) {  // dims g D/8 + 2 k and the next
-                sh.o[warp][c][g * (D / 8) + 2 * k] = o[nt][k][i];
-                sh.o[warp][c][g * (D / 8) + 2 * k + 1] = o[nt][k][2 + i];
+            for (int k = 0; k < MT; ++k) {  // dims vdim + 2 k and the next
+                sh.o[warp][c][vdim + 2 * k] = o[nt][k][i];
+                sh.o[warp][c][vdim + 2 * k + 1] = o[nt][k][2 + i];
             }
         }
     __syncthreads();
@@ -388,11 +417,16 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
     }
 }
 
-// Join a query head's stretches.
+// Join a query head's stretches: a few groups of D threads take every so many of them each.
+constexpr int kJoinBlock = 512;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(D) kv_join_kernel(AttendArgs a, int splits, int stretch)
+__global__ void __launch_bounds__(kJoinBlock) kv_join_kernel(AttendArgs a, int splits, int stretch)
 {
+    constexpr int GROUPS = kJoinBlock / D, kChunk = 512;
+    __shared__ float s_w[kChunk], s_red[kJoinBlock / 32], s_o[GROUPS][D];
     dep_enter();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, d = tid % D, group = tid / D;
     const int64_t unit = blockIdx.x;
     const int64_t token = unit / a.q_heads, head = unit - token * a.q_heads;
     int lo = 0, hi = a.R;  // the row holding the token
@@ -409,39 +443,74 @@ __global__ void __launch_bounds__(D) kv_join_kernel(AttendArgs a, int splits, in
     const int used = int(max(int64_t(1), (len + stretch - 1) / stretch));
     const float* po = static_cast<const float*>(a.workspace);
     const float* pm = po + a.T * a.q_heads * splits * D + 2 * unit * splits;
-    po += unit * splits * D + threadIdx.x;
+    po += unit * splits * D + d;
     float top = -INFINITY;
-    for (int i = 0; i < used; ++i) top = fmaxf(top, pm[2 * i]);
+    for (int i = tid; i < used; i += kJoinBlock) top = fmaxf(top, pm[2 * i]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    if (lane == 0) s_red[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinBlock / 32; ++w) top = fmaxf(top, s_red[w]);
     const float base = top > -INFINITY ? top : 0.f;
     float sum = 0.f, val = 0.f;
-    for (int i = 0; i < used; ++i) {
-        const float m = pm[2 * i];
-        const float z = m > -INFINITY ? ex2(m - base) : 0.f;
-        sum += pm[2 * i + 1] * z;
-        val += po[int64_t(i) * D] * z;
+    for (int c0 = 0; c0 < used; c0 += kChunk) {
+        const int c = min(kChunk, used - c0);
+        __syncthreads();
+        if (tid < c) {
+            const float m = pm[2 * (c0 + tid)];
+            s_w[tid] = m > -INFINITY ? ex2(m - base) : 0.f;
+            sum += pm[2 * (c0 + tid) + 1] * s_w[tid];
+        }
+        __syncthreads();
+#pragma unroll 8
+        for (int i = group; i < c; i += GROUPS) val += po[int64_t(c0 + i) * D] * s_w[i];
     }
-    static_cast<T*>(a.out)[token * a.out_token + head * a.out_head + threadIdx.x] = from_float<T>(sum == 0.f ? 0.f : val / sum);
+    // sums over the threads and groups
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    __syncthreads();
+    if (lane == 0) s_red[warp] = sum;
+    s_o[group][d] = val;
+    __syncthreads();
+    if (group == 0) {
+        sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kJoinBlock / 32; ++w) sum += s_red[w];
+        val = 0.f;
+#pragma unroll
+        for (int k = 0; k < GROUPS; ++k) val += s_o[k][d];
+        static_cast<T*>(a.out)[token * a.out_token + head * a.out_head + d] = from_float<T>(sum == 0.f ? 0.f : val / sum);
+    }
 }
 
 struct DecPlan {
     int splits, stretch, cols, col_blocks;
 };
 
-// Stretches: enough CTAs for the GPU's places (4 per SM), each of 256 to 1024 tokens, in multiples of the
-// longest block; a short row is one stretch, which needs no join.
+// Stretches, multiples of the longest block. One row fills the GPU's places (3 CTAs per SM) once, all with
+// the same work. Several rows, which may be uneven, get about three CTAs per place, of 256 to 1024 tokens.
+// A short row is one stretch, which needs no join.
 static DecPlan dec_plan(const st_kv_cache& c, int32_t q_heads, int32_t R, int32_t max_q, int64_t max_len)
 {
     DecPlan p;
     const int64_t cols = int64_t(max_q) * (q_heads / c.kv_heads);
     p.cols = cols <= 8 ? 8 : 16;
     p.col_blocks = int((cols + p.cols - 1) / p.cols);
-    const int64_t places = 4 * 148;
+    const int64_t places = 3 * 148;
     const int64_t units = int64_t(R) * c.kv_heads * p.col_blocks;
-    int64_t stretch = (max_len * units + places - 1) / places;
-    stretch = stretch < 256 ? 256 : stretch > 1024 ? 1024 : stretch;
+    int64_t stretch;
+    if (R == 1) {
+        const int64_t each = places / units > 1 ? places / units : 1;
+        stretch = (max_len + each - 1) / each;
+        stretch = stretch < 256 ? 256 : stretch > kDecMaxStretch ? 1024 : stretch;
+    } else {
+        stretch = (max_len * units + 3 * places - 1) / (3 * places);
+        stretch = stretch < 256 ? 256 : stretch > 1024 ? 1024 : stretch;
+    }
     stretch = (stretch + 127) / 128 * 128;
+    if (max_len <= 512) stretch = 512;
     p.splits = int((max_len + stretch - 1) / stretch);
-    if (max_len <= 512) p.splits = 1, stretch = 512;
     p.stretch = int(stretch);
     return p;
 }
@@ -464,7 +533,7 @@ static cudaError_t launch_decode(const AttendArgs& a, const DecPlan& p, cudaStre
     kv_decode_kernel<T, D, NT><<<grid, kDecBlock, bytes, s>>>(a, p.splits, p.stretch, p.col_blocks);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.splits == 1) return e;
-    return launch_dep(kv_join_kernel<T, D>, dim3(unsigned(a.T * a.q_heads)), dim3(D), 0, s, a, p.splits, p.stretch);
+    return launch_dep(kv_join_kernel<T, D>, dim3(unsigned(a.T * a.q_heads)), dim3(kJoinBlock), 0, s, a, p.splits, p.stretch);
 }
 
 cudaError_t launch_kv_decode(const AttendArgs& a, cudaStream_t s)

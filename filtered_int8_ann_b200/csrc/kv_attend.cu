@@ -29,6 +29,7 @@ namespace st {
 
 constexpr int kDecWarps = 4;
 constexpr int kDecBlock = 32 * kDecWarps;
+constexpr int kDecMaxCols = 32;            // columns (query tokens x heads per cache head) up to which this kernel is taken
 constexpr int kDecGroup = 32;             // tokens a warp takes at a time
 constexpr int kDecMaxStretch = 4096;      // tokens
 constexpr int kDecMaxBlocks = kDecMaxStretch / 16;
@@ -515,7 +516,7 @@ static DecPlan dec_plan(const st_kv_cache& c, int32_t q_heads, int32_t R, int32_
     return p;
 }
 
-int64_t kv_decode_workspace(const st_kv_cache& c, int64_t T, int32_t q_heads, int32_t R, int32_t max_q, int64_t max_len)
+static int64_t kv_decode_workspace(const st_kv_cache& c, int64_t T, int32_t q_heads, int32_t R, int32_t max_q, int64_t max_len)
 {
     const DecPlan p = dec_plan(c, q_heads, R, max_q, max_len);
     return p.splits == 1 ? 0 : T * q_heads * p.splits * (int64_t(c.head_dim) + 2) * 4;
@@ -533,10 +534,23 @@ static cudaError_t launch_decode(const AttendArgs& a, const DecPlan& p, cudaStre
     kv_decode_kernel<T, D, NT><<<grid, kDecBlock, bytes, s>>>(a, p.splits, p.stretch, p.col_blocks);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.splits == 1) return e;
-    return launch_dep(kv_join_kernel<T, D>, dim3(unsigned(a.T * a.q_heads)), dim3(kJoinBlock), 0, s, a, p.splits, p.stretch);
+    return launch_kv_join(a, p.splits, p.stretch, s);
 }
 
-cudaError_t launch_kv_decode(const AttendArgs& a, cudaStream_t s)
+cudaError_t launch_kv_join(const AttendArgs& a, int splits, int stretch, cudaStream_t s)
+{
+    const int64_t units = a.T * a.q_heads;
+    if (units > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    const dim3 grid{unsigned(units)}, block{kJoinBlock};
+    const bool bf = a.dtype == ST_BF16;
+    if (a.c.head_dim == 128)
+        return bf ? launch_dep(kv_join_kernel<__nv_bfloat16, 128>, grid, block, 0, s, a, splits, stretch)
+                  : launch_dep(kv_join_kernel<__half, 128>, grid, block, 0, s, a, splits, stretch);
+    return bf ? launch_dep(kv_join_kernel<__nv_bfloat16, 64>, grid, block, 0, s, a, splits, stretch)
+              : launch_dep(kv_join_kernel<__half, 64>, grid, block, 0, s, a, splits, stretch);
+}
+
+static cudaError_t launch_kv_decode(const AttendArgs& a, cudaStream_t s)
 {
     const DecPlan p = dec_plan(a.c, a.q_heads, a.R, a.max_q, a.max_len);
     const bool bf = a.dtype == ST_BF16, wide = a.c.head_dim == 128, two = p.cols > 8;
@@ -546,11 +560,21 @@ cudaError_t launch_kv_decode(const AttendArgs& a, cudaStream_t s)
     return bf ? launch_decode<__nv_bfloat16, 64, 1>(a, p, s) : launch_decode<__half, 64, 1>(a, p, s);
 }
 
-int64_t kv_attend_workspace(const st_kv_cache& c, int64_t T, int32_t q_heads, int32_t R, int32_t max_q, int64_t max_len)
+// Up to this many columns go to the decode kernel.
+static bool few_columns(const st_kv_cache& c, int32_t q_heads, int32_t max_q)
 {
-    return kv_decode_workspace(c, T, q_heads, R, max_q, max_len);
+    return int64_t(max_q) * (q_heads / c.kv_heads) <= kDecMaxCols;
 }
 
-cudaError_t launch_kv_attend(const AttendArgs& a, cudaStream_t s) { return launch_kv_decode(a, s); }
+int64_t kv_attend_workspace(const st_kv_cache& c, int64_t T, int32_t q_heads, int32_t R, int32_t max_q, int64_t max_len)
+{
+    return few_columns(c, q_heads, max_q) ? kv_decode_workspace(c, T, q_heads, R, max_q, max_len)
+                                          : kv_prefill_workspace(c, T, q_heads, R, max_q, max_len);
+}
+
+cudaError_t launch_kv_attend(const AttendArgs& a, cudaStream_t s)
+{
+    return few_columns(a.c, a.q_heads, a.max_q) ? launch_kv_decode(a, s) : launch_kv_prefill(a, s);
+}
 
 }  // namespace st

@@ -8,9 +8,10 @@
 //   * warps 0-3 and 4-7: the softmax of tile 0 and 1, a column per thread, so
 //     that maxima and sums need no exchange. Scores come from TMEM; weights go
 //     back over them as fp16, the A operand of the second product;
-//   * warps 8-15: bring the next tokens' codes into registers, and convert them to fp16 operands in
-//     shared memory (128-byte swizzle): K as [token][dim], V transposed as
-//     [dim][token] by byte permutes, so both products read K-major operands;
+//   * warps 8-11 (K) and 12-15 (V): bring the next tokens' codes into registers,
+//     and convert them to fp16 operands in shared memory (128-byte swizzle): K as
+//     [token][dim], V transposed as [dim][token] by byte permutes, so both
+//     products read K-major operands;
 //   * warp 16: issues tcgen05.mma (M = 128, N = 128 tokens or D dims, K = 16, fp32 sums in TMEM). While
 //     one tile's products run, the other tile's softmax does: S and its weights
 //     share TMEM columns, 2 x 128 for them and 2 x 128 for O fill all 512.
@@ -29,21 +30,27 @@ namespace st {
 
 constexpr int kPreTile = 128;                  // tokens per step
 constexpr int kPreCols = 256;                  // columns per CTA: two tiles
-constexpr int kPreProducers = 256;
-constexpr int kPreBlock = 512 + 32;
+constexpr int kPreLoaders = 128;               // threads that bring K, and as many for V
+constexpr int kPreMmaWarp = 16;
+constexpr int kPreBlock = 32 * (kPreMmaWarp + 4);  // whole warpgroups; the last three warps idle
+// Registers per thread after the split of the launch's 96: 2 x 128 + 2 x 72 + 80 = 5 x 96.
+constexpr int kPreSoftmaxRegs = 128, kPreLoaderRegs = 72, kPreMmaRegs = 80;
 constexpr int kPreMaxStretch = 16384;          // tokens: the table of a stretch is held in shared memory
 constexpr int kPreMaxBlocks = kPreMaxStretch / 16;
-constexpr int kPreStages = 2;
+constexpr int kPreStages = 2;  // of K and V operands
 constexpr uint32_t kPreWaitLimit = 1u << 22;
-constexpr float kPreRaise = 8.f;
+constexpr float kPreRaise = 8.f;  // a score this far above the reference raises it
 
 template <int D>
 struct PreShared {
     alignas(1024) uint8_t q[2][D / 64][kPreTile * 128];           // two tiles, halves of 64 dims, 128 rows of 128 bytes
     alignas(1024) uint8_t k[kPreStages][D / 64][kPreTile * 128];  // 128 tokens
     alignas(1024) uint8_t v[kPreStages][2][D * 128];              // halves of 64 tokens, D rows of 128 bytes
-    int32_t page[kPreMaxBlocks];
-    float ks[kPreMaxBlocks], vs[kPreMaxBlocks];                   // ks < 0: the block is hidden
+    // of each 16 tokens of the stretch: where their codes begin (-1: hidden), their block's scales (K: negative
+    // when hidden; V: over the largest of the stretch)
+    int64_t at[kPreMaxBlocks];
+    alignas(16) float ks[kPreMaxBlocks];
+    alignas(16) float vs[kPreMaxBlocks];
     float vtop[kPreBlock / 32];
     alignas(8) uint64_t k_full[kPreStages], k_empty[kPreStages], v_full[kPreStages], v_empty[kPreStages];
     uint64_t s_full[2], p_ready[2], pv_done[2];
@@ -139,6 +146,181 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
     return d;
 }
 
+// Eight columns, as tmem_ld32 and tmem_st32.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&x)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&x)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};"
+                 ::"r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]), "r"(taddr)
+                 : "memory");
+}
+
+// Wait for this warp's TMEM loads; the registers they fill depend on it.
+__device__ __forceinline__ void tmem_wait16(float2 (&s)[8])
+{
+    uint32_t* x = reinterpret_cast<uint32_t*>(s);
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]), "+r"(x[4]), "+r"(x[5]), "+r"(x[6]), "+r"(x[7]),
+                   "+r"(x[8]), "+r"(x[9]), "+r"(x[10]), "+r"(x[11]), "+r"(x[12]), "+r"(x[13]), "+r"(x[14]), "+r"(x[15])
+                 :: "memory");
+}
+__device__ __forceinline__ void tmem_load16(uint32_t taddr, float2 (&s)[8])
+{
+    tmem_ld16(taddr, reinterpret_cast<uint32_t(&)[16]>(s));
+}
+
+// The largest score among the 128 tokens of a step, over the factor sc of their sixteens.
+__device__ __forceinline__ float step_max(uint32_t ts, const float (&sc)[8])
+{
+    float top = -INFINITY;
+    float2 s[2][8];
+    tmem_load16(ts, s[0]);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        float2(&x)[8] = s[c & 1];
+        tmem_wait16(x);
+        if (c < 7) tmem_load16(ts + 16 * (c + 1), s[(c + 1) & 1]);
+        float a = fmaxf(x[0].x, x[0].y), b = fmaxf(x[1].x, x[1].y);
+#pragma unroll
+        for (int i = 2; i < 8; i += 2) {
+            a = fmaxf(fmaxf(a, x[i].x), x[i].y);
+            b = fmaxf(fmaxf(b, x[i + 1].x), x[i + 1].y);
+        }
+        top = fmaxf(top, fmaxf(a, b) * sc[c]);
+    }
+    return top;
+}
+
+// The step's weights 2^(score - base), times their sixteens' V factors, as fp16 over the scores; returns their sum
+// before those factors. Straight-line code: the exponentials bound it.
+__device__ __forceinline__ float step_weights(uint32_t ts, const float (&sc)[8], const float (&vf)[8], float base)
+{
+    float2 total[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    const float2 down = make_float2(-base, -base);
+    float2 s[2][8];
+    tmem_load16(ts, s[0]);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        float2(&x)[8] = s[c & 1];
+        tmem_wait16(x);
+        if (c < 7) tmem_load16(ts + 16 * (c + 1), s[(c + 1) & 1]);
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float2 y = fma2(x[i], make_float2(sc[c], sc[c]), down);
+            y.x = ex2(y.x);
+            y.y = ex2(y.y);
+            total[i & 1] = add2(total[i & 1], y);
+            y = mul2(y, make_float2(vf[c], vf[c]));
+            w[i] = pack_half2(y.x, y.y);
+        }
+        tmem_st8(ts + 8 * c, w);  // over scores that have been read
+    }
+    total[0] = add2(total[0], total[1]);
+    return total[0].x + total[0].y;
+}
+
+// Both for a step of which the column sees `see` tokens, without the hidden blocks' (negative factors).
+__device__ __noinline__ float step_max_masked(uint32_t ts, const float* ks, float mult, int see)
+{
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) {
+        float2 s[8];
+        tmem_load16(ts + 16 * c, s);
+        tmem_wait16(s);
+        const int here = ks[c] >= 0.f ? see - 16 * c : 0;
+        const float sc = ks[c] * mult;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (2 * i < here) top = fmaxf(top, s[i].x * sc);
+            if (2 * i + 1 < here) top = fmaxf(top, s[i].y * sc);
+        }
+    }
+    return top;
+}
+__device__ __noinline__ float step_weights_masked(uint32_t ts, const float* ks, const float* vs, float mult, float base, int see)
+{
+    float sum = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) {
+        float2 s[8];
+        tmem_load16(ts + 16 * c, s);
+        tmem_wait16(s);
+        const int here = ks[c] >= 0.f ? see - 16 * c : 0;
+        const float sc = ks[c] * mult, vf = vs[c];
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float x = 2 * i < here ? ex2(fmaf(s[i].x, sc, -base)) : 0.f;
+            const float y = 2 * i + 1 < here ? ex2(fmaf(s[i].y, sc, -base)) : 0.f;
+            sum += x + y;
+            w[i] = pack_half2(x * vf, y * vf);
+        }
+        tmem_st8(ts + 8 * c, w);
+    }
+    return sum;
+}
+
+// Raise the column's reference m by `up` (>= 0): what has been summed with it, l and O, shrinks.
+template <int D>
+__device__ __noinline__ void raise(uint32_t to, float up, bool has_o, float& m, float& l)
+{
+    const float z = ex2(-up);
+    m += up;
+    l *= z;
+    if (has_o) {
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld16(to + 16 * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * z);
+            tmem_st16(to + 16 * c, o);
+        }
+        tmem_wait_st();
+    }
+}
+
+// mbar_wait that also ends, without success, when another role has set the abort flag.
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, const volatile int32_t* abort)
+{
+    for (uint32_t i = 0; i < kPreWaitLimit / 256; ++i) {
+        if (mbar_wait(bar, parity, 256)) return true;
+        if (*abort) return false;
+    }
+    return false;
+}
+
+// True in one lane of the (whole) warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t lead;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(lead));
+    return lead != 0;
+}
+
+template <int REGS>
+__device__ __forceinline__ void regs_up()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void regs_down()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kPreBlock, 1)
 kv_prefill_kernel(AttendArgs a, int splits, int stretch, int pairs)
@@ -173,13 +355,13 @@ kv_prefill_kernel(AttendArgs a, int splits, int stretch, int pairs)
     const int steps = (tokens + kPreTile - 1) / kPreTile;
     const int tiles = cols > kPreTile ? 2 : 1;
 
-    if (warp == 16) {
+    if (warp == kPreMmaWarp) {
         tmem_alloc(&sh.tmem, 512);
         tmem_relinquish();
         if (lane == 0) {
             for (int i = 0; i < kPreStages; ++i) {
-                mbar_init(&sh.k_full[i], kPreProducers / 32);
-                mbar_init(&sh.v_full[i], kPreProducers / 32);
+                mbar_init(&sh.k_full[i], kPreLoaders / 32);
+                mbar_init(&sh.v_full[i], kPreLoaders / 32);
                 mbar_init(&sh.k_empty[i], 1);
                 mbar_init(&sh.v_empty[i], 1);
             }
@@ -193,33 +375,29 @@ kv_prefill_kernel(AttendArgs a, int splits, int stretch, int pairs)
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
     }
-    // the stretch's blocks
+    // the stretch's tokens, in sixteens up to the end of the last step
+    float vlocal = 0.f;
     {
-        const int pages = (tokens + S - 1) >> shift;
         const int32_t* table = a.table + int64_t(row) * a.max_blocks + (j0 >> shift);
-        float vtop = 0.f;
-        for (int i = tid; i < pages; i += kPreBlock) {
-            int p = table[i];
-            if (p < 0 || p >= a.c.num_blocks) {
-                atomicOr(a.err, kDecErrTable);
-                p = -1;
+        for (int i = tid; i < steps * (kPreTile / 16); i += kPreBlock) {
+            int p = -1;
+            if (16 * i < tokens) {
+                p = table[(16 * i) >> shift];
+                if (p < 0 || p >= a.c.num_blocks) {
+                    atomicOr(a.err, kDecErrTable);
+                    p = -1;
+                }
             }
-            const int64_t at = int64_t(p) * a.c.kv_heads + hk;
-            sh.page[i] = p;
-            sh.ks[i] = p < 0 ? -1.f : a.c.k_scale[at];
-            const float vs = p < 0 ? 0.f : a.c.v_scale[at];
+            const int64_t block = int64_t(p) * a.c.kv_heads + hk;
+            sh.at[i] = p < 0 ? -1 : (block * S + ((16 * i) & (S - 1))) * D;
+            sh.ks[i] = p < 0 ? -1.f : a.c.k_scale[block];
+            const float vs = p < 0 ? 0.f : a.c.v_scale[block];
             sh.vs[i] = vs;
-            vtop = fmaxf(vtop, vs);
-        }
-        // up to the end of the last step
-        for (int i = pages + tid; i < (steps * kPreTile) >> shift; i += kPreBlock) {
-            sh.page[i] = -1;
-            sh.ks[i] = -1.f;
-            sh.vs[i] = 0.f;
+            vlocal = fmaxf(vlocal, vs);
         }
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, off));
-        if (lane == 0) sh.vtop[warp] = vtop;
+        for (int off = 16; off > 0; off >>= 1) vlocal = fmaxf(vlocal, __shfl_xor_sync(0xffffffffu, vlocal, off));
+        if (lane == 0) sh.vtop[warp] = vlocal;
     }
     // the queries, a column per softmax thread
     const int tile = warp >> 2, r = tid & 127;  // warps 0-7
@@ -275,7 +453,11 @@ kv_prefill_kernel(AttendArgs a, int splits, int stretch, int pairs)
     float vtop = 0.f;
 #pragma unroll
     for (int w = 0; w < kPreBlock / 32; ++w) vtop = fmaxf(vtop, sh.vtop[w]);
-    const float vinv = vtop > 0.f ? 1.f / vtop : 0.f;
+    {
+        const float vinv = vtop > 0.f ? 1.f / vtop : 0.f;
+        for (int i = tid; i < steps * (kPreTile / 16); i += kPreBlock) sh.vs[i] *= vinv;
+    }
+    __syncthreads();
     volatile int32_t* abort = &sh.abort;
     auto give_up = [&]() {
         *abort = 1;
@@ -283,113 +465,101 @@ kv_prefill_kernel(AttendArgs a, int splits, int stretch, int pairs)
     };
 
     float m = -INFINITY, l = 0.f;  // softmax threads
-    if (warp == 16) {
+    if (warp >= kPreMmaWarp) {
         // ------------------------------------------------------------ products --
-        if (lane == 0 && steps > 0) {
+        regs_down<kPreMmaRegs>();
+        if (warp == kPreMmaWarp && steps > 0) {
+            // The whole warp walks the steps, so that addresses stay in uniform registers; one lane issues.
             constexpr uint32_t idS = idesc_f16(128, kPreTile), idO = idesc_f16(128, D);
-            bool ok = true;
+            constexpr uint64_t kQHalf = sizeof(sh.q[0][0]) >> 4, kVHalf = sizeof(sh.v[0][0]) >> 4;
+            const uint64_t dq = smem_desc_kmajor(smem_u32(sh.q), 128), dk = smem_desc_kmajor(smem_u32(sh.k), 128),
+                           dv = smem_desc_kmajor(smem_u32(sh.v), 128);
+            const bool lead = elect_one();
             auto scores = [&](int x, int j) {  // S of tile x, step j
-                const int st = j % kPreStages;
+                if (lead) {
+                    const uint64_t q = dq + x * (sizeof(sh.q[0]) >> 4), k = dk + (j & 1) * (sizeof(sh.k[0]) >> 4);
 #pragma unroll
-                for (int s = 0; s < D / 16; ++s)
-                    tc_mma_f16(tmem + x * 128, smem_desc_kmajor(smem_u32(sh.q[x][s / 4]) + (s & 3) * 32, 128),
-                               smem_desc_kmajor(smem_u32(sh.k[st][s / 4]) + (s & 3) * 32, 128), idS, s > 0);
-                tc_commit(&sh.s_full[x]);
+                    for (int s = 0; s < D / 16; ++s)
+                        tc_mma_f16(tmem + x * 128, q + s / 4 * kQHalf + (s & 3) * 2, k + s / 4 * kQHalf + (s & 3) * 2, idS, s > 0);
+                    tc_commit(&sh.s_full[x]);
+                }
             };
             auto values = [&](int x, int j) {  // O += P V
-                const int st = j % kPreStages;
+                if (lead) {
+                    const uint64_t v = dv + (j & 1) * (sizeof(sh.v[0]) >> 4);
 #pragma unroll
-                for (int s = 0; s < kPreTile / 16; ++s)
-                    tc_mma_f16_ts(tmem + 256 + x * 128, tmem + x * 128 + s * 8,
-                                  smem_desc_kmajor(smem_u32(sh.v[st][s / 4]) + (s & 3) * 32, 128), idO, j > 0 || s > 0);
-                tc_commit(&sh.pv_done[x]);
+                    for (int s = 0; s < kPreTile / 16; ++s)
+                        tc_mma_f16_ts(tmem + 256 + x * 128, tmem + x * 128 + s * 8, v + s / 4 * kVHalf + (s & 3) * 2, idO, j > 0 || s > 0);
+                    tc_commit(&sh.pv_done[x]);
+                }
             };
-            ok = mbar_wait(&sh.k_full[0], 0, kPreWaitLimit);
+            auto done = [&](uint64_t* bar) {
+                if (lead) tc_commit(bar);
+            };
+            bool ok = wait_or_abort(&sh.k_full[0], 0, abort);
             if (ok) {
                 tc_fence_after();
+#pragma unroll 1
                 for (int x = 0; x < tiles; ++x) scores(x, 0);
-                tc_commit(&sh.k_empty[0]);
+                done(&sh.k_empty[0]);
             }
+#pragma unroll 1
             for (int j = 0; j < steps && ok; ++j) {
-                const int st = j % kPreStages, nx = (j + 1) % kPreStages;
-                ok = mbar_wait(&sh.v_full[st], j / kPreStages & 1, kPreWaitLimit);
-                if (ok && j + 1 < steps) ok = mbar_wait(&sh.k_full[nx], (j + 1) / kPreStages & 1, kPreWaitLimit);
+                const int st = j & 1, nx = st ^ 1;
+                ok = wait_or_abort(&sh.v_full[st], j >> 1 & 1, abort);
+                if (ok && j + 1 < steps) ok = wait_or_abort(&sh.k_full[nx], (j + 1) >> 1 & 1, abort);
+#pragma unroll 1
                 for (int x = 0; x < tiles && ok; ++x) {
-                    ok = !*abort && mbar_wait(&sh.p_ready[x], j & 1, kPreWaitLimit);
+                    ok = wait_or_abort(&sh.p_ready[x], j & 1, abort);
                     if (!ok) break;
                     tc_fence_after();
                     values(x, j);
                     if (j + 1 < steps) scores(x, j + 1);
                 }
                 if (ok) {
-                    tc_commit(&sh.v_empty[st]);
-                    if (j + 1 < steps) tc_commit(&sh.k_empty[nx]);
+                    done(&sh.v_empty[st]);
+                    if (j + 1 < steps) done(&sh.k_empty[nx]);
                 }
             }
-            if (!ok) give_up();
-            tc_commit(&sh.drain);  // all products issued are done before the TMEM is freed
+            if (!__all_sync(0xffffffffu, ok)) give_up();
+            __syncwarp();
+            done(&sh.drain);  // all products issued are done before the TMEM is freed
             if (!mbar_wait(&sh.drain, 0, kPreWaitLimit)) give_up();
         }
-    } else if (warp >= 8) {
-        // ------------------------------------------------------------ operands --
-        const int p = tid - 256, pw = p >> 5;
-        constexpr int KN = kPreTile * (D / 16) / kPreProducers;  // 16-byte pieces of K per thread
-        constexpr int VN = (D / 32) * 4 / (kPreProducers / 32);  // V tasks (32 dims x 32 tokens) per warp
-        constexpr int ROWP = D / 16;
-        const int64_t head_bytes = int64_t(S) * D;
-        uint4 kr[KN];
+    } else if (warp >= 12) {
+        // ------------------------------------------------------------------ V --
+        regs_down<kPreLoaderRegs>();
+        constexpr int VN = D / 32;  // turns of 32 dims each, for the warp's 32 tokens
         uint32_t vr[VN][8];
-        auto rows_at = [&](const int8_t* base, int jj) -> const int8_t* {
-            const int page = sh.page[jj >> shift];
-            return page < 0 ? nullptr : base + (int64_t(page) * a.c.kv_heads + hk) * head_bytes + (jj & (S - 1)) * D;
-        };
-        // V task: lane bits 0, 3, 4: a word of the 32 dims; bits 1, 2: a group of 8 tokens
-        const int vword = (lane & 1) | (lane >> 3 & 3) << 1, vgroup = lane >> 1 & 3;
+        // lane bits 0, 3, 4: a word of the turn's 32 dims; bits 1, 2: a group of 8 of the warp's 32 tokens
+        const int vword = (lane & 1) | (lane >> 3 & 3) << 1, vrow = (warp - 12) * 32 + (lane >> 1 & 3) * 8;
+        const int8_t* const from = a.c.v + (vrow & 8) * D + vword * 4;
         auto load = [&](int j) {
+            const int64_t at = sh.at[j * 8 + vrow / 16];
+            const bool on = at >= 0;
+            const int8_t* x = from + (on ? at : 0);
 #pragma unroll
-            for (int i = 0; i < KN; ++i) {
-                const int piece = p % ROWP, t = p / ROWP + i * (kPreProducers / ROWP);
-                const int8_t* x = rows_at(a.c.k, j * kPreTile + t);
-                kr[i] = x ? ldg_stream(reinterpret_cast<const uint4*>(x + piece * 16)) : make_uint4(0, 0, 0, 0);
-            }
+            for (int i = 0; i < VN; ++i)
 #pragma unroll
-            for (int i = 0; i < VN; ++i) {
-                const int task = pw * VN + i, dims = (task % (D / 32)) * 32, t0 = (task / (D / 32)) * 32 + vgroup * 8;
-                const int8_t* x = rows_at(a.c.v, j * kPreTile + t0);
+                for (int u = 0; u < 8; ++u) vr[i][u] = __ldg(reinterpret_cast<const uint32_t*>(x + u * D + i * 32));
+            if (!on) {
 #pragma unroll
-                for (int u = 0; u < 8; ++u) vr[i][u] = x ? __ldg(reinterpret_cast<const uint32_t*>(x + u * D + dims) + vword) : 0u;
+                for (int i = 0; i < VN; ++i)
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) vr[i][u] = 0u;
             }
         };
+        // piece of 8 tokens vrow / 8 % 8 of half vrow / 64; rows 4 vword .. of the turn, whose low bits are u and vword's
+        uint8_t* const vto = sh.v[0][vrow / 64] + vword * 4 * 128;
+        const int vc = (vrow / 8 & 7) ^ (vword & 1) << 2;
         bool ok = true;
         if (steps > 0) load(0);
-        for (int j = 0; j < steps && ok; ++j) {
-            const int st = j % kPreStages;
-            const uint32_t phase = (j / kPreStages & 1) ^ 1;
-            ok = !*abort && mbar_wait(&sh.k_empty[st], phase, kPreWaitLimit);
+        for (int j = 0; j < steps; ++j) {
+            ok = wait_or_abort(&sh.v_empty[j & 1], (j >> 1 & 1) ^ 1, abort);
             if (!ok) break;
-#pragma unroll
-            for (int i = 0; i < KN; ++i) {
-                const int piece = p % ROWP, t = p / ROWP + i * (kPreProducers / ROWP);
-                uint4 lo, hi;
-                codes_to_half(kr[i].x, lo.x, lo.y);
-                codes_to_half(kr[i].y, lo.z, lo.w);
-                codes_to_half(kr[i].z, hi.x, hi.y);
-                codes_to_half(kr[i].w, hi.z, hi.w);
-                // dims 16 piece ..: pieces 2 (piece % 4) and the next of half piece / 4; the second half's lanes
-                // store in the other order, so that eight lanes fill eight different pieces
-                uint8_t* to = &sh.k[st][piece / 4][t * 128];
-                const int c = (piece & 3) * 2, swap = piece >> 2 & 1;
-                *reinterpret_cast<uint4*>(to + (((c + swap) ^ (t & 7)) << 4)) = swap ? hi : lo;
-                *reinterpret_cast<uint4*>(to + (((c + (swap ^ 1)) ^ (t & 7)) << 4)) = swap ? lo : hi;
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.k_full[st]);
-            ok = !*abort && mbar_wait(&sh.v_empty[st], phase, kPreWaitLimit);
-            if (!ok) break;
+            uint8_t* to = vto + (j & 1) * int(sizeof(sh.v[0]));
 #pragma unroll
             for (int i = 0; i < VN; ++i) {
-                const int task = pw * VN + i, dims = (task % (D / 32)) * 32, t0 = (task / (D / 32)) * 32 + vgroup * 8;
                 uint32_t out[4][4];  // [dim][pairs of tokens]
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
@@ -397,22 +567,65 @@ kv_prefill_kernel(AttendArgs a, int splits, int stretch, int pairs)
                     biased_to_half(__byte_perm(x, y, 0x5140), out[0][u], out[1][u]);
                     biased_to_half(__byte_perm(x, y, 0x7362), out[2][u], out[3][u]);
                 }
-                const int half = t0 / 64, c = t0 % 64 / 8;
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int d = dims + vword * 4 + u;
-                    *reinterpret_cast<uint4*>(&sh.v[st][half][d * 128 + ((c ^ (d & 7)) << 4)]) =
+                for (int u = 0; u < 4; ++u)
+                    *reinterpret_cast<uint4*>(to + (i * 32 + u) * 128 + ((vc ^ u) << 4)) =
                         make_uint4(out[u][0], out[u][1], out[u][2], out[u][3]);
-                }
             }
+            if (j + 1 < steps) load(j + 1);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.v_full[st]);
-            if (j + 1 < steps) load(j + 1);
+            if (lane == 0) mbar_arrive(&sh.v_full[j & 1]);
         }
         if (!ok) give_up();
-    } else if (tile < tiles) {
+    } else if (warp >= 8) {
+        // ------------------------------------------------------------------ K --
+        regs_down<kPreLoaderRegs>();
+        constexpr int ROWP = D / 16;                 // 16-byte pieces of a row
+        constexpr int ROWS = kPreLoaders / ROWP;     // rows per turn: 16 (D = 128) or 32
+        constexpr int KN = kPreTile / ROWS;          // turns
+        uint4 kr[KN];
+        const int p = tid - 256, piece = p % ROWP, krow = p / ROWP;
+        const int8_t* const from = a.c.k + (krow & 15) * D + piece * 16;
+        auto load = [&](int j) {
+#pragma unroll
+            for (int i = 0; i < KN; ++i) {
+                const int64_t at = sh.at[j * 8 + (krow + i * ROWS) / 16];
+                kr[i] = ldg_stream(reinterpret_cast<const uint4*>(from + (at >= 0 ? at : 0)));
+                if (at < 0) kr[i] = make_uint4(0, 0, 0, 0);
+            }
+        };
+        // dims 16 piece .. are pieces 2 (piece % 4) and the next of half piece / 4; the second half's lanes store them
+        // in the other order, so that eight lanes fill eight different pieces
+        const int swap = piece >> 2 & 1, kc = (piece & 3) * 2;
+        uint8_t* const kto = sh.k[0][piece / 4] + krow * 128;
+        const int k0 = ((kc + swap) ^ (krow & 7)) << 4, k1 = ((kc + (swap ^ 1)) ^ (krow & 7)) << 4;
+        bool ok = true;
+        if (steps > 0) load(0);
+        for (int j = 0; j < steps; ++j) {
+            ok = wait_or_abort(&sh.k_empty[j & 1], (j >> 1 & 1) ^ 1, abort);
+            if (!ok) break;
+            uint8_t* to = kto + (j & 1) * int(sizeof(sh.k[0]));
+#pragma unroll
+            for (int i = 0; i < KN; ++i) {
+                uint4 lo, hi;
+                codes_to_half(kr[i].x, lo.x, lo.y);
+                codes_to_half(kr[i].y, lo.z, lo.w);
+                codes_to_half(kr[i].z, hi.x, hi.y);
+                codes_to_half(kr[i].w, hi.z, hi.w);
+                *reinterpret_cast<uint4*>(to + i * ROWS * 128 + k0) = swap ? hi : lo;
+                *reinterpret_cast<uint4*>(to + i * ROWS * 128 + k1) = swap ? lo : hi;
+            }
+            if (j + 1 < steps) load(j + 1);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.k_full[j & 1]);
+        }
+        if (!ok) give_up();
+    } else {
         // ------------------------------------------------------------- softmax --
+        regs_up<kPreSoftmaxRegs>();
+        if (tile < tiles) {
         const uint32_t lanes = uint32_t(warp & 3) << 21;  // TMEM lane 32 (warp % 4) in bits 16 on
         const uint32_t ts = tmem + lanes + tile * 128, to = tmem + lanes + 256 + tile * 128;
         int see = tokens;  // tokens of the stretch that this column sees
@@ -420,105 +633,36 @@ kv_prefill_kernel(AttendArgs a, int splits, int stretch, int pairs)
         const int least = __reduce_min_sync(0xffffffffu, see);
         bool ok = true;
         for (int j = 0; j < steps && ok; ++j) {
-            ok = !*abort && mbar_wait(&sh.s_full[tile], j & 1, kPreWaitLimit);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
+            const int left = see - j * kPreTile;
+            const float *ks = sh.ks + j * 8, *vs = sh.vs + j * 8;
+            float sc[8], vf[8];  // before the wait: shared memory is slow while products read it
+#pragma unroll
+            for (int b = 0; b < 8; b += 4) {
+                const float4 x = *reinterpret_cast<const float4*>(ks + b), y = *reinterpret_cast<const float4*>(vs + b);
+                sc[b] = x.x, sc[b + 1] = x.y, sc[b + 2] = x.z, sc[b + 3] = x.w;
+                vf[b] = y.x, vf[b + 1] = y.y, vf[b + 2] = y.z, vf[b + 3] = y.w;
             }
-            tc_fence_after();
-            const int jj0 = j * kPreTile;
-            float ks[8], vs[8];  // of each 16 tokens
-            bool whole = jj0 + kPreTile <= least;
+            bool whole = (j + 1) * kPreTile <= least;
 #pragma unroll
             for (int b = 0; b < 8; ++b) {
-                ks[b] = sh.ks[(jj0 + 16 * b) >> shift];
-                whole = whole && ks[b] >= 0.f;
+                whole = whole && sc[b] >= 0.f;
+                sc[b] *= mult;
             }
-            float top = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float s[32];
-                tmem_ld32(ts + 32 * c, s);
-                tmem_wait_ld();
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float sc = ks[2 * c + h] * mult;
-                    float x = -INFINITY;
-                    if (whole) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) x = fmaxf(x, s[16 * h + i]);
-                        top = fmaxf(top, x * sc);
-                    } else if (ks[2 * c + h] >= 0.f) {
-                        const int left = see - (jj0 + 32 * c + 16 * h);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) x = i < left ? fmaxf(x, s[16 * h + i]) : x;
-                        if (left > 0) top = fmaxf(top, x * sc);
-                    }
-                }
-            }
-            // the reference: raised when a score is far above it
-            const bool first = m == -INFINITY;
-            const bool raise = first ? top > -INFINITY : top > m + kPreRaise;
-            if (__any_sync(0xffffffffu, raise && !first)) {
-                ok = mbar_wait(&sh.pv_done[tile], (j - 1) & 1, kPreWaitLimit);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const float z = raise && !first ? ex2(m - top) : 1.f;
-                l *= z;
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    float o[32];
-                    tmem_ld32(to + 32 * c, o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] *= z;
-                    tmem_st32(to + 32 * c, o);
-                }
-                tmem_wait_st();
-            }
-            if (raise) m = top;
+            ok = wait_or_abort(&sh.s_full[tile], j & 1, abort);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();  // the products of the step before are done too
+            const float top = whole ? step_max(ts, sc) : step_max_masked(ts, ks, mult, left);
+            if (m == -INFINITY) m = top;  // nothing seen before: l and O are 0
+            if (__any_sync(0xffffffffu, top > m + kPreRaise)) raise<D>(to, top > m + kPreRaise ? top - m : 0.f, j > 0, m, l);
             const float base = m > -INFINITY ? m : 0.f;
-#pragma unroll
-            for (int b = 0; b < 8; ++b) vs[b] = sh.vs[(jj0 + 16 * b) >> shift] * vinv;
-            float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float s[32];
-                tmem_ld32(ts + 32 * c, s);
-                tmem_wait_ld();
-                uint32_t p[16];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float sc = ks[2 * c + h] * mult, vf = vs[2 * c + h];
-                    const int left = see - (jj0 + 32 * c + 16 * h);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float2 x = fma2(make_float2(s[16 * h + 2 * i], s[16 * h + 2 * i + 1]), make_float2(sc, sc), make_float2(-base, -base));
-                        x.x = ex2(x.x);
-                        x.y = ex2(x.y);
-                        if (!whole) {
-                            const bool on = ks[2 * c + h] >= 0.f;
-                            x.x = on && 2 * i < left ? x.x : 0.f;
-                            x.y = on && 2 * i + 1 < left ? x.y : 0.f;
-                        }
-                        sum = add2(sum, x);
-                        x = mul2(x, make_float2(vf, vf));
-                        p[8 * h + i] = pack_half2(x.x, x.y);
-                    }
-                }
-                // over the scores just read: tokens 32 c .. 32 c + 31 take columns 16 c ..
-                tmem_st16(ts + 16 * c, p);
-            }
-            l += sum.x + sum.y;
+            l += whole ? step_weights(ts, sc, vf, base) : step_weights_masked(ts, ks, vs, mult, base, left);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.p_ready[tile]);
         }
-        if (ok && steps > 0) ok = mbar_wait(&sh.pv_done[tile], (steps - 1) & 1, kPreWaitLimit);
+        if (ok && steps > 0) ok = wait_or_abort(&sh.pv_done[tile], (steps - 1) & 1, abort);
         if (!__all_sync(0xffffffffu, ok)) {
             give_up();
         } else {
@@ -560,10 +704,11 @@ kv_prefill_kernel(AttendArgs a, int splits, int stretch, int pairs)
                 }
             }
         }
+        }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 16) {
+    if (warp == kPreMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }

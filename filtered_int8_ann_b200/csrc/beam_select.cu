@@ -19,6 +19,8 @@
 // the stretch's keep-th logit from below, so only the few logits above it are
 // written. Where equal logits make them too many, a bisection over
 // (logit, index) finds the exact border.
+#include <cfloat>
+
 #include "decode.cuh"
 
 namespace st {
@@ -28,6 +30,7 @@ constexpr int kSelPerThread = 32;
 constexpr int kSelStretch = kSelThreads * kSelPerThread;
 constexpr int kMergeThreads = 1024;
 constexpr int kMergeCap = 2048;   // pairs sorted at the end
+constexpr int kMergeRank = kMergeThreads / 4;  // up to this many are ordered by counting
 constexpr int kMergeUnits = 4096; // stretches listed as holding such pairs
 constexpr int kHistBins = 256;
 
@@ -59,7 +62,7 @@ __device__ const Powers32 kPowers32{};
 // order-preserving unsigned form of a float (no NaN)
 __device__ __forceinline__ uint32_t float_key(float x)
 {
-    const uint32_t u = __float_as_uint(x);
+    const uint32_t u = __float_as_uint(x + 0.f);  // -0 becomes 0
     return u ^ (u & 0x80000000u ? 0xffffffffu : 0x80000000u);
 }
 __device__ __forceinline__ uint64_t double_key(double x)
@@ -81,47 +84,57 @@ __device__ __forceinline__ float warp_min(float m)
     return m;
 }
 
+// Logits as they are held: 16 bytes are PER of them in four words. A 32-bit word holds one (f32) or two.
 template <typename T>
 struct Logit;
 template <>
 struct Logit<float> {
-    static constexpr int kPer = 4;  // per 16 bytes
-    __device__ static void unpack(const uint4& w, float* x)
-    {
-        x[0] = __uint_as_float(w.x);
-        x[1] = __uint_as_float(w.y);
-        x[2] = __uint_as_float(w.z);
-        x[3] = __uint_as_float(w.w);
-    }
+    static constexpr int kPer = 4, kIn = 1;  // per 16 bytes, per word
+    static constexpr uint32_t kNone = 0xff800000u;  // -inf
+    __device__ static uint32_t max2(uint32_t a, uint32_t b) { return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b))); }
+    __device__ static float get(uint32_t w, int) { return __uint_as_float(w); }
+    __device__ static uint32_t both(float x) { return __float_as_uint(x); }
+    // bits of the word's elements that are at least x
+    __device__ static uint32_t reach(uint32_t w, uint32_t x) { return __uint_as_float(w) >= __uint_as_float(x) ? 1u : 0u; }
+    __device__ static uint32_t keep(uint32_t w, uint32_t bits) { return bits & 1u ? w : kNone; }
     __device__ static float one(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
+    __device__ static uint32_t bits(const void* p, int64_t i) { return static_cast<const uint32_t*>(p)[i]; }
+};
+template <typename H, typename H2>
+struct LogitHalf {
+    static constexpr int kPer = 8, kIn = 2;
+    __device__ static H2 as(uint32_t w) { return *reinterpret_cast<const H2*>(&w); }
+    __device__ static uint32_t max2(uint32_t a, uint32_t b)
+    {
+        const H2 m = __hmax2(as(a), as(b));
+        return *reinterpret_cast<const uint32_t*>(&m);
+    }
+    __device__ static uint32_t reach(uint32_t w, uint32_t x)
+    {
+        const unsigned r = __hge2_mask(as(w), as(x));
+        return (r & 1u) | (r >> 30 & 2u);
+    }
+    static __device__ uint32_t keep2(uint32_t w, uint32_t bits, uint32_t none)
+    {
+        const uint32_t on = (bits & 1u ? 0xffffu : 0u) | (bits & 2u ? 0xffff0000u : 0u);
+        return (w & on) | (none & ~on);
+    }
+    __device__ static uint32_t bits(const void* p, int64_t i) { return static_cast<const uint16_t*>(p)[i]; }
 };
 template <>
-struct Logit<__nv_bfloat16> {
-    static constexpr int kPer = 8;
-    __device__ static void unpack(const uint4& w, float* x)
-    {
-        const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(a[i] << 16);
-            x[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
-        }
-    }
+struct Logit<__nv_bfloat16> : LogitHalf<__nv_bfloat16, __nv_bfloat162> {
+    static constexpr uint32_t kNone = 0xff80ff80u;
+    __device__ static float get(uint32_t w, int i) { return __uint_as_float(i ? w & 0xffff0000u : w << 16); }
+    __device__ static uint32_t both(float x) { const __nv_bfloat162 h = __float2bfloat162_rn(fmaxf(x, -3.3895313892515355e38f)); return *reinterpret_cast<const uint32_t*>(&h); }
+    __device__ static uint32_t keep(uint32_t w, uint32_t bits) { return keep2(w, bits, kNone); }
     __device__ static float one(const void* p, int64_t i) { return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]); }
 };
 template <>
-struct Logit<__half> {
-    static constexpr int kPer = 8;
-    __device__ static void unpack(const uint4& w, float* x)
-    {
-        const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a[i]));
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
-        }
-    }
+struct Logit<__half> : LogitHalf<__half, __half2> {
+    static constexpr uint32_t kNone = 0xfc00fc00u;
+    __device__ static float get(uint32_t w, int i) { const __half2 h = as(w); return i ? __high2float(h) : __low2float(h); }
+    __device__ static uint32_t both(float x) { const __half2 h = __float2half2_rn(fmaxf(x, -65504.f)); return *reinterpret_cast<const uint32_t*>(&h); }
+    __device__ static uint32_t keep(uint32_t w, uint32_t bits) { return keep2(w, bits, kNone); }
     __device__ static float one(const void* p, int64_t i) { return __half2float(static_cast<const __half*>(p)[i]); }
 };
 
@@ -161,13 +174,14 @@ __device__ __forceinline__ void find_bin(const uint32_t* hist, uint32_t want, in
 
 // A value's place in the histogram is (best - value) * inv; values not at or above `edge` there are kept
 // (written so that an infinite range, with inv = 0, keeps them).
-__device__ __forceinline__ float bin_scale(float range) { return range > 0.f ? fminf((kHistBins - 1) / range, 3e38f) : 0.f; }
+__device__ __forceinline__ float bin_scale(float range, int bins) { return range > 0.f ? fminf(float(bins - 1) / range, 3e38f) : 0.f; }
 
 template <typename T>
-__global__ void __launch_bounds__(kSelThreads)
+__global__ void __launch_bounds__(kSelThreads, 3)
 beam_stretch_kernel(SelectArgs a, int stretches, int cap, Stretch* res, uint2* lists)
 {
-    constexpr int PER = Logit<T>::kPer, VECS = kSelPerThread / PER;
+    using L = Logit<T>;
+    constexpr int PER = L::kPer, IN = L::kIn, VECS = kSelPerThread / PER, WORDS = VECS * 4;
     __shared__ float s_max[kSelThreads / 32], s_min[kSelThreads / 32];
     __shared__ double s_sum[kSelThreads / 32];
     __shared__ uint32_t s_hist[kHistBins];
@@ -196,58 +210,82 @@ beam_stretch_kernel(SelectArgs a, int stretches, int cap, Stretch* res, uint2* l
     // Vectors of 16 aligned bytes; the first may begin before the row, the last end behind it.
     const T* x = static_cast<const T*>(a.logits) + row * a.stride;
     const int before = int((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
-    const int64_t first = int64_t(blockIdx.x) * kSelStretch - before;  // the row's index of the stretch's first element
-    const uint32_t* allow = a.ex.allow ? a.ex.allow + b * a.ex.allow_request_stride + i * a.ex.allow_beam_stride : nullptr;
-    const int words = (a.V + 31) / 32;
-    float v[kSelPerThread];
+    const int first = int(blockIdx.x) * kSelStretch - before;  // the row's index of the stretch's first element
+    const int live = min(kSelStretch, a.V - first);  // elements from there on
+    // the row's index of element u of this thread's word k
+    auto index_of = [&](int k, int u) { return first + ((k / 4) * kSelThreads + tid) * PER + (k % 4) * IN + u; };
+    uint32_t v[WORDS];
 #pragma unroll
     for (int j = 0; j < VECS; ++j) {
-        const int64_t e = first + int64_t(j * kSelThreads + tid) * PER;
-        float* y = v + j * PER;
+        const int e = first + (j * kSelThreads + tid) * PER;
         if (e >= 0 && e + PER <= a.V) {
-            Logit<T>::unpack(__ldcs(reinterpret_cast<const uint4*>(x + e)), y);
+            const uint4 w = __ldcs(reinterpret_cast<const uint4*>(x + e));
+            v[4 * j] = w.x;
+            v[4 * j + 1] = w.y;
+            v[4 * j + 2] = w.z;
+            v[4 * j + 3] = w.w;
         } else {
 #pragma unroll
-            for (int u = 0; u < PER; ++u) y[u] = e + u >= 0 && e + u < a.V ? Logit<T>::one(x, e + u) : -INFINITY;
+            for (int k = 0; k < 4; ++k) {
+                uint32_t w = L::kNone;
+#pragma unroll
+                for (int u = 0; u < IN; ++u) {
+                    const int at = e + k * IN + u;
+                    if (at >= 0 && at < a.V) {
+                        if (IN == 1) w = L::bits(x, at);
+                        else w = (w & (u ? 0xffffu : 0xffff0000u)) | L::bits(x, at) << (16 * u);
+                    }
+                }
+                v[4 * j + k] = w;
+            }
         }
     }
-    if (allow) {
+    if (a.ex.allow) {
+        const uint32_t* allow = a.ex.allow + b * a.ex.allow_request_stride + i * a.ex.allow_beam_stride;
+        const int words = (a.V + 31) / 32;
 #pragma unroll
         for (int j = 0; j < VECS; ++j) {
-            const int64_t e = first + int64_t(j * kSelThreads + tid) * PER;
+            const int e = first + (j * kSelThreads + tid) * PER;
             if (e + PER <= 0 || e >= a.V) continue;
-            const int64_t at = e < 0 ? 0 : e;  // bits of elements at .. at + PER
+            const int at = e < 0 ? 0 : e;  // bits of elements at .. at + PER
             const int w = int(at >> 5);
             const uint32_t lo = allow[w], hi = w + 1 < words ? allow[w + 1] : 0u;
-            uint32_t bits = __funnelshift_r(lo, hi, uint32_t(at & 31));
-            bits <<= uint32_t(at - e);
+            const uint32_t bits = __funnelshift_r(lo, hi, uint32_t(at & 31)) << uint32_t(at - e);
 #pragma unroll
-            for (int u = 0; u < PER; ++u)
-                if (!(bits >> u & 1u)) v[j * PER + u] = -INFINITY;
+            for (int k = 0; k < 4; ++k) v[4 * j + k] = L::keep(v[4 * j + k], bits >> (k * IN));
         }
     }
-    float tmax = -INFINITY;
+    // The maximum (NaN takes no part). Where it is +inf, those entries leave and it is taken again.
+    s_hist[tid] = 0;
+    if (tid == 0) s_count = s_total = 0;
+    float tmax, m, least;
+    for (int pass = 0;; ++pass) {
+        uint32_t top = v[0];
 #pragma unroll
-    for (int k = 0; k < kSelPerThread; ++k) {
-        v[k] = v[k] < INFINITY ? v[k] + 0.f : -INFINITY;  // NaN and +inf leave; -0 becomes 0
-        tmax = fmaxf(tmax, v[k]);
-    }
-    const int live = int(min(int64_t(kSelStretch), int64_t(a.V) - first));  // elements from the stretch's first on
-    {
+        for (int k = 1; k < WORDS; ++k) top = L::max2(top, v[k]);
+        tmax = IN == 1 ? L::get(top, 0) : fmaxf(L::get(top, 0), L::get(top, 1));
         const float wm = warp_max(tmax), wl = warp_min(tmax > -INFINITY ? tmax : INFINITY);
         if (lane == 0) {
             s_max[warp] = wm;
             s_min[warp] = wl;
         }
-    }
-    s_hist[tid] = 0;
-    if (tid == 0) s_count = s_total = 0;
-    __syncthreads();
-    float m = s_max[0], least = s_min[0];
+        __syncthreads();
+        m = s_max[0];
+        least = s_min[0];
 #pragma unroll
-    for (int w = 1; w < kSelThreads / 32; ++w) {
-        m = fmaxf(m, s_max[w]);
-        least = fminf(least, s_min[w]);
+        for (int w = 1; w < kSelThreads / 32; ++w) {
+            m = fmaxf(m, s_max[w]);
+            least = fminf(least, s_min[w]);
+        }
+        if (m < INFINITY || pass > 0) break;
+#pragma unroll
+        for (int k = 0; k < WORDS; ++k) {
+            uint32_t on = 0;
+#pragma unroll
+            for (int u = 0; u < IN; ++u) on |= (L::get(v[k], u) < INFINITY ? 1u : 0u) << u;
+            v[k] = L::keep(v[k], on);
+        }
+        __syncthreads();
     }
     if (!(m > -INFINITY)) {  // nothing allowed here
         if (tid == 0) res[unit] = Stretch{0.0, -INFINITY, 0};
@@ -256,35 +294,47 @@ beam_stretch_kernel(SelectArgs a, int stretches, int cap, Stretch* res, uint2* l
 
     // sum of exp(x - m)
     const double power = kPowers32.v[lane];
-    constexpr double kC = 46.166241308446828384;  // 32 / ln 2
-    constexpr double kMagic = 6755399441055744.0; // 1.5 * 2^52: adding it leaves the nearest integer in the low bits
-    const double mc = double(m) * -kC;
-    const float floor_x = m - 700.f;              // exp(-700) is nothing next to 1
+    const int power_hi = __double2hiint(power), power_lo = __double2loint(power);
     double sum = 0.0;
-    if (fabsf(m) > 0x1p20f) {                     // that floor is not a number near m: rare, so the plain way
-#pragma unroll
-        for (int k = 0; k < kSelPerThread; ++k) {
-            const double d = double(v[k]) - double(m);
-            if (d >= -700.0) sum += exp(d);
+    if (fabsf(m) > 0x1p20f) {  // m - 700 is not a number near m: rare, so the plain way
+#pragma unroll 1
+        for (int e = tid; e < live; e += kSelThreads) {
+            // (from memory again, so that the registers need no index; allowed ones among them)
+            const int at = first + e;
+            if (at < 0) continue;
+            bool on = true;
+            if (a.ex.allow) on = (a.ex.allow + b * a.ex.allow_request_stride + i * a.ex.allow_beam_stride)[at >> 5] >> (at & 31) & 1u;
+            const float y = L::one(x, at);
+            const double d = double(y) - double(m);
+            if (on && y < INFINITY && d >= -700.0) sum += exp(d);
         }
     } else {
+        constexpr double kC = 46.166241308446828384;  // 32 / ln 2
+        constexpr double kMagic = 6755399441055744.0; // 1.5 * 2^52: adding it leaves the nearest integer in the low bits
+        constexpr double z = 0.0216608493924982908;   // ln 2 / 32
+        const double mc = double(m) * -kC;
+        const uint32_t floor2 = L::both(m - 700.f);   // exp(-700) is nothing next to 1; takes the place of -inf and NaN
+        double part[2] = {0.0, 0.0};
 #pragma unroll
-      for (int j = 0; j < VECS; ++j) {
-        if (j * kSelThreads * PER >= live) break;
+        for (int j = 0; j < VECS; ++j) {
+            if (j * kSelThreads * PER >= live) break;
 #pragma unroll
-        for (int u = 0; u < PER; ++u) {
-            const double y = fma(double(fmaxf(v[j * PER + u], floor_x)), kC, mc);
-            const double t = y + kMagic;
-            const double r = y - (t - kMagic);
-            const int k = __double2loint(t);
-            const int hi = __shfl_sync(0xffffffffu, __double2hiint(power), k & 31);
-            const int lo = __shfl_sync(0xffffffffu, __double2loint(power), k & 31);
-            const double scaled = __hiloint2double(hi + ((k >> 5) << 20), lo);
-            constexpr double z = 0.0216608493924982908;  // ln 2 / 32
-            const double p = fma(r, fma(r, fma(r, fma(r, z * z * z * z / 24, z * z * z / 6), z * z / 2), z), 1.0);
-            sum = fma(scaled, p, sum);
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t w = L::max2(v[4 * j + k], floor2);
+#pragma unroll
+                for (int u = 0; u < IN; ++u) {
+                    const double y = fma(double(L::get(w, u)), kC, mc);
+                    const double t = y + kMagic;
+                    const double r = y - (t - kMagic);
+                    const int n = __double2loint(t);
+                    const int hi = __shfl_sync(0xffffffffu, power_hi, n), lo = __shfl_sync(0xffffffffu, power_lo, n);
+                    const double scaled = __hiloint2double(hi + ((n >> 5) << 20), lo);
+                    const double p = fma(r, fma(r, fma(r, fma(r, z * z * z * z / 24, z * z * z / 6), z * z / 2), z), 1.0);
+                    part[(k + u) & 1] = fma(scaled, p, part[(k + u) & 1]);
+                }
+            }
         }
-      }
+        sum = part[0] + part[1];
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
@@ -292,38 +342,36 @@ beam_stretch_kernel(SelectArgs a, int stretches, int cap, Stretch* res, uint2* l
 
     // the edge below which at least `keep` maxima lie
     const uint32_t keep = uint32_t(a.keep);
-    float inv = bin_scale(m - least);
-    {
-        const bool coarse = keep <= kSelThreads / 2;  // a maximum per thread is enough to choose from
-        if (coarse) {
-            if (tmax > -INFINITY) {
-                atomicAdd(&s_hist[min(kHistBins - 1, int((m - tmax) * inv))], 1u);
-            }
-        } else {
+    const float inv = bin_scale(m - least, kHistBins);
+    if (keep <= kSelThreads / 2) {  // a maximum per thread is enough to choose from
+        if (tmax > -INFINITY) atomicAdd(&s_hist[min(kHistBins - 1, int((m - tmax) * inv))], 1u);
+    } else {  // one per vector
 #pragma unroll
-            for (int j = 0; j < VECS; ++j) {
-                float y = v[j * PER];
-#pragma unroll
-                for (int u = 1; u < PER; ++u) y = fmaxf(y, v[j * PER + u]);
-                if (y >= least) atomicAdd(&s_hist[min(kHistBins - 1, int((m - y) * inv))], 1u);
-            }
+        for (int j = 0; j < VECS; ++j) {
+            const uint32_t w = L::max2(L::max2(v[4 * j], v[4 * j + 1]), L::max2(v[4 * j + 2], v[4 * j + 3]));
+            const float y = IN == 1 ? L::get(w, 0) : fmaxf(L::get(w, 0), L::get(w, 1));
+            if (y >= least) atomicAdd(&s_hist[min(kHistBins - 1, int((m - y) * inv))], 1u);
         }
     }
     __syncthreads();
     find_bin<kHistBins>(s_hist, keep, &s_bin);
     __syncthreads();
-    float edge = s_bin >= 0 ? float(s_bin + 1) : INFINITY;
-    if (s_bin == kHistBins - 1) edge = INFINITY;  // that bin also holds what lies below `least`
-    // entries above the edge
+    // Entries down to a value that is surely not above the edge. The last bin also holds what lies below `least`.
+    float edge = -FLT_MAX;
+    if (s_bin >= 0 && s_bin < kHistBins - 1 && inv > 0.f) edge = fmaxf(edge, m - float(s_bin + 1) / inv * 1.00001f - fabsf(m) * 0x1p-20f);
+    if (edge <= tmax) {  // (false where this thread has none: NaN or -inf)
+        const uint32_t e2 = L::both(edge);
+        // a value rounded up to the type would lose entries: one step down then
+        const uint32_t from = L::get(e2, 0) <= edge ? e2 : L::both(edge - fabsf(edge) * 0.01f - FLT_MIN);
+        uint32_t found = 0;
 #pragma unroll
-    for (int k = 0; k < kSelPerThread; ++k) {
-        const float x0 = v[k];
-        if (x0 > -INFINITY && !((m - x0) * inv >= edge)) {
+        for (int k = 0; k < WORDS; ++k) found |= L::reach(v[k], from) << (k * IN);
+        while (found) {
+            const int k = __ffs(found) - 1;
+            found &= found - 1;
+            const int e = index_of(k / IN, k % IN);
             const uint32_t at = atomicAdd(&s_count, 1u);
-            if (at < uint32_t(cap)) {
-                const int64_t e = first + int64_t((k / PER) * kSelThreads + tid) * PER + k % PER;
-                list[at] = make_uint2(__float_as_uint(x0), uint32_t(e));
-            }
+            if (at < uint32_t(cap)) list[at] = make_uint2(__float_as_uint(L::one(x, e)), uint32_t(e));
         }
     }
     __syncthreads();
@@ -336,11 +384,13 @@ beam_stretch_kernel(SelectArgs a, int stretches, int cap, Stretch* res, uint2* l
             const uint64_t mid = border | 1ull << bit;
             uint32_t c = 0;
 #pragma unroll
-            for (int k = 0; k < kSelPerThread; ++k) {
-                const int64_t e = first + int64_t((k / PER) * kSelThreads + tid) * PER + k % PER;
-                const uint64_t key = uint64_t(float_key(v[k])) << 32 | (0xffffffffu - uint32_t(e));
-                c += v[k] > -INFINITY && key >= mid;
-            }
+            for (int k = 0; k < WORDS; ++k)
+#pragma unroll
+                for (int u = 0; u < IN; ++u) {
+                    const float y = L::get(v[k], u);
+                    const uint64_t key = uint64_t(float_key(y)) << 32 | (0xffffffffu - uint32_t(index_of(k, u)));
+                    c += y > -INFINITY && key >= mid;
+                }
             c = __reduce_add_sync(0xffffffffu, c);
             if (lane == 0) atomicAdd(&s_total, c);
             __syncthreads();
@@ -353,14 +403,17 @@ beam_stretch_kernel(SelectArgs a, int stretches, int cap, Stretch* res, uint2* l
         if (tid == 0) s_count = 0;
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < kSelPerThread; ++k) {
-            const int64_t e = first + int64_t((k / PER) * kSelThreads + tid) * PER + k % PER;
-            const uint64_t key = uint64_t(float_key(v[k])) << 32 | (0xffffffffu - uint32_t(e));
-            if (v[k] > -INFINITY && key >= border) {
-                const uint32_t at = atomicAdd(&s_count, 1u);
-                if (at < uint32_t(cap)) list[at] = make_uint2(__float_as_uint(v[k]), uint32_t(e));
+        for (int k = 0; k < WORDS; ++k)
+#pragma unroll
+            for (int u = 0; u < IN; ++u) {
+                const float y = L::get(v[k], u);
+                const int e = index_of(k, u);
+                const uint64_t key = uint64_t(float_key(y)) << 32 | (0xffffffffu - uint32_t(e));
+                if (y > -INFINITY && key >= border) {
+                    const uint32_t at = atomicAdd(&s_count, 1u);
+                    if (at < uint32_t(cap)) list[at] = make_uint2(__float_as_uint(y), uint32_t(e));
+                }
             }
-        }
         __syncthreads();
         count = min(s_count, uint32_t(cap));
     }
@@ -372,121 +425,181 @@ beam_stretch_kernel(SelectArgs a, int stretches, int cap, Stretch* res, uint2* l
     }
 }
 
+// The second launch keeps a request's pairs in shared memory.
+constexpr int kMergePairs = 4096;  // pairs collected
+constexpr int kMergeBins = 1024;
+
 struct MergeShared {
     double base[ST_BEAM_MAX_BEAMS];  // score minus normaliser; NaN: no candidates
-    uint64_t key[kMergeCap];
-    uint32_t flat[kMergeCap];
+    uint64_t key[kMergePairs];       // score (order-preserving); then the sorted ones
+    uint32_t flat[kMergePairs];      // i * V + v
+    uint64_t out_key[kMergeCap];
+    uint32_t out_flat[kMergeCap];
     int32_t units[kMergeUnits];
-    uint32_t hist[kHistBins];
-    double red[kMergeThreads / 32], red2[kMergeThreads / 32];
-    uint32_t n_units, n_pairs, n_tops;
+    uint32_t hist[kMergeBins];
+    double best[kMergeThreads / 32], least[kMergeThreads / 32];
+    uint32_t n_units, n_pairs, n_out, n_tops;
     int bin;
 };
+
+__device__ __forceinline__ double key_double(uint64_t key)
+{
+    return __longlong_as_double((long long)(key >> 63 ? key ^ 1ull << 63 : ~key));
+}
 
 __global__ void __launch_bounds__(kMergeThreads)
 beam_merge_kernel(SelectArgs a, int stretches, int cap, const Stretch* res, const uint2* lists)
 {
+    dep_enter();
     extern __shared__ __align__(16) unsigned char raw[];
     MergeShared& sh = *reinterpret_cast<MergeShared*>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b = blockIdx.x;
     const int64_t row0 = int64_t(b) * a.K;
     const int n_units = a.K * stretches;
-    const double kNone = __longlong_as_double(0x7ff8000000000000ll);
+    const uint32_t keep = uint32_t(a.keep);
     res += row0 * stretches;
     lists += row0 * stretches * cap;
 
-    // the beams' normalisers, a warp per beam
-    for (int i = warp; i < a.K; i += kMergeThreads / 32) {
-        float m = -INFINITY;
-        for (int c = lane; c < stretches; c += 32) m = fmaxf(m, res[int64_t(i) * stretches + c].max);
-        m = warp_max(m);
-        double s = 0.0;
-        if (m > -INFINITY)
-            for (int c = lane; c < stretches; c += 32) {
-                const Stretch t = res[int64_t(i) * stretches + c];
-                if (t.max > -INFINITY) s += t.sum * exp(double(t.max) - double(m));
-            }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        if (lane == 0) sh.base[i] = m > -INFINITY ? double(a.scores[row0 + i]) - (double(m) + log(s)) : kNone;
-    }
-    for (int i = tid; i < kHistBins; i += kMergeThreads) sh.hist[i] = 0;
-    if (tid == 0) sh.n_units = sh.n_pairs = sh.n_tops = 0;
+    // the beams' normalisers, a warp per beam, and the range of the stretches' best scores
+    if (tid == 0) sh.n_units = sh.n_pairs = sh.n_out = sh.n_tops = 0;
+    for (int i = tid; i < kMergeBins; i += kMergeThreads) sh.hist[i] = 0;
     __syncthreads();
-
-    // the stretches' best scores: their range, and how many there are
     double best = -INFINITY, least = INFINITY;
     uint32_t tops = 0;
-    for (int u = tid; u < n_units; u += kMergeThreads) {
-        const float m = res[u].max;
-        const double s = sh.base[u / stretches] + double(m);
-        if (m > -INFINITY && s == s) {
-            best = fmax(best, s);
-            least = fmin(least, s);
-            ++tops;
+    for (int i = warp; i < a.K; i += kMergeThreads / 32) {
+        const Stretch* r = res + int64_t(i) * stretches;
+        float m = -INFINITY, low = INFINITY;
+        uint32_t n = 0;
+        for (int c = lane; c < stretches; c += 32) {
+            const float t = r[c].max;
+            m = fmaxf(m, t);
+            if (t > -INFINITY) {
+                low = fminf(low, t);
+                ++n;
+            }
         }
+        m = warp_max(m);
+        low = warp_min(low);
+        double s = 0.0, base = __longlong_as_double(0x7ff8000000000000ll);
+        if (m > -INFINITY) {
+            for (int c = lane; c < stretches; c += 32)
+                if (r[c].max > -INFINITY) s += r[c].sum * exp(double(r[c].max) - double(m));
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+            base = double(a.scores[row0 + i]) - (double(m) + log(s));
+            best = fmax(best, base + double(m));
+            least = fmin(least, base + double(low));
+            tops += n;
+        }
+        if (lane == 0) sh.base[i] = base;
     }
+    tops = __reduce_add_sync(0xffffffffu, tops);
+    if (lane == 0) {
+        sh.best[warp] = best;
+        sh.least[warp] = least;
+        if (tops) atomicAdd(&sh.n_tops, tops);
+    }
+    __syncthreads();
+    best = sh.best[lane];
+    least = sh.least[lane];
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
         best = fmax(best, __shfl_xor_sync(0xffffffffu, best, off));
         least = fmin(least, __shfl_xor_sync(0xffffffffu, least, off));
     }
-    tops = __reduce_add_sync(0xffffffffu, tops);
-    if (lane == 0) {
-        sh.red[warp] = best;
-        sh.red2[warp] = least;
-        if (tops) atomicAdd(&sh.n_tops, tops);
-    }
-    __syncthreads();
-    for (int w = 0; w < kMergeThreads / 32; ++w) {
-        best = fmax(best, sh.red[w]);
-        least = fmin(least, sh.red2[w]);
-    }
-    const uint32_t keep = uint32_t(a.keep);
+    // a score's place below the best: bins of `inv` per unit; scores whose place is not at or above the edge are kept
     float edge = INFINITY, inv = 0.f;
-    if (sh.n_tops >= keep) {  // the edge that `keep` of them reach: the keep-th score is not below it
-        inv = bin_scale(float(best - least));
+    auto place = [&](double s) { return float(best - s) * inv; };
+    auto score_of = [&](int u, float x) { return sh.base[u / stretches] + double(x); };
+    if (sh.n_tops >= keep) {  // the edge that `keep` of the stretches' best reach: the keep-th score is not below it
+        inv = bin_scale(float(best - least), kMergeBins);
         for (int u = tid; u < n_units; u += kMergeThreads) {
             const float m = res[u].max;
-            const double s = sh.base[u / stretches] + double(m);
-            if (m > -INFINITY && s == s) atomicAdd(&sh.hist[min(kHistBins - 1, int(float(best - s) * inv))], 1u);
+            if (m > -INFINITY) atomicAdd(&sh.hist[min(kMergeBins - 1, int(place(score_of(u, m))))], 1u);
         }
         __syncthreads();
-        find_bin<kHistBins>(sh.hist, keep, &sh.bin);
+        find_bin<kMergeBins>(sh.hist, keep, &sh.bin);
         __syncthreads();
-        if (sh.bin >= 0 && sh.bin < kHistBins - 1) edge = float(sh.bin + 1);
+        if (sh.bin >= 0 && sh.bin < kMergeBins - 1) edge = float(sh.bin + 1);
     }
-    // the stretches that reach it, then their entries
+    // the stretches that reach it
     for (int u = tid; u < n_units; u += kMergeThreads) {
         const float m = res[u].max;
-        const double s = sh.base[u / stretches] + double(m);
-        if (m > -INFINITY && s == s && !(float(best - s) * inv >= edge)) {
+        if (m > -INFINITY && !(place(score_of(u, m)) >= edge)) {
             const uint32_t at = atomicAdd(&sh.n_units, 1u);
             if (at < kMergeUnits) sh.units[at] = u;
         }
     }
     __syncthreads();
-    bool fits = sh.n_units <= kMergeUnits;
-    if (fits) {
-        const int n = int(sh.n_units);
-        for (int k = warp; k < n; k += kMergeThreads / 32) {
-            const int u = sh.units[k], i = u / stretches;
-            const int count = res[u].count;
+    const int listed = int(sh.n_units);
+    bool fits = listed <= kMergeUnits;
+    // their entries that reach it; where those are too many, a finer edge from a histogram of them all first
+    auto each_listed = [&](auto&& f) {
+        for (int k = warp; k < listed; k += kMergeThreads / 32) {
+            const int u = sh.units[k], i = u / stretches, count = res[u].count;
             for (int e = lane; e < count; e += 32) {
                 const uint2 w = lists[int64_t(u) * cap + e];
                 const double s = sh.base[i] + double(__uint_as_float(w.x));
-                if (!(float(best - s) * inv >= edge)) {
-                    const uint32_t at = atomicAdd(&sh.n_pairs, 1u);
-                    if (at < kMergeCap) {
-                        sh.key[at] = double_key(s);
-                        sh.flat[at] = uint32_t(i) * uint32_t(a.V) + w.y;
-                    }
+                if (!(place(s) >= edge)) f(s, uint32_t(i) * uint32_t(a.V) + w.y);
+            }
+        }
+    };
+    for (int pass = 0; fits && pass < 2; ++pass) {
+        each_listed([&](double s, uint32_t flat) {
+            const uint32_t at = atomicAdd(&sh.n_pairs, 1u);
+            if (at < kMergePairs) {
+                sh.key[at] = double_key(s);
+                sh.flat[at] = flat;
+            }
+        });
+        __syncthreads();
+        const bool all = sh.n_pairs <= kMergePairs;
+        __syncthreads();
+        if (all) break;
+        fits = pass == 0;
+        if (!fits) break;
+        const float span = edge == INFINITY ? float(best - least) : edge / inv;  // (least bounds no entries, so the last bin takes those below)
+        const float fine = bin_scale(span, kMergeBins);
+        for (int i = tid; i < kMergeBins; i += kMergeThreads) sh.hist[i] = 0;
+        if (tid == 0) sh.n_pairs = 0;
+        __syncthreads();
+        each_listed([&](double s, uint32_t) { atomicAdd(&sh.hist[min(kMergeBins - 1, int(float(best - s) * fine))], 1u); });
+        __syncthreads();
+        find_bin<kMergeBins>(sh.hist, keep, &sh.bin);
+        __syncthreads();
+        if (sh.bin < 0 || sh.bin >= kMergeBins - 1) {
+            fits = false;
+        } else {
+            inv = fine;
+            edge = float(sh.bin + 1);
+        }
+    }
+    if (fits) {
+        // In shared memory now: the edge that `keep` of them reach, and those above it.
+        const int n = int(sh.n_pairs);
+        const float span = edge == INFINITY ? float(best - least) : edge / inv;
+        const float fine = bin_scale(span, kMergeBins);
+        for (int i = tid; i < kMergeBins; i += kMergeThreads) sh.hist[i] = 0;
+        __syncthreads();
+        for (int k = tid; k < n; k += kMergeThreads)
+            atomicAdd(&sh.hist[min(kMergeBins - 1, int(float(best - key_double(sh.key[k])) * fine))], 1u);
+        __syncthreads();
+        find_bin<kMergeBins>(sh.hist, keep, &sh.bin);
+        __syncthreads();
+        const float last = sh.bin >= 0 && sh.bin < kMergeBins - 1 ? float(sh.bin + 1) : INFINITY;
+        for (int k = tid; k < n; k += kMergeThreads) {
+            const uint64_t key = sh.key[k];
+            if (!(float(best - key_double(key)) * fine >= last)) {
+                const uint32_t at = atomicAdd(&sh.n_out, 1u);
+                if (at < kMergeCap) {
+                    sh.out_key[at] = key;
+                    sh.out_flat[at] = sh.flat[k];
                 }
             }
         }
         __syncthreads();
-        fits = sh.n_pairs <= kMergeCap;
+        fits = sh.n_out <= kMergeCap;
     }
     if (!fits) {
         // Exact: the keep-th largest score by its eight digits, then the
@@ -507,7 +620,7 @@ beam_merge_kernel(SelectArgs a, int stretches, int cap, const Stretch* res, cons
         };
         for (int d = 7; d >= 0 && !all; --d) {  // digits from the top; bins reversed: the largest first
             __syncthreads();
-            for (int i = tid; i < kHistBins; i += kMergeThreads) sh.hist[i] = 0;
+            for (int i = tid; i < 256; i += kMergeThreads) sh.hist[i] = 0;
             __syncthreads();
             each([&](bool on, uint64_t key, uint32_t) {
                 on = on && (d == 7 || key >> (8 * d + 8) == prefix >> (8 * d + 8));
@@ -515,7 +628,7 @@ beam_merge_kernel(SelectArgs a, int stretches, int cap, const Stretch* res, cons
                 if (on) count_bin(sh.hist, 255 - int(key >> (8 * d) & 255), members);
             });
             __syncthreads();
-            find_bin<kHistBins>(sh.hist, want, &sh.bin);
+            find_bin<256>(sh.hist, want, &sh.bin);
             __syncthreads();
             if (sh.bin < 0) {
                 all = true;  // fewer than `keep` entries in all
@@ -527,7 +640,7 @@ beam_merge_kernel(SelectArgs a, int stretches, int cap, const Stretch* res, cons
         uint32_t last = 0;  // of the entries equal to the border, `want` are taken: the lowest indexes
         for (int d = 3; d >= 0 && !all; --d) {
             __syncthreads();
-            for (int i = tid; i < kHistBins; i += kMergeThreads) sh.hist[i] = 0;
+            for (int i = tid; i < 256; i += kMergeThreads) sh.hist[i] = 0;
             __syncthreads();
             each([&](bool on, uint64_t key, uint32_t flat) {
                 on = on && key == prefix && (d == 3 || flat >> (8 * d + 8) == last >> (8 * d + 8));
@@ -535,63 +648,88 @@ beam_merge_kernel(SelectArgs a, int stretches, int cap, const Stretch* res, cons
                 if (on) count_bin(sh.hist, int(flat >> (8 * d) & 255), members);
             });
             __syncthreads();
-            find_bin<kHistBins>(sh.hist, want, &sh.bin);
+            find_bin<256>(sh.hist, want, &sh.bin);
             __syncthreads();
             const int bin = max(sh.bin, 0);
             for (int i = 0; i < bin; ++i) want -= sh.hist[i];
             last |= uint32_t(bin) << (8 * d);
         }
         __syncthreads();
-        if (tid == 0) sh.n_pairs = 0;
+        if (tid == 0) sh.n_out = 0;
         __syncthreads();
         each([&](bool on, uint64_t key, uint32_t flat) {
             if (on && (all || key > prefix || (key == prefix && flat <= last))) {
-                const uint32_t at = atomicAdd(&sh.n_pairs, 1u);
+                const uint32_t at = atomicAdd(&sh.n_out, 1u);
                 if (at < kMergeCap) {
-                    sh.key[at] = key;
-                    sh.flat[at] = flat;
+                    sh.out_key[at] = key;
+                    sh.out_flat[at] = flat;
                 }
             }
         });
         __syncthreads();
     }
 
-    // order the pairs (bitonic, padded with the least key), write the best
-    const int n = int(min(sh.n_pairs, uint32_t(kMergeCap)));
-    int size = 32;
-    while (size < n) size <<= 1;
-    for (int i = n + tid; i < size; i += kMergeThreads) {
-        sh.key[i] = 0;
-        sh.flat[i] = 0xffffffffu;
-    }
-    __syncthreads();
-    for (int k = 2; k <= size; k <<= 1)
-        for (int j = k >> 1; j > 0; j >>= 1) {
-            for (int t = tid; t < size / 2; t += kMergeThreads) {
-                const int lo = 2 * t - (t & (j - 1)), hi = lo + j;
-                const uint64_t ka = sh.key[lo], kb = sh.key[hi];
-                const uint32_t fa = sh.flat[lo], fb = sh.flat[hi];
-                const bool ordered = ka > kb || (ka == kb && fa < fb);
-                if (ordered != ((lo & k) == 0)) {
-                    sh.key[lo] = kb;
-                    sh.key[hi] = ka;
-                    sh.flat[lo] = fb;
-                    sh.flat[hi] = fa;
-                }
+    // order the pairs: few by counting what precedes each, many by a bitonic sort
+    const int n = int(min(sh.n_out, uint32_t(kMergeCap)));
+    const uint64_t* keys = sh.out_key;
+    const uint32_t* flats = sh.out_flat;
+    if (n <= kMergeRank) {
+        // 4 threads per pair
+        const int k = tid / 4, part = tid & 3;
+        int before = 0;
+        uint64_t key = 0;
+        uint32_t flat = 0;
+        if (k < n) {
+            key = sh.out_key[k];
+            flat = sh.out_flat[k];
+            for (int o = part; o < n; o += 4) {
+                const uint64_t ko = sh.out_key[o];
+                before += ko > key || (ko == key && sh.out_flat[o] < flat);
             }
-            __syncthreads();
         }
+        before += __shfl_xor_sync(0xffffffffu, before, 1);
+        before += __shfl_xor_sync(0xffffffffu, before, 2);
+        if (k < n && part == 0) {  // the collected pairs are not needed any more
+            sh.key[before] = key;
+            sh.flat[before] = flat;
+        }
+        keys = sh.key;
+        flats = sh.flat;
+        __syncthreads();
+    } else {
+        int size = 32;
+        while (size < n) size <<= 1;
+        for (int i = n + tid; i < size; i += kMergeThreads) {
+            sh.out_key[i] = 0;
+            sh.out_flat[i] = 0xffffffffu;
+        }
+        __syncthreads();
+        for (int k = 2; k <= size; k <<= 1)
+            for (int j = k >> 1; j > 0; j >>= 1) {
+                for (int t = tid; t < size / 2; t += kMergeThreads) {
+                    const int lo = 2 * t - (t & (j - 1)), hi = lo + j;
+                    const uint64_t ka = sh.out_key[lo], kb = sh.out_key[hi];
+                    const uint32_t fa = sh.out_flat[lo], fb = sh.out_flat[hi];
+                    const bool ordered = ka > kb || (ka == kb && fa < fb);
+                    if (ordered != ((lo & k) == 0)) {
+                        sh.out_key[lo] = kb;
+                        sh.out_key[hi] = ka;
+                        sh.out_flat[lo] = fb;
+                        sh.out_flat[hi] = fa;
+                    }
+                }
+                __syncthreads();
+            }
+    }
     for (int r = tid; r < a.keep; r += kMergeThreads) {
         const int64_t o = int64_t(b) * a.keep + r;
         float s = -INFINITY;
         int parent = -1, token = -1;
         bool done = false;
         if (r < n) {
-            const uint64_t key = sh.key[r];
-            const uint64_t bits = key >> 63 ? key ^ 1ull << 63 : ~key;
-            s = float(__longlong_as_double((long long)(bits)));
-            parent = int(sh.flat[r] / uint32_t(a.V));
-            token = int(sh.flat[r] - uint32_t(parent) * uint32_t(a.V));
+            s = float(key_double(keys[r]));
+            parent = int(flats[r] / uint32_t(a.V));
+            token = int(flats[r] - uint32_t(parent) * uint32_t(a.V));
             if (a.ex.finished) done = a.ex.finished[row0 + parent] || token == a.ex.end_token;
         }
         a.out_scores[o] = s;
@@ -644,8 +782,8 @@ cudaError_t launch_beam_select(const SelectArgs& a, cudaStream_t s)
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    beam_merge_kernel<<<a.B, kMergeThreads, sizeof(MergeShared), s>>>(a, stretches, cap, res, lists);
-    return cudaGetLastError();
+    return launch_dep(beam_merge_kernel, dim3(unsigned(a.B)), dim3(kMergeThreads), sizeof(MergeShared), s, a, stretches, cap,
+                      static_cast<const Stretch*>(res), static_cast<const uint2*>(lists));
 }
 
 }  // namespace st

@@ -27,7 +27,7 @@ namespace st {
 constexpr int kPlanCtas = 8;      // CTAs of the cluster for large calls
 constexpr int kPlanBlock = 1024;
 // Calls up to these sizes take one CTA.
-constexpr int kPlanSmallRows = 1024;
+constexpr int kPlanSmallRows = 256;
 constexpr int kPlanSmallBlocks = 131072;
 constexpr int64_t kPlanSmallEntries = 32768;
 constexpr int kPlanWarps = kPlanBlock / 32;
@@ -77,90 +77,106 @@ __global__ void __launch_bounds__(kPlanBlock) kv_plan_kernel(PlanArgs a, int row
     extern __shared__ uint32_t smem[];
     __shared__ PlanShared sh;
     cg::cluster_group cluster = cg::this_cluster();
-    const int me = int(cluster.block_rank());
+    const int me = CTAS > 1 ? int(cluster.block_rank()) : 0;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto sync_all = [&]() {
+        if (CTAS > 1) cluster.sync();
+        else __syncthreads();
+    };
+    auto of = [&](auto* p, int rank) { return CTAS > 1 ? cluster.map_shared_rank(p, rank) : p; };
     // this CTA's part of the pool (bitmaps of words_per words) and of the rows
     uint32_t* used_bits = smem;
-    uint32_t* twice_bits = smem + words_per;
+    uint32_t* twice_bits = smem + words_per;        // later: free blocks before each word
     uint32_t* row_end = smem + 2 * words_per;       // [rows_per] blocks needed by rows up to this one, within the CTA
-    uint32_t* row_need = row_end + rows_per;        // [rows_per] blocks this row needs; bit 31: its last block is replaced
-    int32_t* row_tail = reinterpret_cast<int32_t*>(row_need + rows_per);  // [rows_per] that last block
-    const int r0 = min(a.R, me * rows_per), r1 = min(a.R, r0 + rows_per);
-    const int pages_per = words_per * 32;
-    const int S = a.block_size;
+    uint32_t* row_need = row_end + rows_per;        // [rows_per] blocks this row needs, and flags
+    int32_t* row_tail = reinterpret_cast<int32_t*>(row_need + rows_per);  // [rows_per] last block; later -1 if it stays
+    int32_t* row_have = row_tail + rows_per;
+    int32_t* row_tok = row_have + rows_per;         // [rows_per] end of the row's tokens
+    constexpr uint32_t kUnserved = 1u << 30, kRefused = 1u << 29, kNeed = kRefused - 1;
+    const int r0 = min(a.R, me * rows_per), r1 = min(a.R, r0 + rows_per), rows = r1 - r0;
+    const int pages_per = words_per * 32, width = a.max_blocks;
+    const int S = a.block_size, shift = 31 - __clz(S);
+    const int64_t room = int64_t(width) << shift;
 
     for (int i = tid; i < 2 * words_per; i += kPlanBlock) smem[i] = 0;
     if (tid == 0) sh.failed = sh.refused = 0;
-    __syncthreads();
-    cluster.sync();
+    for (int i = tid; i < rows; i += kPlanBlock) {
+        const int64_t have = a.have[r0 + i], add = a.add[r0 + i];
+        row_have[i] = int32_t(have);
+        row_need[i] = have < 0 || add < 0 || have > room ? kUnserved | kRefused : have + add > room ? kUnserved : 0u;
+        row_tail[i] = -1;
+    }
+    sync_all();
 
-    // 1. mark the blocks of the stored tokens, a warp per row; row_need holds the row's state meanwhile:
-    // 0 in order, 1 refused, 2 no room in its table row
-    for (int r = r0 + warp; r < r1; r += kPlanWarps) {
-        const int64_t have = a.have[r], add = a.add[r], room = int64_t(a.max_blocks) * S;
-        int state = have < 0 || add < 0 || have > room ? 1 : have + add > room ? 2 : 0;
-        if (have >= 0 && have <= room) {
-            const int n = int((have + S - 1) / S);
-            const int32_t* row = a.table + int64_t(r) * a.max_blocks;
-            bool bad = false;
-            for (int c = lane; c < n; c += 32) {
-                const int32_t p = row[c];
-                if (p < 0 || p >= a.num_blocks) {
+    // 1. mark the blocks of the stored tokens: eight lanes per row, a few entries each at a time
+    for (int i0 = warp * 4; i0 < rows; i0 += kPlanWarps * 4) {
+        const int i = i0 + (lane >> 3);
+        const int64_t have = i < rows ? row_have[i] : 0;
+        const int n = have > 0 && have <= room ? int((have + S - 1) >> shift) : 0;
+        const int32_t* row = a.table + int64_t(r0 + i) * width;
+        bool bad = false;
+        for (int c0 = lane & 7; c0 < n; c0 += 32) {
+            int32_t p[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) p[u] = c0 + 8 * u < n ? row[c0 + 8 * u] : 0;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int c = c0 + 8 * u;
+                if (c >= n) continue;
+                if (p[u] < 0 || p[u] >= a.num_blocks) {
                     bad = true;
                     continue;
                 }
-                const int owner = p / pages_per, w = (p - owner * pages_per) >> 5;
-                const uint32_t bit = 1u << (p & 31);
-                const uint32_t old = atomicOr(cluster.map_shared_rank(used_bits, owner) + w, bit);
-                if (old & bit) atomicOr(cluster.map_shared_rank(twice_bits, owner) + w, bit);
-            }
-            if (__any_sync(0xffffffffu, bad)) {
-                state = 1;
-                if (lane == 0) atomicOr(a.err, kDecErrTable);
+                const int owner = CTAS > 1 ? p[u] / pages_per : 0, w = (p[u] - owner * pages_per) >> 5;
+                const uint32_t bit = 1u << (p[u] & 31);
+                const uint32_t old = atomicOr(of(used_bits, owner) + w, bit);
+                if (old & bit) atomicOr(of(twice_bits, owner) + w, bit);
+                if (c == n - 1) row_tail[i] = p[u];
             }
         }
-        if (lane == 0) row_need[r - r0] = uint32_t(state);
+        if (bad) {
+            atomicOr(&row_need[i], kUnserved | kRefused);
+            atomicOr(a.err, kDecErrTable);
+        }
     }
-    __syncthreads();
-    cluster.sync();
+    sync_all();
 
     // 2a. rows: blocks needed and tokens, with prefix sums inside the CTA
     unsigned long long tok_base = 0;
     uint32_t need_base = 0;
     for (int i0 = 0; i0 < rows_per; i0 += kPlanBlock) {
-        const int r = r0 + i0 + tid;
-        const bool mine = i0 + tid < rows_per && r < r1;
+        const int i = i0 + tid;
+        const bool mine = i < rows;
         uint32_t need = 0;
-        int32_t tail = -1;
         unsigned long long tok = 0;
         if (mine) {
-            const int state = int(row_need[r - r0]);
-            const int have = a.have[r], add = a.add[r];
+            const uint32_t state = row_need[i];
+            const int have = row_have[i], add = a.add[r0 + i];
+            int32_t tail = -1;
             tok = add > 0 ? (unsigned long long)(add) : 0ull;
-            if (state == 0) {
-                const int used = int((int64_t(have) + S - 1) / S);
-                need = uint32_t((int64_t(have) + add + S - 1) / S) - uint32_t(used);
-                if (have % S != 0 && add > 0) {
-                    const int32_t p = a.table[int64_t(r) * a.max_blocks + used - 1];
-                    const int owner = p / pages_per, w = (p - owner * pages_per) >> 5;
-                    if (cluster.map_shared_rank(twice_bits, owner)[w] >> (p & 31) & 1u) {
+            if (!(state & kUnserved)) {
+                need = uint32_t(((int64_t(have) + add + S - 1) >> shift) - ((int64_t(have) + S - 1) >> shift));
+                if ((have & (S - 1)) != 0 && add > 0) {
+                    const int32_t p = row_tail[i];
+                    const int owner = CTAS > 1 ? p / pages_per : 0, w = (p - owner * pages_per) >> 5;
+                    if (of(twice_bits, owner)[w] >> (p & 31) & 1u) {  // the last block is replaced
                         tail = p;
                         ++need;
                     }
                 }
             }
-            if (state == 1) atomicAdd(&cluster.map_shared_rank(&sh, 0)->refused, 1u);
-            // state in the top bits: not to be served whatever the pool holds
-            row_need[r - r0] = need | (tail >= 0 ? 1u << 31 : 0u) | (state ? 1u << 30 : 0u) | (state == 1 ? 1u << 29 : 0u);
-            row_tail[r - r0] = tail;
+            if (state & kRefused) atomicAdd(&of(&sh, 0)->refused, 1u);
+            row_need[i] = need | state;
+            row_tail[i] = tail;
         }
         unsigned long long tok_total = 0;
         const unsigned long long tok_incl = block_incl_scan64(tok, sh.part64, tok_total);
         uint32_t need_total = 0;
         const uint32_t need_excl = block_excl_scan<kPlanBlock>(need, sh.part, need_total);
-        if (mine) row_end[r - r0] = need_base + need_excl + need;
-        // the row's token end within the CTA waits in row_start until the CTAs' bases are known
-        if (mine) a.row_start[r + 1] = int32_t(min((unsigned long long)(0x7fffffff), tok_base + tok_incl));
+        if (mine) {
+            row_end[i] = need_base + need_excl + need;
+            row_tok[i] = int32_t(min((unsigned long long)(0x7fffffff), tok_base + tok_incl));
+        }
         tok_base += tok_total;
         need_base += need_total;
     }
@@ -182,17 +198,15 @@ __global__ void __launch_bounds__(kPlanBlock) kv_plan_kernel(PlanArgs a, int row
         sh.need = need_base;
         sh.free = free_total;
     }
-    __syncthreads();
-    cluster.sync();
+    sync_all();
 
-    // 3. bases of the CTAs; token starts; which rows are served
-    unsigned long long tok_before = 0, tok_all = 0;
+    // 3. bases of the CTAs; token starts; which rows are served; free blocks before each word
+    unsigned long long tok_before = 0, tok_all = 0, need_all = 0;
     uint32_t need_before = 0, free_before = 0, free_all = 0;
-    unsigned long long need_all = 0;
     uint32_t need_ends[CTAS];  // blocks needed by the rows of CTAs 0..c
 #pragma unroll
     for (int c = 0; c < CTAS; ++c) {
-        const PlanShared* o = cluster.map_shared_rank(&sh, c);
+        const PlanShared* o = of(&sh, c);
         if (c < me) {
             tok_before += o->tokens;
             need_before += o->need;
@@ -204,75 +218,77 @@ __global__ void __launch_bounds__(kPlanBlock) kv_plan_kernel(PlanArgs a, int row
         need_ends[c] = uint32_t(need_all);
     }
     rank += free_before;
-    for (int i = tid; i < r1 - r0; i += kPlanBlock) {
-        const int r = r0 + i;
-        const unsigned long long end = tok_before + (unsigned long long)(uint32_t(a.row_start[r + 1]));
-        const uint32_t word = row_need[i], need = word & 0x1fffffffu;
-        const int have = a.have[r], add = a.add[r];
-        bool served = !(word >> 30 & 1u);
-        if (served && need > 0 && uint32_t(need_before + row_end[i]) > free_all) served = false;
+    for (int w = w0; w < w1; ++w) {
+        twice_bits[w] = rank;
+        rank += __popc(free_word(w));
+    }
+    if (me == 0 && tid == 0) a.row_start[0] = 0;
+    for (int i = tid; i < rows; i += kPlanBlock) {
+        const unsigned long long end = tok_before + (unsigned long long)(uint32_t(row_tok[i]));
+        const uint32_t word = row_need[i];
+        const int have = row_have[i], add = a.add[r0 + i];
+        bool served = !(word & kUnserved);
+        if (served && (word & kNeed) > 0 && need_before + row_end[i] > free_all) served = false;
         if (served && add > 0 && end > (unsigned long long)(a.T)) served = false;
-        a.lens[r] = served ? have + add : -1;
-        if (!served && !(word >> 29 & 1u)) atomicAdd(&cluster.map_shared_rank(&sh, 0)->failed, 1u);
-        if (!served) row_need[i] |= 1u << 30;
-        a.row_start[r + 1] = int32_t(min(end, (unsigned long long)(a.T)));
-        if (r == 0) a.row_start[0] = 0;
+        if (!served && !(word & kRefused)) atomicAdd(&of(&sh, 0)->failed, 1u);
+        if (!served) row_need[i] = word | kUnserved;
+        const int tok = int(min(end, (unsigned long long)(a.T)));
+        row_tok[i] = tok;
+        a.row_start[r0 + i + 1] = tok;
+        a.lens[r0 + i] = served ? have + add : -1;
     }
-    __syncthreads();
-    cluster.sync();
+    sync_all();
 
-    // 4. the free block of rank j goes to the row whose needed blocks hold j
-    for (int w = w0; w < w1 && rank < need_all; ++w) {
-        uint32_t bits = free_word(w);
-        while (bits && rank < need_all) {
-            const int b = __ffs(bits) - 1;
-            bits &= bits - 1;
-            const uint32_t j = rank++;
-            int c = 0;
+    // 4. the free block of rank j goes to the row whose needed blocks hold j: a warp per word, a lane per block
+    for (int w = warp; w < words_per; w += kPlanWarps) {
+        const uint32_t bits = free_word(w), j = twice_bits[w] + __popc(bits & lanemask_lt());
+        if (twice_bits[w] >= need_all) break;
+        if (!(bits >> lane & 1u) || j >= need_all) continue;
+        int c = 0;
+        uint32_t before = 0;
 #pragma unroll
-            for (int i = 0; i < CTAS - 1; ++i) c += need_ends[i] <= j;
-            uint32_t before = 0;
-#pragma unroll
-            for (int i = 0; i < CTAS - 1; ++i)
-                if (i < c) before = need_ends[i];
-            const uint32_t* ends = cluster.map_shared_rank(row_end, c);
-            int lo = 0, hi = min(a.R, (c + 1) * rows_per) - c * rows_per - 1;  // first row whose end is above j
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (before + ends[mid] > j) hi = mid;
-                else lo = mid + 1;
+        for (int i = 0; i < CTAS - 1; ++i)
+            if (need_ends[i] <= j) {
+                c = i + 1;
+                before = need_ends[i];
             }
-            const int r = c * rows_per + lo;
-            const uint32_t word = cluster.map_shared_rank(row_need, c)[lo];
-            if (word >> 30 & 1u) continue;  // not served
-            const uint32_t need = word & 0x1fffffffu;
-            const int used = int((int64_t(a.have[r]) + S - 1) / S) - int(word >> 31);
-            a.table[int64_t(r) * a.max_blocks + used + int(j - (before + ends[lo] - need))] =
-                int32_t(int64_t(me) * pages_per + int64_t(w) * 32 + b);
+        const uint32_t* ends = of(row_end, c);
+        int lo = 0, hi = min(a.R, (c + 1) * rows_per) - c * rows_per - 1;  // first row whose end is above j
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (before + ends[mid] > j) hi = mid;
+            else lo = mid + 1;
         }
+        const uint32_t word = of(row_need, c)[lo];
+        if (word & kUnserved) continue;
+        const int used = int((int64_t(of(row_have, c)[lo]) + S - 1) >> shift) - (of(row_tail, c)[lo] >= 0);
+        a.table[int64_t(c * rows_per + lo) * width + used + int(j - (before + ends[lo] - (word & kNeed)))] =
+            int32_t(int64_t(me) * pages_per + int64_t(w) * 32 + lane);
     }
-    __syncthreads();
-    cluster.sync();
+    sync_all();
 
-    // 5. slots, a warp per row
-    for (int r = r0 + warp; r < r1; r += kPlanWarps) {
-        const int64_t start = __ldcg(a.row_start + r), end = __ldcg(a.row_start + r + 1);
-        const bool served = !(row_need[r - r0] >> 30 & 1u);
-        const int have = a.have[r], into = have % S;
-        const int32_t tail = row_tail[r - r0];
-        const int64_t n = !served || all_slots ? end - start : into ? min(end - start, int64_t(S - into)) : 0;
-        const int32_t* row = a.table + int64_t(r) * a.max_blocks;
-        for (int64_t i = lane; i < n; i += 32) {
+    // 5. slots: rows of a few tokens have eight lanes each
+    const int per_row = all_slots ? 8 : 32;
+    for (int i0 = warp * (32 / per_row); i0 < rows; i0 += kPlanWarps * (32 / per_row)) {
+        const int i = i0 + lane / per_row;
+        if (i >= rows) continue;
+        const int start = i > 0 ? row_tok[i - 1] : int(min(tok_before, (unsigned long long)(a.T))), end = row_tok[i];
+        const bool served = !(row_need[i] & kUnserved);
+        const int have = row_have[i], into = have & (S - 1);
+        const int32_t tail = row_tail[i];
+        const int n = !served || all_slots ? end - start : into ? min(end - start, S - into) : 0;
+        const int32_t* row = a.table + int64_t(r0 + i) * width;
+        for (int k = lane % per_row; k < n; k += per_row) {
             int64_t slot = -1;
             int32_t src = -1;
             if (served) {
-                const int p = have + int(i), c = p / S;
+                const int p = have + k, c = p >> shift;
                 src = __ldcg(row + c);
-                slot = int64_t(src) * S + (p - c * S);
-                if (c == have / S && tail >= 0) src = tail;
+                slot = (int64_t(src) << shift) + (p & (S - 1));
+                if (c == have >> shift && tail >= 0) src = tail;
             }
-            a.slots[start + i] = slot;
-            a.sources[start + i] = src;
+            a.slots[start + k] = slot;
+            a.sources[start + k] = src;
         }
     }
     if (all_slots)  // behind the last row's tokens
@@ -286,7 +302,7 @@ __global__ void __launch_bounds__(kPlanBlock) kv_plan_kernel(PlanArgs a, int row
         a.report[2] = int32_t(sh.failed);
         a.report[3] = int32_t(sh.refused);
     }
-    cluster.sync();  // the CTAs' shared memory stays until all are done with it
+    if (CTAS > 1) cluster.sync();  // the CTAs' shared memory stays until all are done with it
 }
 
 // The slots of rows that get many tokens: each warp walks a stretch of tokens,
@@ -360,14 +376,14 @@ static cudaError_t launch_plan(const PlanArgs& a, bool all_slots, cudaStream_t s
 {
     const int rows_per = (a.R + CTAS - 1) / CTAS;
     const int words_per = ((a.num_blocks + 31) / 32 + CTAS - 1) / CTAS;
-    // the largest: 2 x 16384 words and 3 x 4096 rows
+    // the largest: 2 x 16384 words and 5 x 4096 rows
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kv_plan_kernel<CTAS>),
-                                     (2 * (ST_KV_MAX_BLOCKS / 32 / kPlanCtas) + 3 * (ST_KV_MAX_ROWS / kPlanCtas)) * 4);
+                                     (2 * (ST_KV_MAX_BLOCKS / 32 / kPlanCtas) + 5 * (ST_KV_MAX_ROWS / kPlanCtas)) * 4);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(CTAS);
     cfg.blockDim = dim3(kPlanBlock);
-    cfg.dynamicSmemBytes = size_t(2 * words_per + 3 * rows_per) * 4;
+    cfg.dynamicSmemBytes = size_t(2 * words_per + 5 * rows_per) * 4;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;

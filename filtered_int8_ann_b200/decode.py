@@ -47,13 +47,38 @@ def _array(x: torch.Tensor, dtype, shape, name: str) -> int:
     return x.data_ptr()
 
 
-def _empty(shape, dtype, device, stream):
-    """A new tensor, in the allocator's books of the stream that will use it."""
+try:  # torch.empty on the current device with its cost halved (what torch's own generated code calls)
+    from torch._C._dynamo.guards import _empty_strided_cuda
+except ImportError:
+    def _empty_strided_cuda(shape, strides, dtype):
+        return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
+
+
+def _empty(shape, dtype, stream):
+    """A new tensor on the current device, in the allocator's books of the stream that will use it."""
+    shape, strides, n = tuple(shape), [], 1
+    for size in shape[::-1]:
+        strides.append(n)
+        n *= size or 1
+    strides = tuple(strides[::-1])
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _empty_strided_cuda(shape, strides, dtype)
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
     with torch.cuda.stream(s):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _empty_strided_cuda(shape, strides, dtype)
+
+
+def _on_gpu(x: torch.Tensor, name: str):
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be on the current CUDA device")
+
+
+def _empty1(n, dtype, stream):
+    return _empty_strided_cuda((n,), (1,), dtype) if stream is None else _empty((n,), dtype, stream)
+
+
+def _empty2(n, m, dtype, stream):
+    return _empty_strided_cuda((n, m), (m, 1), dtype) if stream is None else _empty((n, m), dtype, stream)
 
 
 @functools.lru_cache(maxsize=256)
@@ -137,19 +162,20 @@ def st_kv_plan(table: torch.Tensor, have: torch.Tensor, add: torch.Tensor, num_b
     if table.dim() != 2:
         raise ValueError("table must be [R, max_blocks]")
     R, width = table.shape
-    dev, i32 = table.device, torch.int32
+    i32 = torch.int32
+    pt, ph, pa = _array(table, i32, (R, width), "table"), _array(have, i32, (R,), "have"), _array(add, i32, (R,), "add")
+    _on_gpu(table, "table")
     if slots is None:
-        slots = _empty((T,), torch.int64, dev, stream)
+        slots = _empty1(T, torch.int64, stream)
     if sources is None:
-        sources = _empty((T,), i32, dev, stream)
+        sources = _empty1(T, i32, stream)
     if row_start is None:
-        row_start = _empty((R + 1,), i32, dev, stream)
+        row_start = _empty1(R + 1, i32, stream)
     if lens is None:
-        lens = _empty((R,), i32, dev, stream)
+        lens = _empty1(R, i32, stream)
     if report is None:
-        report = _empty((4,), i32, dev, stream)
-    _check(lib().st_kv_plan(_array(table, i32, (R, width), "table"), _array(have, i32, (R,), "have"),
-                            _array(add, i32, (R,), "add"), R, width, num_blocks, block_size, T,
+        report = _empty1(4, i32, stream)
+    _check(lib().st_kv_plan(pt, ph, pa, R, width, num_blocks, block_size, T,
                             _array(slots, torch.int64, (T,), "slots"), _array(sources, i32, (T,), "sources"),
                             _array(row_start, i32, (R + 1,), "row_start"), _array(lens, i32, (R,), "lens"),
                             _array(report, i32, (4,), "report"), _stream(stream)), "st_kv_plan")
@@ -188,8 +214,11 @@ def st_kv_attend(cache: KvCache, q: torch.Tensor, table: torch.Tensor, row_start
     R, width = table.shape
     if max_len is None:
         max_len = width * c.block_size
+    pt = _array(table, torch.int32, (R, width), "table")
+    ps, pl = _array(row_start, torch.int32, (R + 1,), "row_start"), _array(lens, torch.int32, (R,), "lens")
     if out is None:
-        out = _empty(q.shape, q.dtype, q.device, stream)
+        _on_gpu(q, "q")
+        out = _empty(q.shape, q.dtype, stream)
         po, ot, oh = out.data_ptr(), heads * dim, dim
     else:
         _need(out.shape == q.shape and out.dtype == q.dtype, "out must be like q")
@@ -202,11 +231,8 @@ def st_kv_attend(cache: KvCache, q: torch.Tensor, table: torch.Tensor, row_start
     if workspace is not None:
         room = workspace.numel() * workspace.element_size()
     elif need:
-        workspace, room = _empty((need,), torch.uint8, q.device, stream), need
-    _check(lib().st_kv_attend(ctypes.byref(c), pq, _DTYPES[q.dtype], T, heads, qt, qh,
-                              _array(table, torch.int32, (R, width), "table"), width,
-                              _array(row_start, torch.int32, (R + 1,), "row_start"),
-                              _array(lens, torch.int32, (R,), "lens"), R, max_q, max_len,
+        workspace, room = _empty1(need, torch.uint8, stream), need
+    _check(lib().st_kv_attend(ctypes.byref(c), pq, _DTYPES[q.dtype], T, heads, qt, qh, pt, width, ps, pl, R, max_q, max_len,
                               dim ** -0.5 if scale is None else scale, int(causal), po, ot, oh,
                               None if workspace is None else workspace.data_ptr(), room, _stream(stream)),
            "st_kv_attend")
@@ -232,7 +258,7 @@ def st_beam_select(logits: torch.Tensor, scores: torch.Tensor, keep: int, allow:
     stride = beam if K > 1 else request if B > 1 else V
     if B > 1 and K > 1 and request != K * stride:
         raise ValueError("logits' beams must be evenly spaced")
-    dev = logits.device
+    pscores = _array(scores, torch.float32, (B, K), "scores")
     ex = out_finished = None
     if allow is not None or finished is not None:
         ex = _BeamExtras()
@@ -242,19 +268,21 @@ def st_beam_select(logits: torch.Tensor, scores: torch.Tensor, keep: int, allow:
             _need(allow.shape[2] <= 1 or allow.stride(2) == 1, "allow must have dense words")
             ex.allow, ex.allow_request_stride, ex.allow_beam_stride = allow.data_ptr(), allow.stride(0), allow.stride(1)
         if finished is not None:
-            out_finished = _empty((B, keep), torch.bool, dev, stream)
-            ex.finished, ex.out_finished = _array(finished, torch.bool, (B, K), "finished"), out_finished.data_ptr()
+            pf = _array(finished, torch.bool, (B, K), "finished")
+            _on_gpu(finished, "finished")
+            out_finished = _empty2(B, keep, torch.bool, stream)
+            ex.finished, ex.out_finished = pf, out_finished.data_ptr()
             ex.end_token = end_token
+    _on_gpu(logits, "logits")
     need = _select_workspace(B, K, V, keep)
-    out_scores = _empty((B, keep), torch.float32, dev, stream)
-    out_parents, out_tokens = _empty((B, keep), torch.int32, dev, stream), _empty((B, keep), torch.int32, dev, stream)
+    out_scores = _empty2(B, keep, torch.float32, stream)
+    out_parents, out_tokens = _empty2(B, keep, torch.int32, stream), _empty2(B, keep, torch.int32, stream)
     room = 0
     if workspace is not None:
         room = workspace.numel() * workspace.element_size()
     elif need:
-        workspace, room = _empty((need,), torch.uint8, dev, stream), need
-    _check(lib().st_beam_select(logits.data_ptr(), kind, stride, _array(scores, torch.float32, (B, K), "scores"),
-                                B, K, V, keep, out_scores.data_ptr(), out_parents.data_ptr(), out_tokens.data_ptr(),
+        workspace, room = _empty1(need, torch.uint8, stream), need
+    _check(lib().st_beam_select(logits.data_ptr(), kind, stride, pscores, B, K, V, keep, out_scores.data_ptr(), out_parents.data_ptr(), out_tokens.data_ptr(),
                                 None if ex is None else ctypes.byref(ex),
                                 None if workspace is None else workspace.data_ptr(), room, _stream(stream)),
            "st_beam_select")
@@ -287,6 +315,7 @@ def st_beam_reorder(states: Sequence[torch.Tensor], parents: torch.Tensor, out: 
         raise ValueError("parents must be [B, keep], beam_dim 1 or 2, and states not empty")
     B, keep = parents.shape
     K = states[0].shape[beam_dim] if states[0].dim() > beam_dim else -1
+    pp = _array(parents, torch.int32, (B, keep), "parents")
     made = []
     table = (_BeamState * len(states))()
     for i, x in enumerate(states):
@@ -294,16 +323,20 @@ def st_beam_reorder(states: Sequence[torch.Tensor], parents: torch.Tensor, out: 
         if len(shape) <= beam_dim or shape[beam_dim - 1] != B or shape[beam_dim] != K:
             raise ValueError(f"state {i} must have {B} requests of {K} beams at dimension {beam_dim}")
         new = shape[:beam_dim] + (keep,) + shape[beam_dim + 1:]
-        y = _empty(new, x.dtype, x.device, stream) if out is None else out[i]
+        step = _rows(x, beam_dim, f"state {i}")
+        if out is None:
+            _on_gpu(x, f"state {i}")
+            y = _empty(new, x.dtype, stream)
+        else:
+            y = out[i]
         if out is not None and (y.shape != new or y.dtype != x.dtype):
             raise ValueError(f"out {i} must be {tuple(new)} {x.dtype}")
         size = x.element_size()
         layers = (shape[0], size * x.stride(0), size * y.stride(0)) if beam_dim == 2 else (1, 0, 0)
-        table[i] = (x.data_ptr(), y.data_ptr(), size * math.prod(shape[beam_dim + 1:]), size * _rows(x, beam_dim, f"state {i}"),
+        table[i] = (x.data_ptr(), y.data_ptr(), size * math.prod(shape[beam_dim + 1:]), size * step,
                     size * _rows(y, beam_dim, f"out {i}"), *layers)
         made.append(y)
-    _check(lib().st_beam_reorder(table, len(states), _array(parents, torch.int32, (B, keep), "parents"), B, K, keep,
-                                 _stream(stream)), "st_beam_reorder")
+    _check(lib().st_beam_reorder(table, len(states), pp, B, K, keep, _stream(stream)), "st_beam_reorder")
     return made
 
 

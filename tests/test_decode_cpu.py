@@ -137,9 +137,23 @@ def test_binding_refuses_wrong_tensors():
 
 
 def test_binding_refuses_host_tensors():
-    """Tensors that are not on the current device: refused by the library (or, without a GPU, by CUDA)."""
-    logits, scores = torch.zeros(2, 3, 50), torch.zeros(2, 3)
-    with pytest.raises(st.StError):
+    """Well-formed tensors of the host."""
+    z = torch.zeros
+    i32 = torch.int32
+    logits, scores = z(2, 3, 50), z(2, 3)
+    with pytest.raises(ValueError, match="CUDA device"):
         st.st_beam_select(logits, scores, 4)
+    with pytest.raises(ValueError, match="CUDA device"):
+        st.st_beam_reorder([logits], z(2, 3, dtype=i32))
+    with pytest.raises(ValueError, match="CUDA device"):
+        st.st_kv_plan(z(2, 4, dtype=i32), z(2, dtype=i32), z(2, dtype=i32), 8, 16, 3)
+    k, sc = z(4, 2, 16, 64, dtype=torch.int8), z(4, 2)
+    c = st.KvCache(k, k.clone(), sc, sc.clone())
+    x = z(3, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA device"):
+        st.st_kv_attend(c, x, z(2, 4, dtype=i32), z(3, dtype=i32), z(2, dtype=i32), 1)
+    # with every array given, the library refuses them (or, without a GPU, CUDA does)
     with pytest.raises(st.StError):
-        st.st_beam_reorder([logits], torch.zeros(2, 3, dtype=torch.int32))
+        st.st_beam_reorder([logits], z(2, 3, dtype=i32), out=[z(2, 3, 50)])
+    with pytest.raises(st.StError):
+        st.st_kv_append(c, x, x, z(3, dtype=torch.int64))

@@ -31,13 +31,16 @@ constexpr int kDecWarps = 4;
 constexpr int kDecBlock = 32 * kDecWarps;
 constexpr int kDecMaxCols = 32;            // columns (query tokens x heads per cache head) up to which this kernel is taken
 constexpr int kDecGroup = 32;             // tokens a warp takes at a time
+constexpr int kDecSixteens = 4096 / 16 + 2 * kDecWarps * kDecGroup / 16;  // of the longest stretch, and of the stages copied past it
 constexpr int kDecMaxStretch = 4096;      // tokens
-constexpr int kDecMaxBlocks = kDecMaxStretch / 16;
+
 
 template <int D, int NT>
 struct DecShared {
-    int32_t page[kDecMaxBlocks];
-    float ks[kDecMaxBlocks], vs[kDecMaxBlocks];
+    // of each 16 tokens of the stretch: where their codes begin (-1: none), their block's K scale, its V scale over
+    // the largest of the stretch
+    int64_t at[kDecSixteens];
+    float ks[kDecSixteens], vs[kDecSixteens];
     float m[kDecWarps][8 * NT], l[kDecWarps][8 * NT];
     union {
         alignas(128) uint8_t codes[kDecWarps][2][2][kDecGroup * D];  // per warp: two stages of K and V codes
@@ -95,7 +98,8 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
     DecShared<D, NT>& sh = *reinterpret_cast<DecShared<D, NT>*>(raw);
     __shared__ float s_vmax[kDecWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    const int hk = blockIdx.y, unit = blockIdx.x / splits, split = blockIdx.x - unit * splits;
+    // the cache heads of one stretch run together: their codes lie side by side in each block
+    const int hk = blockIdx.x % a.c.kv_heads, part_id = blockIdx.x / a.c.kv_heads, unit = part_id / splits, split = part_id - unit * splits;
     const int row = unit / col_blocks, col0 = (unit - row * col_blocks) * COLS;
     const int G = a.q_heads / a.c.kv_heads, S = a.c.block_size;
 
@@ -115,21 +119,55 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
     if (j0 >= len && split > 0) return;  // the join knows how many stretches a row has
     const int tokens = int(min(int64_t(stretch), len - j0));
 
-    // blocks of the stretch and their scales
-    const int shift = 31 - __clz(S), pages = (tokens + S - 1) >> shift;
+    // the stretch's tokens in sixteens, and as many more as stages are copied ahead
+    const int shift = 31 - __clz(S), sixteens = (tokens + 15) / 16;
     const int32_t* table = a.table + int64_t(row) * a.max_blocks + (j0 >> shift);
-    float vmax = 0.f;
-    for (int i = tid; i < pages; i += kDecBlock) {
-        int p = table[i];
-        if (p < 0 || p >= a.c.num_blocks) {
-            atomicOr(a.err, kDecErrTable);
-            p = -1;
+    for (int i = tid; i < sixteens + 2 * kDecWarps * kDecGroup / 16; i += kDecBlock) {
+        int p = -1;
+        if (i < sixteens) {
+            p = table[(16 * i) >> shift];
+            if (p < 0 || p >= a.c.num_blocks) {
+                atomicOr(a.err, kDecErrTable);
+                p = -1;
+            }
         }
-        const int64_t at = int64_t(p) * a.c.kv_heads + hk;
-        sh.page[i] = p;
-        sh.ks[i] = p < 0 ? 0.f : a.c.k_scale[at];
-        sh.vs[i] = p < 0 ? 0.f : a.c.v_scale[at];
-        vmax = fmaxf(vmax, fabsf(sh.vs[i]));
+        sh.at[i] = p < 0 ? -1 : ((int64_t(p) * a.c.kv_heads + hk) * S + ((16 * i) & (S - 1))) * D;
+    }
+    __syncthreads();
+    // Codes of the 32 tokens of sixteens i and i + 1 into stage `st`: each sixteen is one run of bytes.
+    uint8_t* codes = sh.codes[warp][0][0];
+    const uint32_t codes_at = smem_u32(codes);
+    constexpr int kStage = 2 * kDecGroup * D, kHalf = 16 * D, kCopies = kHalf / 512;
+    constexpr int kLaneRows = 512 / D;  // tokens that a warp's copy covers
+    uint32_t dst[2];  // of copies with even and odd numbers
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        dst[i] = codes_at + piece_at<D>(i * kLaneRows + lane / (D / 16), lane % (D / 16)) - i * 512;
+    const int8_t *const from_k = a.c.k + lane * 16, *const from_v = a.c.v + lane * 16;
+    auto copy_stage = [&](int i16, int st) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t at = sh.at[i16 + h];
+            if (at >= 0) {
+                const int8_t *k = from_k + at, *v = from_v + at;
+                const uint32_t to = uint32_t(st * kStage + h * kHalf);
+#pragma unroll
+                for (int i = 0; i < kCopies; ++i) {
+                    copy_async(dst[i & 1] + to + i * 512, k + i * 512);
+                    copy_async(dst[i & 1] + to + kDecGroup * D + i * 512, v + i * 512);
+                }
+            }
+        }
+        cp_async_commit();
+    };
+    copy_stage(warp * (kDecGroup / 16), 0);  // on its way while scales and queries come
+    float vmax = 0.f;
+    for (int i = tid; i < sixteens; i += kDecBlock) {
+        const int64_t at = sh.at[i], block = at >> (shift + (D == 128 ? 7 : 6));
+        sh.ks[i] = at < 0 ? 0.f : a.c.k_scale[block];
+        const float vs = at < 0 ? 0.f : a.c.v_scale[block];
+        sh.vs[i] = vs;
+        vmax = fmaxf(vmax, vs);
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
@@ -165,13 +203,14 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
         const unsigned ok = __ballot_sync(0xffffffffu, finite) >> (lane & 28) & 15u;
-        const float down = ok == 15u ? pow2_down(big) : 0.f, up = ok == 15u ? pow2_up(big) : NAN;
+        // a negative scale's sign goes to the query: scores are then multiplied by positive numbers
+        const float down = ok == 15u ? copysignf(pow2_down(big), a.scale_log2) : 0.f, up = ok == 15u ? pow2_up(big) : NAN;
 #pragma unroll
         for (int v = 0; v < KV; ++v)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 q[nt][v][i] = ok == 15u ? pack_half2(x[16 * v + 2 * i] * down, x[16 * v + 2 * i + 1] * down) : 0u;
-        own_mult[nt] = a.scale_log2 * up;
+        own_mult[nt] = fabsf(a.scale_log2) * up;
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -185,10 +224,15 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
             seen[nt][i] = 8 * nt + c < cols ? int(max(int64_t(0), min(int64_t(tokens), see))) : 0;
         }
     __syncthreads();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may come up meanwhile
     float vtop = s_vmax[0];
 #pragma unroll
     for (int w = 1; w < kDecWarps; ++w) vtop = fmaxf(vtop, s_vmax[w]);
-    const float vinv = vtop > 0.f ? 1.f / vtop : 0.f;
+    {
+        const float vinv = vtop > 0.f ? 1.f / vtop : 0.f;
+        for (int i = tid; i < sixteens; i += kDecBlock) sh.vs[i] *= vinv;
+    }
+    __syncthreads();
     int least_seen = 0x7fffffff;  // of the whole warp's columns: tiles below it need no mask
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -207,43 +251,14 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
         for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
     }
 
-    // Codes of 32 tokens from jj0 on into stage `st`: 16 tokens lie in one block and are one run of bytes.
-    const int64_t head_bytes = int64_t(S) * D;
-    uint8_t* codes = sh.codes[warp][0][0];
-    const uint32_t codes_at = smem_u32(codes);
-    constexpr int kStage = 2 * kDecGroup * D, kHalf = 16 * D, kCopies = kHalf / 512;
-    constexpr int kLaneRows = 512 / D;  // tokens that a warp's copy covers
-    uint32_t dst[2];  // of copies with even and odd numbers
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        dst[i] = codes_at + piece_at<D>(i * kLaneRows + lane / (D / 16), lane % (D / 16)) - i * 512;
-    auto block_of = [&](int jj) { return jj < tokens ? sh.page[jj >> shift] : -1; };
-    auto copy_stage = [&](int jj0, int st) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int jj = jj0 + 16 * h, page = block_of(jj);
-            if (page >= 0) {
-                const int64_t at = (int64_t(page) * a.c.kv_heads + hk) * head_bytes + (jj & (S - 1)) * D + lane * 16;
-                const int8_t *k = a.c.k + at, *v = a.c.v + at;
-                const uint32_t to = uint32_t(st * kStage + h * kHalf);
-#pragma unroll
-                for (int i = 0; i < kCopies; ++i) {
-                    copy_async(dst[i & 1] + to + i * 512, k + i * 512);
-                    copy_async(dst[i & 1] + to + kDecGroup * D + i * 512, v + i * 512);
-                }
-            }
-        }
-        cp_async_commit();
-    };
     // lane (g, t)'s pieces: K pieces t (and t + 4) of tokens g, g + 8; V dims of tokens 2t, 2t+1 (and + 8)
     const int vdim = D == 128 ? (g >> 1 | (g & 1) << 2) * 16 : g * 8;  // first of the lane's D/8 dims of V
     const int k_at[2] = {piece_at<D>(g, t), D == 128 ? piece_at<D>(g, t + 4) : 0};
     const int v_at[2] = {kDecGroup * D + piece_at<D>(2 * t, vdim / 16) + vdim % 16,
                          kDecGroup * D + piece_at<D>(2 * t + 1, vdim / 16) + vdim % 16};
     int stage = 0;
-    copy_stage(warp * kDecGroup, 0);
     for (int jj0 = warp * kDecGroup; jj0 < tokens; jj0 += kDecWarps * kDecGroup, stage ^= 1) {
-        copy_stage(jj0 + kDecWarps * kDecGroup, stage ^ 1);
+        copy_stage(jj0 / 16 + kDecWarps * (kDecGroup / 16), stage ^ 1);
         cp_async_wait_group<1>();
         __syncwarp();
         const uint8_t* from = codes + stage * kStage;
@@ -267,9 +282,10 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
                 }
             }
         }
-        // scores, masked; the columns' maxima
-        float f[2];  // V factor of each half
+        // the columns' maxima; a sixteen's factor takes its products to scores
+        float f[2], sc[2][NT][2];
         float mx[NT][2];
+        const bool whole = jj0 + kDecGroup <= least_seen && sh.at[jj0 / 16] >= 0 && sh.at[jj0 / 16 + 1] >= 0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             mx[nt][0] = m[nt][0];
@@ -277,23 +293,34 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int jj = jj0 + 16 * h, page = block_of(jj);
-            const float ks = page >= 0 ? sh.ks[jj >> shift] : 0.f;
-            f[h] = page >= 0 ? sh.vs[jj >> shift] * vinv : 0.f;
-            const bool whole = page >= 0 && jj + 16 <= least_seen;
+            const float ks = sh.ks[jj0 / 16 + h];
+            f[h] = sh.vs[jj0 / 16 + h];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
+                sc[h][nt][0] = ks * mult[nt][0];
+                sc[h][nt][1] = ks * mult[nt][1];
+            }
+        }
+        if (!whole) {  // scores now, those that the column does not see masked
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    s[h][nt][i] *= ks * mult[nt][i & 1];
-                    if (!whole) {
-                        const bool sees = page >= 0 && jj + g + 8 * (i >> 1) < seen[nt][i & 1];
-                        s[h][nt][i] = sees ? s[h][nt][i] : -INFINITY;
-                    }
-                    mx[nt][i & 1] = fmaxf(mx[nt][i & 1], s[h][nt][i]);
+            for (int h = 0; h < 2; ++h) {
+                const int jj = jj0 + 16 * h;
+                const bool none = sh.at[jj / 16] < 0;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        s[h][nt][i] = !none && jj + g + 8 * (i >> 1) < seen[nt][i & 1] ? s[h][nt][i] * sc[h][nt][i & 1] : -INFINITY;
+                    sc[h][nt][0] = sc[h][nt][1] = 1.f;
                 }
             }
         }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) mx[nt][i] = fmaxf(mx[nt][i], fmaxf(s[h][nt][i], s[h][nt][2 + i]) * sc[h][nt][i]);
         bool grew = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -332,7 +359,7 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const float p0 = ex2(s[h][nt][2 * r] - b0), p1 = ex2(s[h][nt][2 * r + 1] - b1);
+                    const float p0 = ex2(fmaf(s[h][nt][2 * r], sc[h][nt][0], -b0)), p1 = ex2(fmaf(s[h][nt][2 * r + 1], sc[h][nt][1], -b1));
                     l[nt][0] += p0;
                     l[nt][1] += p1;
                     p[h][nt][r] = transpose8x8(pack_half2(p0 * f[h], p1 * f[h]));
@@ -418,15 +445,12 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
     }
 }
 
-// Join a query head's stretches: a few groups of D threads take every so many of them each.
-constexpr int kJoinBlock = 512;
-
-template <typename T, int D>
+// Join a query head's stretches: groups of D threads take every so many of them each.
+template <typename T, int D, int kJoinBlock>
 __global__ void __launch_bounds__(kJoinBlock) kv_join_kernel(AttendArgs a, int splits, int stretch)
 {
-    constexpr int GROUPS = kJoinBlock / D, kChunk = 512;
+    constexpr int GROUPS = kJoinBlock / D, kChunk = kJoinBlock;
     __shared__ float s_w[kChunk], s_red[kJoinBlock / 32], s_o[GROUPS][D];
-    dep_enter();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, d = tid % D, group = tid / D;
     const int64_t unit = blockIdx.x;
     const int64_t token = unit / a.q_heads, head = unit - token * a.q_heads;
@@ -445,6 +469,7 @@ __global__ void __launch_bounds__(kJoinBlock) kv_join_kernel(AttendArgs a, int s
     const float* po = static_cast<const float*>(a.workspace);
     const float* pm = po + a.T * a.q_heads * splits * D + 2 * unit * splits;
     po += unit * splits * D + d;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // what the stretches' launch wrote is read from here on
     float top = -INFINITY;
     for (int i = tid; i < used; i += kJoinBlock) top = fmaxf(top, pm[2 * i]);
 #pragma unroll
@@ -528,26 +553,30 @@ static cudaError_t launch_decode(const AttendArgs& a, const DecPlan& p, cudaStre
     const int bytes = int(sizeof(DecShared<D, NT>));
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kv_decode_kernel<T, D, NT>), bytes);
     if (e != cudaSuccess) return e;
-    const int64_t ctas = int64_t(a.R) * p.col_blocks * p.splits;
+    const int64_t ctas = int64_t(a.R) * p.col_blocks * p.splits * a.c.kv_heads;
     if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    const dim3 grid(unsigned(ctas), unsigned(a.c.kv_heads));
-    kv_decode_kernel<T, D, NT><<<grid, kDecBlock, bytes, s>>>(a, p.splits, p.stretch, p.col_blocks);
+    kv_decode_kernel<T, D, NT><<<unsigned(ctas), kDecBlock, bytes, s>>>(a, p.splits, p.stretch, p.col_blocks);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.splits == 1) return e;
     return launch_kv_join(a, p.splits, p.stretch, s);
+}
+
+template <typename T, int D>
+static cudaError_t launch_join(const AttendArgs& a, int splits, int stretch, cudaStream_t s)
+{
+    const dim3 grid{unsigned(a.T * a.q_heads)};
+    // few stretches are joined faster by small CTAs, many heads at a time
+    if (splits <= 16) return launch_dep(kv_join_kernel<T, D, 128>, grid, dim3(128), 0, s, a, splits, stretch);
+    return launch_dep(kv_join_kernel<T, D, 512>, grid, dim3(512), 0, s, a, splits, stretch);
 }
 
 cudaError_t launch_kv_join(const AttendArgs& a, int splits, int stretch, cudaStream_t s)
 {
     const int64_t units = a.T * a.q_heads;
     if (units > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    const dim3 grid{unsigned(units)}, block{kJoinBlock};
     const bool bf = a.dtype == ST_BF16;
-    if (a.c.head_dim == 128)
-        return bf ? launch_dep(kv_join_kernel<__nv_bfloat16, 128>, grid, block, 0, s, a, splits, stretch)
-                  : launch_dep(kv_join_kernel<__half, 128>, grid, block, 0, s, a, splits, stretch);
-    return bf ? launch_dep(kv_join_kernel<__nv_bfloat16, 64>, grid, block, 0, s, a, splits, stretch)
-              : launch_dep(kv_join_kernel<__half, 64>, grid, block, 0, s, a, splits, stretch);
+    if (a.c.head_dim == 128) return bf ? launch_join<__nv_bfloat16, 128>(a, splits, stretch, s) : launch_join<__half, 128>(a, splits, stretch, s);
+    return bf ? launch_join<__nv_bfloat16, 64>(a, splits, stretch, s) : launch_join<__half, 64>(a, splits, stretch, s);
 }
 
 static cudaError_t launch_kv_decode(const AttendArgs& a, cudaStream_t s)

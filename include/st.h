@@ -423,7 +423,7 @@ typedef enum { ST_BF16 = 0, ST_F16 = 1, ST_F32 = 2 } st_dtype;
  * with one scale per block and head: the key of head h of the token at offset
  * o of block b is k[b][h][o][:] * k_scale[b][h]. Caller-owned device arrays.
  * block_size is 16, 32, 64 or 128; head_dim 64 or 128; kv_heads 1 to 1024;
- * k and v 16-byte aligned. A token's slot is block * block_size + offset.
+ * k and v 16-byte aligned; scales are finite and not negative. A token's slot is block * block_size + offset.
  */
 typedef struct {
     int8_t* k;       /* [num_blocks][kv_heads][block_size][head_dim] */

@@ -2,8 +2,8 @@
 //   score(i, v) = scores[i] + x[i][v] - ln sum_u exp(x[i][u]),
 // ordered by score descending, then i * V + v ascending.
 //
-// Two launches. The first reads the logits once, a CTA per stretch of up to
-// 8192 of one beam's logits, which it holds in registers: their maximum, the
+// Two launches. The first reads the logits once, a CTA per stretch of one beam's logits, which pass
+// through its registers in chunks of 16 KB: their maximum, the
 // sum of exp(x - max), and the stretch's best entries. The second, a CTA per
 // request, forms the beams' normalisers and picks among the entries.
 //
@@ -26,8 +26,10 @@
 namespace st {
 
 constexpr int kSelThreads = 256;
-constexpr int kSelPerThread = 32;
-constexpr int kSelStretch = kSelThreads * kSelPerThread;
+constexpr int kSelVecs = 4;        // 16-byte vectors of a chunk per thread
+constexpr int kSelChunkBytes = kSelThreads * kSelVecs * 16;
+constexpr int kSelPlaces = 4 * 148; // CTAs of the first launch that the GPU holds
+constexpr int kListCap = 2048;     // entries that a stretch collects
 constexpr int kMergeThreads = 1024;
 constexpr int kMergeCap = 2048;   // pairs sorted at the end
 constexpr int kMergeRank = kMergeThreads / 4;  // up to this many are ordered by counting
@@ -94,8 +96,12 @@ struct Logit<float> {
     __device__ static uint32_t max2(uint32_t a, uint32_t b) { return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b))); }
     __device__ static float get(uint32_t w, int) { return __uint_as_float(w); }
     __device__ static uint32_t both(float x) { return __float_as_uint(x); }
-    // bits of the word's elements that are at least x
-    __device__ static uint32_t reach(uint32_t w, uint32_t x) { return __uint_as_float(w) >= __uint_as_float(x) ? 1u : 0u; }
+    // the bits of word k's elements that are at least x, and which element of which word a bit stands for
+    __device__ static uint32_t reach(uint32_t w, uint32_t x, int k) { return __uint_as_float(w) >= __uint_as_float(x) ? 1u << k : 0u; }
+    __device__ static int word_of(int bit) { return bit; }
+    __device__ static int part_of(int) { return 0; }
+    // the next value above
+    __device__ static uint32_t up(uint32_t w) { return w << 1 == 0 ? 1u : w >> 31 ? w - 1 : w + 1; }
     __device__ static uint32_t keep(uint32_t w, uint32_t bits) { return bits & 1u ? w : kNone; }
     __device__ static float one(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
     __device__ static uint32_t bits(const void* p, int64_t i) { return static_cast<const uint32_t*>(p)[i]; }
@@ -109,10 +115,13 @@ struct LogitHalf {
         const H2 m = __hmax2(as(a), as(b));
         return *reinterpret_cast<const uint32_t*>(&m);
     }
-    __device__ static uint32_t reach(uint32_t w, uint32_t x)
+    __device__ static uint32_t reach(uint32_t w, uint32_t x, int k) { return __hge2_mask(as(w), as(x)) & (0x10001u << k); }
+    __device__ static int word_of(int bit) { return bit & 15; }
+    __device__ static int part_of(int bit) { return bit >> 4; }
+    __device__ static uint32_t up(uint32_t w)
     {
-        const unsigned r = __hge2_mask(as(w), as(x));
-        return (r & 1u) | (r >> 30 & 2u);
+        const uint32_t h = w & 0xffffu, n = (h & 0x7fffu) == 0 ? 1u : h & 0x8000u ? h - 1 : h + 1;
+        return n | n << 16;
     }
     static __device__ uint32_t keep2(uint32_t w, uint32_t bits, uint32_t none)
     {
@@ -176,23 +185,108 @@ __device__ __forceinline__ void find_bin(const uint32_t* hist, uint32_t want, in
 // (written so that an infinite range, with inv = 0, keeps them).
 __device__ __forceinline__ float bin_scale(float range, int bins) { return range > 0.f ? fminf(float(bins - 1) / range, 3e38f) : 0.f; }
 
+// A value surely not above the far edge of histogram bin `bin` below m (every finite value when there is none,
+// or it is the last, which also holds what lies further down).
+__device__ __forceinline__ float edge_of(float m, float inv, int bin)
+{
+    if (bin < 0 || bin >= kHistBins - 1 || !(inv > 0.f)) return -FLT_MAX;
+    return fmaxf(-FLT_MAX, m - float(bin + 1) / inv * 1.00001f - fabsf(m) * 0x1p-20f);
+}
+
+// An entry's order as one number: the logit, then the lower index.
+__device__ __forceinline__ uint64_t entry_key(float x, uint32_t index) { return uint64_t(float_key(x)) << 32 | (0xffffffffu - index); }
+__device__ __forceinline__ float key_float(uint32_t key) { return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key); }
+
+// What a CTA of the first launch shares.
+struct StretchShared {
+    uint2 list[2][kListCap];  // entries (logit, token), in one of the two buffers
+    float max[kSelThreads / 32], min[kSelThreads / 32];
+    double sum[kSelThreads / 32];
+    uint32_t hist[kHistBins];
+    uint32_t count[4], total;  // entries found by chunk j: count[j % 4]
+    int bin, slow;
+};
+
+// The largest key with at least `keep` keys at or above it among the list's n and those that `more` gives to its
+// argument, by bisection. All threads of the CTA.
+template <bool MORE, typename F>
+__device__ uint64_t list_border(StretchShared& sh, const uint2* list, uint32_t n, uint32_t keep, F&& more)
+{
+    uint64_t border = 0;
+    for (int bit = 63; bit >= 0; --bit) {
+        const uint64_t mid = border | 1ull << bit;
+        uint32_t c = 0;
+        for (uint32_t k = threadIdx.x; k < n; k += kSelThreads) c += entry_key(__uint_as_float(list[k].x), list[k].y) >= mid;
+        if (MORE) more([&](uint64_t key) { c += key >= mid; });
+        c = __reduce_add_sync(0xffffffffu, c);
+        if ((threadIdx.x & 31) == 0 && c) atomicAdd(&sh.total, c);
+        __syncthreads();
+        const uint32_t total = sh.total;
+        __syncthreads();
+        if (threadIdx.x == 0) sh.total = 0;
+        __syncthreads();
+        if (total >= keep) border = mid;
+    }
+    return border;
+}
+
+// Narrow a list of n entries in buffer `buf` to those that can be among its best `keep`, by a histogram; they go to
+// the other buffer. False (and nothing done) when that cannot be told apart.
+__device__ bool list_trim(StretchShared& sh, int buf, uint32_t& n, uint32_t keep, float& edge, bool& above)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    float hi = -INFINITY, lo = INFINITY;
+    for (uint32_t k = tid; k < n; k += kSelThreads) {
+        const float y = __uint_as_float(sh.list[buf][k].x);
+        hi = fmaxf(hi, y);
+        lo = fminf(lo, y);
+    }
+    hi = warp_max(hi);
+    lo = warp_min(lo);
+    __syncthreads();
+    if (lane == 0) {
+        sh.max[warp] = hi;
+        sh.min[warp] = lo;
+    }
+    sh.hist[tid] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kSelThreads / 32; ++w) {
+        hi = fmaxf(hi, sh.max[w]);
+        lo = fminf(lo, sh.min[w]);
+    }
+    const float inv = bin_scale(hi - lo, kHistBins);
+    for (uint32_t k = tid; k < n; k += kSelThreads)
+        atomicAdd(&sh.hist[min(kHistBins - 1, int((hi - __uint_as_float(sh.list[buf][k].x)) * inv))], 1u);
+    __syncthreads();
+    find_bin<kHistBins>(sh.hist, keep, &sh.bin);
+    __syncthreads();
+    const float e = edge_of(hi, inv, sh.bin);
+    if (!(e > edge)) return false;  // the same in all threads
+    for (uint32_t k = tid; k < n; k += kSelThreads) {  // (the total is 0 between uses)
+        const uint2 w = sh.list[buf][k];
+        if (__uint_as_float(w.x) >= e) sh.list[buf ^ 1][atomicAdd(&sh.total, 1u)] = w;
+    }
+    edge = e;
+    above = false;
+    __syncthreads();
+    n = sh.total;
+    __syncthreads();
+    if (tid == 0) sh.total = 0;
+    __syncthreads();
+    return true;
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kSelThreads, 3)
-beam_stretch_kernel(SelectArgs a, int stretches, int cap, Stretch* res, uint2* lists)
+__global__ void __launch_bounds__(kSelThreads, 4)
+beam_stretch_kernel(SelectArgs a, int stretches, int chunks, int cap, Stretch* res, uint2* lists)
 {
     using L = Logit<T>;
-    constexpr int PER = L::kPer, IN = L::kIn, VECS = kSelPerThread / PER, WORDS = VECS * 4;
-    __shared__ float s_max[kSelThreads / 32], s_min[kSelThreads / 32];
-    __shared__ double s_sum[kSelThreads / 32];
-    __shared__ uint32_t s_hist[kHistBins];
-    __shared__ int s_bin;
-    __shared__ uint32_t s_count, s_total;
+    constexpr int PER = L::kPer, IN = L::kIn, VECS = kSelVecs, WORDS = VECS * 4, kSelChunk = kSelChunkBytes / int(sizeof(T));
+    __shared__ StretchShared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t row = blockIdx.y;
-    const int b = int(row / a.K), i = int(row - int64_t(b) * a.K);
-    const int64_t unit = row * stretches + blockIdx.x;
-    uint2* list = lists + unit * cap;
-
+    const int row = blockIdx.y;
+    const int64_t unit = int64_t(row) * stretches + blockIdx.x;
     const float base = a.scores[row];
     const bool finished = a.ex.finished && a.ex.finished[row];
     if (!(fabsf(base) < INFINITY) || finished) {  // no logit counts
@@ -200,127 +294,189 @@ beam_stretch_kernel(SelectArgs a, int stretches, int cap, Stretch* res, uint2* l
             Stretch s{0.0, -INFINITY, 0};
             if (finished && fabsf(base) < INFINITY && blockIdx.x == 0) {  // one candidate of logit 0 with normaliser 0
                 s = Stretch{1.0, 0.f, 1};
-                list[0] = make_uint2(__float_as_uint(0.f), uint32_t(a.ex.end_token));
+                lists[unit * cap] = make_uint2(__float_as_uint(0.f), uint32_t(a.ex.end_token));
             }
             res[unit] = s;
         }
         return;
     }
 
-    // Vectors of 16 aligned bytes; the first may begin before the row, the last end behind it.
+    // Vectors of 16 aligned bytes; the first may begin before the row, the last end behind it. Chunk j's first element is
+    // the row's element first + j kSelChunk.
     const T* x = static_cast<const T*>(a.logits) + row * a.stride;
     const int before = int((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
-    const int first = int(blockIdx.x) * kSelStretch - before;  // the row's index of the stretch's first element
-    const int live = min(kSelStretch, a.V - first);  // elements from there on
-    // the row's index of element u of this thread's word k
-    auto index_of = [&](int k, int u) { return first + ((k / 4) * kSelThreads + tid) * PER + (k % 4) * IN + u; };
-    uint32_t v[WORDS];
-#pragma unroll
-    for (int j = 0; j < VECS; ++j) {
-        const int e = first + (j * kSelThreads + tid) * PER;
-        if (e >= 0 && e + PER <= a.V) {
-            const uint4 w = __ldcs(reinterpret_cast<const uint4*>(x + e));
-            v[4 * j] = w.x;
-            v[4 * j + 1] = w.y;
-            v[4 * j + 2] = w.z;
-            v[4 * j + 3] = w.w;
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint32_t w = L::kNone;
-#pragma unroll
-                for (int u = 0; u < IN; ++u) {
-                    const int at = e + k * IN + u;
-                    if (at >= 0 && at < a.V) {
-                        if (IN == 1) w = L::bits(x, at);
-                        else w = (w & (u ? 0xffffu : 0xffff0000u)) | L::bits(x, at) << (16 * u);
-                    }
-                }
-                v[4 * j + k] = w;
-            }
-        }
-    }
+    const int first = int(blockIdx.x) * chunks * kSelChunk - before;
+    const uint32_t* allow = nullptr;
     if (a.ex.allow) {
-        const uint32_t* allow = a.ex.allow + b * a.ex.allow_request_stride + i * a.ex.allow_beam_stride;
-        const int words = (a.V + 31) / 32;
+        const int b = row / a.K;
+        allow = a.ex.allow + b * a.ex.allow_request_stride + (row - b * a.K) * a.ex.allow_beam_stride;
+    }
+    auto load = [&](int c, uint32_t(&v)[WORDS]) {
 #pragma unroll
         for (int j = 0; j < VECS; ++j) {
-            const int e = first + (j * kSelThreads + tid) * PER;
-            if (e + PER <= 0 || e >= a.V) continue;
-            const int at = e < 0 ? 0 : e;  // bits of elements at .. at + PER
-            const int w = int(at >> 5);
-            const uint32_t lo = allow[w], hi = w + 1 < words ? allow[w + 1] : 0u;
-            const uint32_t bits = __funnelshift_r(lo, hi, uint32_t(at & 31)) << uint32_t(at - e);
+            const int e = c + (j * kSelThreads + tid) * PER;
+            if (e >= 0 && e + PER <= a.V) {
+                const uint4 w = __ldcs(reinterpret_cast<const uint4*>(x + e));
+                v[4 * j] = w.x;
+                v[4 * j + 1] = w.y;
+                v[4 * j + 2] = w.z;
+                v[4 * j + 3] = w.w;
+            } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[4 * j + k] = L::keep(v[4 * j + k], bits >> (k * IN));
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t w = L::kNone;
+#pragma unroll
+                    for (int u = 0; u < IN; ++u) {
+                        const int at = e + k * IN + u;
+                        if (at >= 0 && at < a.V) {
+                            if (IN == 1) w = L::bits(x, at);
+                            else w = (w & (u ? 0xffffu : 0xffff0000u)) | L::bits(x, at) << (16 * u);
+                        }
+                    }
+                    v[4 * j + k] = w;
+                }
+            }
         }
+    };
+
+    if (tid < 4) sh.count[tid] = 0;
+    if (tid == 0) {
+        sh.total = 0;
+        sh.slow = 0;
     }
-    // The maximum (NaN takes no part). Where it is +inf, those entries leave and it is taken again.
-    s_hist[tid] = 0;
-    if (tid == 0) s_count = s_total = 0;
-    float tmax, m, least;
-    for (int pass = 0;; ++pass) {
+    __syncthreads();
+    const uint32_t keep = uint32_t(a.keep);
+    const double power = kPowers32.v[lane];
+    const int power_hi = __double2hiint(power), power_lo = __double2loint(power);
+    constexpr double kC = 46.166241308446828384;  // 32 / ln 2
+    constexpr double kMagic = 6755399441055744.0; // 1.5 * 2^52: adding it leaves the nearest integer in the low bits
+    constexpr double z = 0.0216608493924982908;   // ln 2 / 32
+    bool known = false;          // a reference for the exponentials: the maximum of the first chunk that has any
+    float ref = 0.f, most = -INFINITY;
+    double mc = 0.0, part[2] = {0.0, 0.0};
+    uint32_t floor2 = 0;
+    float edge = -FLT_MAX;       // entries from here up are candidates (`above`: only those above it)
+    bool above = false;
+    int buf = 0;
+    uint32_t count = 0, fetched = 0;  // entries in the list, and those whose logits have been read into it
+    auto fetch = [&]() {         // (an index is enough until then, and a load for each would be waited for)
+        for (uint32_t k = fetched + tid; k < count; k += kSelThreads) sh.list[buf][k].x = __float_as_uint(L::one(x, sh.list[buf][k].y));
+        fetched = count;
+        __syncthreads();
+    };
+
+    // Pass 0 goes through the chunks without waiting for one another's candidates. Where they are more than the list
+    // holds (equal logits, as a rule), pass 1 goes through them again, a chunk at a time.
+    uint32_t v[WORDS];
+    for (int pass = 0; pass < 2; ++pass) {
+    for (int j = 0; j < chunks; ++j) {
+        const int c0 = first + j * kSelChunk;
+        if (c0 >= a.V) break;
+        load(c0, v);
+        // the row's index of element u of this thread's word k
+        auto index_of = [&](int k, int u) { return c0 + ((k / 4) * kSelThreads + tid) * PER + (k % 4) * IN + u; };
+        if (allow) {
+            const int words = (a.V + 31) / 32;
+#pragma unroll
+            for (int i = 0; i < VECS; ++i) {
+                const int e = c0 + (i * kSelThreads + tid) * PER;
+                if (e + PER <= 0 || e >= a.V) continue;
+                const int at = e < 0 ? 0 : e;  // bits of elements at .. at + PER
+                const int w = at >> 5;
+                const uint32_t lo = allow[w], hi = w + 1 < words ? allow[w + 1] : 0u;
+                const uint32_t bits = __funnelshift_r(lo, hi, uint32_t(at & 31)) << uint32_t(at - e);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[4 * i + k] = L::keep(v[4 * i + k], bits >> (k * IN));
+            }
+        }
+        // this thread's maximum (NaN takes no part); +inf leaves
         uint32_t top = v[0];
 #pragma unroll
         for (int k = 1; k < WORDS; ++k) top = L::max2(top, v[k]);
-        tmax = IN == 1 ? L::get(top, 0) : fmaxf(L::get(top, 0), L::get(top, 1));
-        const float wm = warp_max(tmax), wl = warp_min(tmax > -INFINITY ? tmax : INFINITY);
-        if (lane == 0) {
-            s_max[warp] = wm;
-            s_min[warp] = wl;
-        }
-        __syncthreads();
-        m = s_max[0];
-        least = s_min[0];
+        float tmax = IN == 1 ? L::get(top, 0) : fmaxf(L::get(top, 0), L::get(top, 1));
+        if (tmax == INFINITY) {
+            tmax = -INFINITY;
 #pragma unroll
-        for (int w = 1; w < kSelThreads / 32; ++w) {
-            m = fmaxf(m, s_max[w]);
-            least = fminf(least, s_min[w]);
-        }
-        if (m < INFINITY || pass > 0) break;
+            for (int k = 0; k < WORDS; ++k) {
+                uint32_t on = 0;
 #pragma unroll
-        for (int k = 0; k < WORDS; ++k) {
-            uint32_t on = 0;
-#pragma unroll
-            for (int u = 0; u < IN; ++u) on |= (L::get(v[k], u) < INFINITY ? 1u : 0u) << u;
-            v[k] = L::keep(v[k], on);
+                for (int u = 0; u < IN; ++u) {
+                    const float y = L::get(v[k], u);
+                    on |= (y < INFINITY ? 1u : 0u) << u;
+                    if (y < INFINITY) tmax = fmaxf(tmax, y);
+                }
+                v[k] = L::keep(v[k], on);
+            }
         }
-        __syncthreads();
-    }
-    if (!(m > -INFINITY)) {  // nothing allowed here
-        if (tid == 0) res[unit] = Stretch{0.0, -INFINITY, 0};
-        return;
-    }
-
-    // sum of exp(x - m)
-    const double power = kPowers32.v[lane];
-    const int power_hi = __double2hiint(power), power_lo = __double2loint(power);
-    double sum = 0.0;
-    if (fabsf(m) > 0x1p20f) {  // m - 700 is not a number near m: rare, so the plain way
-#pragma unroll 1
-        for (int e = tid; e < live; e += kSelThreads) {
-            // (from memory again, so that the registers need no index; allowed ones among them)
-            const int at = first + e;
-            if (at < 0) continue;
-            bool on = true;
-            if (a.ex.allow) on = (a.ex.allow + b * a.ex.allow_request_stride + i * a.ex.allow_beam_stride)[at >> 5] >> (at & 31) & 1u;
-            const float y = L::one(x, at);
-            const double d = double(y) - double(m);
-            if (on && y < INFINITY && d >= -700.0) sum += exp(d);
-        }
-    } else {
-        constexpr double kC = 46.166241308446828384;  // 32 / ln 2
-        constexpr double kMagic = 6755399441055744.0; // 1.5 * 2^52: adding it leaves the nearest integer in the low bits
-        constexpr double z = 0.0216608493924982908;   // ln 2 / 32
-        const double mc = double(m) * -kC;
-        const uint32_t floor2 = L::both(m - 700.f);   // exp(-700) is nothing next to 1; takes the place of -inf and NaN
-        double part[2] = {0.0, 0.0};
+        most = fmaxf(most, tmax);
+        if (!known) {
+            sh.hist[tid] = 0;
+            const float wm = warp_max(tmax), wl = warp_min(tmax > -INFINITY ? tmax : INFINITY);
+            if (lane == 0) {
+                sh.max[warp] = wm;
+                sh.min[warp] = wl;
+            }
+            __syncthreads();
+            float m = sh.max[0], least = sh.min[0];
 #pragma unroll
-        for (int j = 0; j < VECS; ++j) {
-            if (j * kSelThreads * PER >= live) break;
+            for (int w = 1; w < kSelThreads / 32; ++w) {
+                m = fmaxf(m, sh.max[w]);
+                least = fminf(least, sh.min[w]);
+            }
+            if (!(m > -INFINITY)) {  // nothing allowed in this chunk
+                __syncthreads();
+                continue;
+            }
+            known = true;
+            ref = m;
+            mc = double(m) * -kC;
+            floor2 = L::both(m - 700.f);  // exp(-700) is nothing next to 1; takes the place of -inf and NaN
+            if (fabsf(m) > 0x1p20f && tid == 0) sh.slow = 1;  // m - 700 is not a number near m
+            // The edge: the chunk's threads' (or, for many, vectors') maxima in a histogram; the bin that `keep` of them
+            // reach bounds the chunk's keep-th logit from below.
+            const float inv = bin_scale(m - least, kHistBins);
+            if (keep <= kSelThreads / 2) {
+                if (tmax > -INFINITY) atomicAdd(&sh.hist[min(kHistBins - 1, int((m - tmax) * inv))], 1u);
+            } else {
+#pragma unroll
+                for (int i = 0; i < VECS; ++i) {
+                    const uint32_t w = L::max2(L::max2(v[4 * i], v[4 * i + 1]), L::max2(v[4 * i + 2], v[4 * i + 3]));
+                    const float y = IN == 1 ? L::get(w, 0) : fmaxf(L::get(w, 0), L::get(w, 1));
+                    if (y >= least) atomicAdd(&sh.hist[min(kHistBins - 1, int((m - y) * inv))], 1u);
+                }
+            }
+            __syncthreads();
+            find_bin<kHistBins>(sh.hist, keep, &sh.bin);
+            __syncthreads();
+            edge = edge_of(m, inv, sh.bin);
+        }
+        // candidates: their indexes go behind the list
+        const uint32_t old = count;
+        if (edge <= tmax) {  // (false where this thread has none)
+            const uint32_t e2 = L::both(edge);
+            // above the edge, which is an entry's value then; or from it on, a step further down where the type rounds it up
+            const uint32_t from = above ? L::up(e2) : L::get(e2, 0) <= edge ? e2 : L::both(edge - fabsf(edge) * 0.01f - FLT_MIN);
+            uint32_t found = 0;
+#pragma unroll
+            for (int k = 0; k < WORDS; ++k) found |= L::reach(v[k], from, k);
+            if (found) {
+                uint32_t at = old + atomicAdd(&sh.count[pass == 0 ? 0 : j & 3], uint32_t(__popc(found)));
+                while (found) {
+                    const int bit = __ffs(found) - 1;
+                    found &= found - 1;
+                    if (at < kListCap) sh.list[buf][at].y = uint32_t(index_of(L::word_of(bit), L::part_of(bit)));
+                    ++at;
+                }
+            }
+        }
+        // exp(x - ref)
+        if (tmax - ref > 600.f) sh.slow = 1;
+#pragma unroll
+        for (int i = 0; i < VECS; ++i) {
+            if (pass > 0 || i * kSelThreads * PER >= a.V - c0) break;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const uint32_t w = L::max2(v[4 * j + k], floor2);
+                const uint32_t w = L::max2(v[4 * i + k], floor2);
 #pragma unroll
                 for (int u = 0; u < IN; ++u) {
                     const double y = fma(double(L::get(w, u)), kC, mc);
@@ -334,95 +490,122 @@ beam_stretch_kernel(SelectArgs a, int stretches, int cap, Stretch* res, uint2* l
                 }
             }
         }
-        sum = part[0] + part[1];
-    }
+        if (pass == 0) continue;
+        __syncthreads();
+        count = old + sh.count[j & 3];
+        if (tid == 0) sh.count[(j + 2) & 3] = 0;  // read last two barriers ago
+        if (count > kListCap) {
+            // Too many: exactly the best `keep` of the list and this chunk's candidates (the logit's order first, then
+            // the lower index). Later entries that equal the last of them come behind it.
+            count = old;
+            fetch();
+            const uint64_t border = list_border<true>(sh, sh.list[buf], old, keep, [&](auto&& f) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (lane == 0) s_sum[warp] = sum;
-
-    // the edge below which at least `keep` maxima lie
-    const uint32_t keep = uint32_t(a.keep);
-    const float inv = bin_scale(m - least, kHistBins);
-    if (keep <= kSelThreads / 2) {  // a maximum per thread is enough to choose from
-        if (tmax > -INFINITY) atomicAdd(&s_hist[min(kHistBins - 1, int((m - tmax) * inv))], 1u);
-    } else {  // one per vector
+                for (int k = 0; k < WORDS; ++k)
 #pragma unroll
-        for (int j = 0; j < VECS; ++j) {
-            const uint32_t w = L::max2(L::max2(v[4 * j], v[4 * j + 1]), L::max2(v[4 * j + 2], v[4 * j + 3]));
-            const float y = IN == 1 ? L::get(w, 0) : fmaxf(L::get(w, 0), L::get(w, 1));
-            if (y >= least) atomicAdd(&s_hist[min(kHistBins - 1, int((m - y) * inv))], 1u);
-        }
-    }
-    __syncthreads();
-    find_bin<kHistBins>(s_hist, keep, &s_bin);
-    __syncthreads();
-    // Entries down to a value that is surely not above the edge. The last bin also holds what lies below `least`.
-    float edge = -FLT_MAX;
-    if (s_bin >= 0 && s_bin < kHistBins - 1 && inv > 0.f) edge = fmaxf(edge, m - float(s_bin + 1) / inv * 1.00001f - fabsf(m) * 0x1p-20f);
-    if (edge <= tmax) {  // (false where this thread has none: NaN or -inf)
-        const uint32_t e2 = L::both(edge);
-        // a value rounded up to the type would lose entries: one step down then
-        const uint32_t from = L::get(e2, 0) <= edge ? e2 : L::both(edge - fabsf(edge) * 0.01f - FLT_MIN);
-        uint32_t found = 0;
-#pragma unroll
-        for (int k = 0; k < WORDS; ++k) found |= L::reach(v[k], from) << (k * IN);
-        while (found) {
-            const int k = __ffs(found) - 1;
-            found &= found - 1;
-            const int e = index_of(k / IN, k % IN);
-            const uint32_t at = atomicAdd(&s_count, 1u);
-            if (at < uint32_t(cap)) list[at] = make_uint2(__float_as_uint(L::one(x, e)), uint32_t(e));
-        }
-    }
-    __syncthreads();
-    uint32_t count = s_count;
-    if (count > uint32_t(cap)) {
-        // Too many: the exact border, the largest key with at least `keep` keys at or above it
-        // (the logit's order first, then the lower index).
-        uint64_t border = 0;
-        for (int bit = 63; bit >= 0; --bit) {
-            const uint64_t mid = border | 1ull << bit;
-            uint32_t c = 0;
+                    for (int u = 0; u < IN; ++u) {
+                        const float y = L::get(v[k], u);
+                        if (y > -INFINITY && (above ? y > edge : y >= edge)) f(entry_key(y, uint32_t(index_of(k, u))));
+                    }
+            });
+            if (tid == 0) sh.total = 0;
+            __syncthreads();
+            auto take = [&](uint64_t key) {
+                if (key >= border) {
+                    const uint32_t at = atomicAdd(&sh.total, 1u);
+                    if (at < kListCap) sh.list[buf ^ 1][at] = make_uint2(__float_as_uint(key_float(uint32_t(key >> 32))), 0xffffffffu - uint32_t(key));
+                }
+            };
+            for (uint32_t k = tid; k < old; k += kSelThreads) take(entry_key(__uint_as_float(sh.list[buf][k].x), sh.list[buf][k].y));
 #pragma unroll
             for (int k = 0; k < WORDS; ++k)
 #pragma unroll
                 for (int u = 0; u < IN; ++u) {
                     const float y = L::get(v[k], u);
-                    const uint64_t key = uint64_t(float_key(y)) << 32 | (0xffffffffu - uint32_t(index_of(k, u)));
-                    c += y > -INFINITY && key >= mid;
+                    if (y > -INFINITY && (above ? y > edge : y >= edge)) take(entry_key(y, uint32_t(index_of(k, u))));
                 }
-            c = __reduce_add_sync(0xffffffffu, c);
-            if (lane == 0) atomicAdd(&s_total, c);
+            buf ^= 1;
+            edge = key_float(uint32_t(border >> 32));
+            above = true;
             __syncthreads();
-            const uint32_t total = s_total;
+            count = fetched = min(sh.total, uint32_t(kListCap));
             __syncthreads();
-            if (tid == 0) s_total = 0;
-            __syncthreads();
-            if (total >= keep) border = mid;
+            if (tid == 0) sh.total = 0;
+        } else if (count > kListCap / 2 && j + 1 < chunks) {
+            fetch();
+            if (list_trim(sh, buf, count, keep, edge, above)) buf ^= 1;
+            fetched = count;
         }
-        if (tid == 0) s_count = 0;
+    }
+    if (pass > 0) break;
+    __syncthreads();
+    count = sh.count[0];
+    if (count <= kListCap) break;
+    count = 0;
+    __syncthreads();
+    if (tid == 0) sh.count[0] = 0;
+    __syncthreads();
+    }
+    if (!known) {  // nothing allowed here
+        if (tid == 0) res[unit] = Stretch{0.0, -INFINITY, 0};
+        return;
+    }
+
+    // the sum, over the maximum
+    double sum = part[0] + part[1];
+    const float wm = warp_max(most);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (lane == 0) {
+        sh.max[warp] = wm;
+        sh.sum[warp] = sum;
+    }
+    __syncthreads();
+    float m = sh.max[0];
+#pragma unroll
+    for (int w = 1; w < kSelThreads / 32; ++w) m = fmaxf(m, sh.max[w]);
+    double total = 0.0;
+    if (sh.slow) {  // logits too far apart for one reference: once more from memory, the plain way
+        double s = 0.0;
+        const int end = min(a.V, first + chunks * kSelChunk);
+#pragma unroll 1
+        for (int e = max(first, 0) + tid; e < end; e += kSelThreads) {
+            const float y = L::one(x, e);
+            const double d = double(y) - double(m);
+            if ((!allow || (allow[e >> 5] >> (e & 31) & 1u)) && y < INFINITY && d >= -700.0) s += exp(d);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+        __syncthreads();
+        if (lane == 0) sh.sum[warp] = s;
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < WORDS; ++k)
+        for (int w = 0; w < kSelThreads / 32; ++w) total += sh.sum[w];
+    } else {
 #pragma unroll
-            for (int u = 0; u < IN; ++u) {
-                const float y = L::get(v[k], u);
-                const int e = index_of(k, u);
-                const uint64_t key = uint64_t(float_key(y)) << 32 | (0xffffffffu - uint32_t(e));
-                if (y > -INFINITY && key >= border) {
-                    const uint32_t at = atomicAdd(&s_count, 1u);
-                    if (at < uint32_t(cap)) list[at] = make_uint2(__float_as_uint(y), uint32_t(e));
-                }
+        for (int w = 0; w < kSelThreads / 32; ++w) total += sh.sum[w];
+        total *= exp(double(ref) - double(m));
+    }
+    // the entries: no more than a list holds
+    __syncthreads();
+    fetch();
+    if (count > uint32_t(cap) && list_trim(sh, buf, count, keep, edge, above)) buf ^= 1;
+    if (count > uint32_t(cap)) {
+        const uint64_t border = list_border<false>(sh, sh.list[buf], count, keep, [](auto&&) {});
+        for (uint32_t k = tid; k < count; k += kSelThreads) {
+            const uint2 w = sh.list[buf][k];
+            if (entry_key(__uint_as_float(w.x), w.y) >= border) {
+                const uint32_t at = atomicAdd(&sh.total, 1u);
+                if (at < uint32_t(cap)) sh.list[buf ^ 1][at] = w;
             }
+        }
+        buf ^= 1;
         __syncthreads();
-        count = min(s_count, uint32_t(cap));
+        count = min(sh.total, uint32_t(cap));
     }
-    if (tid == 0) {
-        double total = 0.0;
-#pragma unroll
-        for (int w = 0; w < kSelThreads / 32; ++w) total += s_sum[w];
-        res[unit] = Stretch{total, m, int32_t(count)};
-    }
+    uint2* list = lists + unit * cap;
+    for (uint32_t k = tid; k < count; k += kSelThreads) list[k] = sh.list[buf][k];
+    if (tid == 0) res[unit] = Stretch{total, m, int32_t(count)};
 }
 
 // The second launch keeps a request's pairs in shared memory.
@@ -739,25 +922,42 @@ beam_merge_kernel(SelectArgs a, int stretches, int cap, const Stretch* res, cons
     }
 }
 
-// A stretch begins at a 16-byte boundary, up to 7 elements before the row.
-static int select_stretches(int32_t V) { return (V + 7 + kSelStretch - 1) / kSelStretch; }
+// Chunks per stretch: as many as leave the GPU three CTAs per place (kSelPlaces), and their candidates (keep and a
+// few more each) the list's room, at most 16. A stretch begins at a 16-byte boundary, up to 7 elements before the row.
+static int select_chunks(int64_t rows, int32_t V, int32_t keep, int size)
+{
+    const int chunk = kSelChunkBytes / size;
+    const int64_t all = (V + 7 + chunk - 1) / chunk;
+    int64_t chunks = rows * all / (3 * kSelPlaces);
+    if (chunks > kListCap / 2 / keep) chunks = kListCap / 2 / keep;
+    return int(chunks < 1 ? 1 : chunks > 16 ? 16 : chunks > all ? all : chunks);
+}
+static int select_stretches(int64_t rows, int32_t V, int32_t keep, int size)
+{
+    const int64_t stretch = int64_t(select_chunks(rows, V, keep, size)) * (kSelChunkBytes / size);
+    return int((V + 7 + stretch - 1) / stretch);
+}
 // Entries a stretch may write: room for the bin that holds the border.
 static int select_cap(int32_t V, int32_t keep)
 {
-    const int most = V < kSelStretch ? V : kSelStretch;
-    return keep + 64 < most ? keep + 64 : most;
+    return keep + 64 < V ? keep + 64 : V;
 }
 
 int64_t beam_select_workspace(int32_t B, int32_t K, int32_t V, int32_t keep)
 {
-    const int64_t units = int64_t(B) * K * select_stretches(V);
+    // the type is not known here: the longest, whose stretches are the most
+    const int64_t rows = int64_t(B) * K;
+    const int two = select_stretches(rows, V, keep, 2), four = select_stretches(rows, V, keep, 4);
+    const int64_t units = rows * (two > four ? two : four);
     return units * int64_t(sizeof(Stretch)) + units * select_cap(V, keep) * 8;
 }
 
 cudaError_t launch_beam_select(const SelectArgs& a, cudaStream_t s)
 {
-    const int stretches = select_stretches(a.V), cap = select_cap(a.V, a.keep);
     const int64_t rows = int64_t(a.B) * a.K;
+    const int size = a.dtype == ST_F32 ? 4 : 2;
+    const int chunks = select_chunks(rows, a.V, a.keep, size), stretches = select_stretches(rows, a.V, a.keep, size);
+    const int cap = select_cap(a.V, a.keep);
     Stretch* res = static_cast<Stretch*>(a.workspace);
     uint2* lists = reinterpret_cast<uint2*>(res + rows * stretches);
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(beam_merge_kernel), int(sizeof(MergeShared)));
@@ -767,7 +967,6 @@ cudaError_t launch_beam_select(const SelectArgs& a, cudaStream_t s)
     for (int64_t r0 = 0; r0 < rows; r0 += step) {
         const dim3 grid(unsigned(stretches), unsigned(rows - r0 < step ? rows - r0 : step));
         SelectArgs p = a;
-        const int64_t size = a.dtype == ST_F32 ? 4 : 2;
         p.logits = static_cast<const char*>(a.logits) + r0 * a.stride * size;
         p.scores += r0;
         if (p.ex.finished) p.ex.finished += r0;
@@ -775,9 +974,9 @@ cudaError_t launch_beam_select(const SelectArgs& a, cudaStream_t s)
         Stretch* pr = res + r0 * stretches;
         uint2* pl = lists + r0 * stretches * cap;
         switch (a.dtype) {
-            case ST_BF16: beam_stretch_kernel<__nv_bfloat16><<<grid, kSelThreads, 0, s>>>(p, stretches, cap, pr, pl); break;
-            case ST_F16: beam_stretch_kernel<__half><<<grid, kSelThreads, 0, s>>>(p, stretches, cap, pr, pl); break;
-            default: beam_stretch_kernel<float><<<grid, kSelThreads, 0, s>>>(p, stretches, cap, pr, pl); break;
+            case ST_BF16: beam_stretch_kernel<__nv_bfloat16><<<grid, kSelThreads, 0, s>>>(p, stretches, chunks, cap, pr, pl); break;
+            case ST_F16: beam_stretch_kernel<__half><<<grid, kSelThreads, 0, s>>>(p, stretches, chunks, cap, pr, pl); break;
+            default: beam_stretch_kernel<float><<<grid, kSelThreads, 0, s>>>(p, stretches, chunks, cap, pr, pl); break;
         }
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;

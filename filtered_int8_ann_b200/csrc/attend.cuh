@@ -98,7 +98,8 @@ __device__ void zero_rows(const AttendArgs& a, int start, int n, int h0, int hea
 
 // kv_attend.cu: the join of partial results in the workspace, [T][q_heads][splits][D] sums and then
 // [T][q_heads][splits] {maximum, sum of weights}; kv_prefill.cu: many query tokens per row.
-cudaError_t launch_kv_join(const AttendArgs& a, int splits, int stretch, cudaStream_t s);
+// per_row: columns per row and cache head to join, or 0: every token's.
+cudaError_t launch_kv_join(const AttendArgs& a, int splits, int stretch, int per_row, cudaStream_t s);
 int64_t kv_prefill_workspace(const st_kv_cache& c, int64_t T, int32_t q_heads, int32_t R, int32_t max_q, int64_t max_len);
 cudaError_t launch_kv_prefill(const AttendArgs& a, cudaStream_t s);
 

@@ -66,6 +66,9 @@ struct AttendArgs {
     int64_t out_token, out_head;
     void* workspace;
     uint32_t* err;
+    // rows that a launch takes, by their columns (query tokens x heads per cache head): more than the first, up to
+    // the second
+    int32_t above_cols = 0, most_cols = 0x7fffffff;
 };
 int64_t kv_attend_workspace(const st_kv_cache& c, int64_t T, int32_t q_heads, int32_t R, int32_t max_q,
                             int64_t max_len);

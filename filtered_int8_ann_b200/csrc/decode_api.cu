@@ -2,6 +2,7 @@
 // and the device's decode error word.
 #include <cmath>
 #include <mutex>
+#include <new>
 
 #include "decode.cuh"
 
@@ -66,7 +67,28 @@ st_status to_status(cudaError_t e)
 {
     if (e == cudaSuccess) return ST_OK;
     cudaGetLastError();
+    if (e == cudaErrorInvalidConfiguration) return ST_ERR_UNSUPPORTED;  // more CTAs than a grid holds
     return e == cudaErrorMemoryAllocation ? ST_ERR_OOM : ST_ERR_CUDA;
+}
+
+// Do the byte ranges [p, p + n) and [q, q + m) share a byte?
+bool overlap(const void* p, int64_t n, const void* q, int64_t m)
+{
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return n > 0 && m > 0 && a < b + uintptr_t(m) && b < a + uintptr_t(n);
+}
+
+// No exception leaves the library: what the host side's containers and locks may throw becomes a status.
+template <typename F>
+st_status guarded(F&& f) noexcept
+{
+    try {
+        return f();
+    } catch (const std::bad_alloc&) {
+        return ST_ERR_OOM;
+    } catch (...) {
+        return ST_ERR_CUDA;
+    }
 }
 
 bool block_size_ok(int32_t s) { return s == 16 || s == 32 || s == 64 || s == 128; }
@@ -118,20 +140,31 @@ st_status st_kv_plan(int32_t* table, const int32_t* have, const int32_t* add, in
                      int32_t num_blocks, int32_t block_size, int64_t T, int64_t* slots, int32_t* sources,
                      int32_t* row_start, int32_t* lens, int32_t* report, cudaStream_t stream)
 {
-    if (R < 1 || max_blocks < 1 || num_blocks < 1 || T < 0 || !block_size_ok(block_size)) return ST_ERR_INVALID_ARG;
-    if (R > ST_KV_MAX_ROWS || num_blocks > ST_KV_MAX_BLOCKS || int64_t(R) * max_blocks >= kLimit31 || T >= kLimit31 - 1 ||
-        int64_t(max_blocks) * block_size >= kLimit31)
-        return ST_ERR_UNSUPPORTED;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return ST_ERR_CUDA;
-    if (!on_device(table, dev, 4) || !on_device(have, dev, 4) || !on_device(add, dev, 4) ||
-        !on_device(row_start, dev, 4) || !on_device(lens, dev, 4) || !on_device(report, dev, 4))
-        return ST_ERR_INVALID_ARG;
-    if (T > 0 && (!on_device(slots, dev, 8) || !on_device(sources, dev, 4))) return ST_ERR_INVALID_ARG;
-    st::PlanArgs a{table, have, add, R, max_blocks, num_blocks, block_size, T, slots, sources, row_start, lens, report, nullptr};
-    cudaError_t e = st::decode_error_address(&a.err);
-    if (e == cudaSuccess) e = st::launch_kv_plan(a, stream);
-    return to_status(e);
+    return guarded([&]() -> st_status {
+        if (R < 1 || max_blocks < 1 || num_blocks < 1 || T < 0 || !block_size_ok(block_size)) return ST_ERR_INVALID_ARG;
+        if (R > ST_KV_MAX_ROWS || num_blocks > ST_KV_MAX_BLOCKS || int64_t(R) * max_blocks >= kLimit31 || T >= kLimit31 - 1 ||
+            int64_t(max_blocks) * block_size >= kLimit31)
+            return ST_ERR_UNSUPPORTED;
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return ST_ERR_CUDA;
+        if (!on_device(table, dev, 4) || !on_device(have, dev, 4) || !on_device(add, dev, 4) ||
+            !on_device(row_start, dev, 4) || !on_device(lens, dev, 4) || !on_device(report, dev, 4))
+            return ST_ERR_INVALID_ARG;
+        if (T > 0 && (!on_device(slots, dev, 8) || !on_device(sources, dev, 4))) return ST_ERR_INVALID_ARG;
+        // a launch of two kernels reads the inputs while it writes the outputs
+        const struct {
+            const void* p;
+            int64_t bytes;
+        } part[] = {{table, int64_t(R) * max_blocks * 4}, {slots, T * 8}, {sources, T * 4}, {row_start, (int64_t(R) + 1) * 4},
+                    {lens, int64_t(R) * 4}, {report, 16}, {have, int64_t(R) * 4}, {add, int64_t(R) * 4}};
+        for (int i = 0; i < 6; ++i)
+            for (int j = i + 1; j < 8; ++j)
+                if (overlap(part[i].p, part[i].bytes, part[j].p, part[j].bytes)) return ST_ERR_INVALID_ARG;
+        st::PlanArgs a{table, have, add, R, max_blocks, num_blocks, block_size, T, slots, sources, row_start, lens, report, nullptr};
+        cudaError_t e = st::decode_error_address(&a.err);
+        if (e == cudaSuccess) e = st::launch_kv_plan(a, stream);
+        return to_status(e);
+    });
 }
 
 st_status st_kv_append(const st_kv_cache* cache, const void* k, const void* v, st_dtype dtype, int64_t T,
@@ -139,20 +172,22 @@ st_status st_kv_append(const st_kv_cache* cache, const void* k, const void* v, s
                        int64_t v_head_stride, const int64_t* slots, const int32_t* sources,
                        cudaStream_t stream)
 {
-    if (cache_sizes(cache) == ST_ERR_INVALID_ARG || T < 0 || (dtype != ST_BF16 && dtype != ST_F16) ||
-        !strides_ok(k_token_stride, k_head_stride) || !strides_ok(v_token_stride, v_head_stride))
-        return ST_ERR_INVALID_ARG;
-    if (cache_sizes(cache) != ST_OK || T >= kLimit31) return ST_ERR_UNSUPPORTED;
-    if (T == 0) return ST_OK;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return ST_ERR_CUDA;
-    if (!cache_arrays(cache, dev) || !on_device(k, dev, 16) || !on_device(v, dev, 16) || !on_device(slots, dev, 8) ||
-        (sources != nullptr && !on_device(sources, dev, 4)))
-        return ST_ERR_INVALID_ARG;
-    st::AppendArgs a{*cache, k, v, dtype, T, k_token_stride, k_head_stride, v_token_stride, v_head_stride, slots, sources, nullptr};
-    cudaError_t e = st::decode_error_address(&a.err);
-    if (e == cudaSuccess) e = st::launch_kv_append(a, stream);
-    return to_status(e);
+    return guarded([&]() -> st_status {
+        if (cache_sizes(cache) == ST_ERR_INVALID_ARG || T < 0 || (dtype != ST_BF16 && dtype != ST_F16) ||
+            !strides_ok(k_token_stride, k_head_stride) || !strides_ok(v_token_stride, v_head_stride))
+            return ST_ERR_INVALID_ARG;
+        if (cache_sizes(cache) != ST_OK || T >= kLimit31) return ST_ERR_UNSUPPORTED;
+        if (T == 0) return ST_OK;
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return ST_ERR_CUDA;
+        if (!cache_arrays(cache, dev) || !on_device(k, dev, 16) || !on_device(v, dev, 16) || !on_device(slots, dev, 8) ||
+            (sources != nullptr && !on_device(sources, dev, 4)))
+            return ST_ERR_INVALID_ARG;
+        st::AppendArgs a{*cache, k, v, dtype, T, k_token_stride, k_head_stride, v_token_stride, v_head_stride, slots, sources, nullptr};
+        cudaError_t e = st::decode_error_address(&a.err);
+        if (e == cudaSuccess) e = st::launch_kv_append(a, stream);
+        return to_status(e);
+    });
 }
 
 st_status st_kv_attend_workspace(const st_kv_cache* cache, int64_t T, int32_t q_heads, int32_t R, int32_t max_q,
@@ -171,28 +206,30 @@ st_status st_kv_attend(const st_kv_cache* cache, const void* q, st_dtype dtype, 
                        float scale, int32_t causal, void* out, int64_t out_token_stride,
                        int64_t out_head_stride, void* workspace, int64_t workspace_bytes, cudaStream_t stream)
 {
-    const st_status s = attend_sizes(cache, T, q_heads, R, max_q, max_len);
-    if (s == ST_ERR_INVALID_ARG) return s;
-    if ((dtype != ST_BF16 && dtype != ST_F16) || max_blocks < 1 || !std::isfinite(scale) ||
-        !strides_ok(q_token_stride, q_head_stride) || !strides_ok(out_token_stride, out_head_stride) ||
-        max_len > int64_t(max_blocks) * cache->block_size)
-        return ST_ERR_INVALID_ARG;
-    if (s != ST_OK) return s;
-    if (int64_t(R) * max_blocks >= kLimit31) return ST_ERR_UNSUPPORTED;
-    if (T == 0) return ST_OK;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return ST_ERR_CUDA;
-    if (!cache_arrays(cache, dev) || !on_device(q, dev, 16) || !on_device(out, dev, 16) || !on_device(table, dev, 4) ||
-        !on_device(row_start, dev, 4) || !on_device(lens, dev, 4))
-        return ST_ERR_INVALID_ARG;
-    const int64_t need = st::kv_attend_workspace(*cache, T, q_heads, R, max_q, max_len);
-    if (need > 0 && (workspace_bytes < need || !on_device(workspace, dev, 16))) return ST_ERR_INVALID_ARG;
-    st::AttendArgs a{*cache, q, dtype, T, q_heads, q_token_stride, q_head_stride, table, max_blocks, row_start, lens,
-                     R, max_q, max_len, scale * 1.44269504088896340736f, causal, out, out_token_stride, out_head_stride,
-                     workspace, nullptr};
-    cudaError_t e = st::decode_error_address(&a.err);
-    if (e == cudaSuccess) e = st::launch_kv_attend(a, stream);
-    return to_status(e);
+    return guarded([&]() -> st_status {
+        const st_status s = attend_sizes(cache, T, q_heads, R, max_q, max_len);
+        if (s == ST_ERR_INVALID_ARG) return s;
+        if ((dtype != ST_BF16 && dtype != ST_F16) || max_blocks < 1 || !std::isfinite(scale) ||
+            !strides_ok(q_token_stride, q_head_stride) || !strides_ok(out_token_stride, out_head_stride) ||
+            max_len > int64_t(max_blocks) * cache->block_size)
+            return ST_ERR_INVALID_ARG;
+        if (s != ST_OK) return s;
+        if (int64_t(R) * max_blocks >= kLimit31) return ST_ERR_UNSUPPORTED;
+        if (T == 0) return ST_OK;
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return ST_ERR_CUDA;
+        if (!cache_arrays(cache, dev) || !on_device(q, dev, 16) || !on_device(out, dev, 16) || !on_device(table, dev, 4) ||
+            !on_device(row_start, dev, 4) || !on_device(lens, dev, 4))
+            return ST_ERR_INVALID_ARG;
+        const int64_t need = st::kv_attend_workspace(*cache, T, q_heads, R, max_q, max_len);
+        if (need > 0 && (workspace_bytes < need || !on_device(workspace, dev, 16))) return ST_ERR_INVALID_ARG;
+        st::AttendArgs a{*cache, q, dtype, T, q_heads, q_token_stride, q_head_stride, table, max_blocks, row_start, lens,
+                         R, max_q, max_len, scale * 1.44269504088896340736f, causal, out, out_token_stride, out_head_stride,
+                         workspace, nullptr};
+        cudaError_t e = st::decode_error_address(&a.err);
+        if (e == cudaSuccess) e = st::launch_kv_attend(a, stream);
+        return to_status(e);
+    });
 }
 
 st_status st_beam_select_workspace(int32_t B, int32_t K, int32_t V, int32_t keep, int64_t* bytes)
@@ -209,84 +246,90 @@ st_status st_beam_select(const void* logits, st_dtype dtype, int64_t logits_stri
                          int32_t* out_tokens, const st_beam_extras* extras, void* workspace,
                          int64_t workspace_bytes, cudaStream_t stream)
 {
-    const st_status s = select_sizes(B, K, V, keep);
-    if (s == ST_ERR_INVALID_ARG) return s;
-    if ((dtype != ST_BF16 && dtype != ST_F16 && dtype != ST_F32) || logits_stride < V) return ST_ERR_INVALID_ARG;
-    st::SelectArgs a{logits, dtype, logits_stride, scores, B, K, V, keep, out_scores, out_parents, out_tokens, {}, workspace};
-    if (extras) a.ex = *extras;
-    if (a.ex.allow_request_stride < 0 || a.ex.allow_beam_stride < 0 ||
-        (a.ex.finished == nullptr) != (a.ex.out_finished == nullptr) ||
-        (a.ex.finished && (a.ex.end_token < 0 || a.ex.end_token >= V)))
-        return ST_ERR_INVALID_ARG;
-    if (s != ST_OK) return s;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return ST_ERR_CUDA;
-    if (!on_device(logits, dev, dtype == ST_F32 ? 4 : 2) || !on_device(scores, dev, 4) ||
-        !on_device(out_scores, dev, 4) || !on_device(out_parents, dev, 4) || !on_device(out_tokens, dev, 4) ||
-        (a.ex.allow && !on_device(a.ex.allow, dev, 4)) || (a.ex.finished && !on_device(a.ex.finished, dev, 1)) ||
-        (a.ex.out_finished && !on_device(a.ex.out_finished, dev, 1)))
-        return ST_ERR_INVALID_ARG;
-    const int64_t need = st::beam_select_workspace(B, K, V, keep);
-    if (need > 0 && (workspace_bytes < need || !on_device(workspace, dev, 16))) return ST_ERR_INVALID_ARG;
-    return to_status(st::launch_beam_select(a, stream));
+    return guarded([&]() -> st_status {
+        const st_status s = select_sizes(B, K, V, keep);
+        if (s == ST_ERR_INVALID_ARG) return s;
+        if ((dtype != ST_BF16 && dtype != ST_F16 && dtype != ST_F32) || logits_stride < V) return ST_ERR_INVALID_ARG;
+        st::SelectArgs a{logits, dtype, logits_stride, scores, B, K, V, keep, out_scores, out_parents, out_tokens, {}, workspace};
+        if (extras) a.ex = *extras;
+        if (a.ex.allow_request_stride < 0 || a.ex.allow_beam_stride < 0 ||
+            (a.ex.finished == nullptr) != (a.ex.out_finished == nullptr) ||
+            (a.ex.finished && (a.ex.end_token < 0 || a.ex.end_token >= V)))
+            return ST_ERR_INVALID_ARG;
+        if (s != ST_OK) return s;
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return ST_ERR_CUDA;
+        if (!on_device(logits, dev, dtype == ST_F32 ? 4 : 2) || !on_device(scores, dev, 4) ||
+            !on_device(out_scores, dev, 4) || !on_device(out_parents, dev, 4) || !on_device(out_tokens, dev, 4) ||
+            (a.ex.allow && !on_device(a.ex.allow, dev, 4)) || (a.ex.finished && !on_device(a.ex.finished, dev, 1)) ||
+            (a.ex.out_finished && !on_device(a.ex.out_finished, dev, 1)))
+            return ST_ERR_INVALID_ARG;
+        const int64_t need = st::beam_select_workspace(B, K, V, keep);
+        if (need > 0 && (workspace_bytes < need || !on_device(workspace, dev, 16))) return ST_ERR_INVALID_ARG;
+        return to_status(st::launch_beam_select(a, stream));
+    });
 }
 
 st_status st_beam_reorder(const st_beam_state* states, int32_t n_states, const int32_t* parents, int32_t B,
                           int32_t K, int32_t keep, cudaStream_t stream)
 {
-    if (states == nullptr || n_states < 1 || B < 1 || K < 1 || keep < 1) return ST_ERR_INVALID_ARG;
-    const int64_t n_src = int64_t(B) * K, n_dst = int64_t(B) * keep;
-    const int64_t far = int64_t(1) << 62;
-    for (int i = 0; i < n_states; ++i) {
-        const st_beam_state& x = states[i];
-        if (x.row_bytes < 0 || x.outer < 0 || x.src_row_stride < 0 || x.dst_row_stride < 0 ||
-            x.src_outer_stride < 0 || x.dst_outer_stride < 0)
-            return ST_ERR_INVALID_ARG;
-    }
-    if (n_states > ST_BEAM_MAX_STATES || n_src >= kLimit31 || n_dst >= kLimit31) return ST_ERR_UNSUPPORTED;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return ST_ERR_CUDA;
-    if (!on_device(parents, dev, 4)) return ST_ERR_INVALID_ARG;
-    // the bytes that each array's rows span, for the overlap checks
-    struct Span {
-        __int128 lo, hi;
-    } src[ST_BEAM_MAX_STATES], dst[ST_BEAM_MAX_STATES];
-    for (int i = 0; i < n_states; ++i) {
-        const st_beam_state& x = states[i];
-        src[i] = dst[i] = Span{0, 0};
-        if (x.row_bytes == 0 || x.outer == 0) continue;
-        if (!on_device(x.src, dev, 1) || !on_device(x.dst, dev, 1)) return ST_ERR_INVALID_ARG;
-        const __int128 ls = __int128(x.outer - 1) * x.src_outer_stride + __int128(n_src - 1) * x.src_row_stride + x.row_bytes;
-        const __int128 ld = __int128(x.outer - 1) * x.dst_outer_stride + __int128(n_dst - 1) * x.dst_row_stride + x.row_bytes;
-        if (ls > far || ld > far) return ST_ERR_INVALID_ARG;
-        // rows of dst apart from each other: rows inside outer parts, or outer parts inside rows
-        const bool rows_inside = (n_dst == 1 || x.dst_row_stride >= x.row_bytes) &&
-                                 (x.outer == 1 || __int128(x.dst_outer_stride) >= __int128(n_dst - 1) * x.dst_row_stride + x.row_bytes);
-        const bool outer_inside = (x.outer == 1 || x.dst_outer_stride >= x.row_bytes) &&
-                                  (n_dst == 1 || __int128(x.dst_row_stride) >= __int128(x.outer - 1) * x.dst_outer_stride + x.row_bytes);
-        if (!rows_inside && !outer_inside) return ST_ERR_INVALID_ARG;
-        src[i].lo = reinterpret_cast<uintptr_t>(x.src);
-        src[i].hi = src[i].lo + ls;
-        dst[i].lo = reinterpret_cast<uintptr_t>(x.dst);
-        dst[i].hi = dst[i].lo + ld;
-    }
-    for (int i = 0; i < n_states; ++i)
-        for (int j = 0; j < n_states; ++j) {
-            if (dst[i].lo < src[j].hi && src[j].lo < dst[i].hi) return ST_ERR_INVALID_ARG;
-            if (i < j && dst[i].lo < dst[j].hi && dst[j].lo < dst[i].hi) return ST_ERR_INVALID_ARG;
+    return guarded([&]() -> st_status {
+        if (states == nullptr || n_states < 1 || B < 1 || K < 1 || keep < 1) return ST_ERR_INVALID_ARG;
+        const int64_t n_src = int64_t(B) * K, n_dst = int64_t(B) * keep;
+        const int64_t far = int64_t(1) << 62;
+        for (int i = 0; i < n_states; ++i) {
+            const st_beam_state& x = states[i];
+            if (x.row_bytes < 0 || x.outer < 0 || x.src_row_stride < 0 || x.dst_row_stride < 0 ||
+                x.src_outer_stride < 0 || x.dst_outer_stride < 0)
+                return ST_ERR_INVALID_ARG;
         }
-    uint32_t* err = nullptr;
-    cudaError_t e = st::decode_error_address(&err);
-    if (e == cudaSuccess) e = st::launch_beam_reorder(states, n_states, parents, B, K, keep, err, stream);
-    return to_status(e);
+        if (n_states > ST_BEAM_MAX_STATES || n_src >= kLimit31 || n_dst >= kLimit31) return ST_ERR_UNSUPPORTED;
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return ST_ERR_CUDA;
+        if (!on_device(parents, dev, 4)) return ST_ERR_INVALID_ARG;
+        // the bytes that each array's rows span, for the overlap checks
+        struct Span {
+            __int128 lo, hi;
+        } src[ST_BEAM_MAX_STATES], dst[ST_BEAM_MAX_STATES];
+        for (int i = 0; i < n_states; ++i) {
+            const st_beam_state& x = states[i];
+            src[i] = dst[i] = Span{0, 0};
+            if (x.row_bytes == 0 || x.outer == 0) continue;
+            if (!on_device(x.src, dev, 1) || !on_device(x.dst, dev, 1)) return ST_ERR_INVALID_ARG;
+            const __int128 ls = __int128(x.outer - 1) * x.src_outer_stride + __int128(n_src - 1) * x.src_row_stride + x.row_bytes;
+            const __int128 ld = __int128(x.outer - 1) * x.dst_outer_stride + __int128(n_dst - 1) * x.dst_row_stride + x.row_bytes;
+            if (ls > far || ld > far) return ST_ERR_INVALID_ARG;
+            // rows of dst apart from each other: rows inside outer parts, or outer parts inside rows
+            const bool rows_inside = (n_dst == 1 || x.dst_row_stride >= x.row_bytes) &&
+                                     (x.outer == 1 || __int128(x.dst_outer_stride) >= __int128(n_dst - 1) * x.dst_row_stride + x.row_bytes);
+            const bool outer_inside = (x.outer == 1 || x.dst_outer_stride >= x.row_bytes) &&
+                                      (n_dst == 1 || __int128(x.dst_row_stride) >= __int128(x.outer - 1) * x.dst_outer_stride + x.row_bytes);
+            if (!rows_inside && !outer_inside) return ST_ERR_INVALID_ARG;
+            src[i].lo = reinterpret_cast<uintptr_t>(x.src);
+            src[i].hi = src[i].lo + ls;
+            dst[i].lo = reinterpret_cast<uintptr_t>(x.dst);
+            dst[i].hi = dst[i].lo + ld;
+        }
+        for (int i = 0; i < n_states; ++i)
+            for (int j = 0; j < n_states; ++j) {
+                if (dst[i].lo < src[j].hi && src[j].lo < dst[i].hi) return ST_ERR_INVALID_ARG;
+                if (i < j && dst[i].lo < dst[j].hi && dst[j].lo < dst[i].hi) return ST_ERR_INVALID_ARG;
+            }
+        uint32_t* err = nullptr;
+        cudaError_t e = st::decode_error_address(&err);
+        if (e == cudaSuccess) e = st::launch_beam_reorder(states, n_states, parents, B, K, keep, err, stream);
+        return to_status(e);
+    });
 }
 
 st_status st_decode_check(cudaStream_t stream)
 {
-    if (cudaStreamSynchronize(stream) != cudaSuccess) return ST_ERR_CUDA;
-    uint32_t word = 0;
-    if (st::decode_error_word(&word) != cudaSuccess) return ST_ERR_CUDA;
-    return word ? ST_ERR_DEVICE : ST_OK;
+    return guarded([&]() -> st_status {
+        if (cudaStreamSynchronize(stream) != cudaSuccess) return ST_ERR_CUDA;
+        uint32_t word = 0;
+        if (st::decode_error_word(&word) != cudaSuccess) return ST_ERR_CUDA;
+        return word ? ST_ERR_DEVICE : ST_OK;
+    });
 }
 
 }  // extern "C"

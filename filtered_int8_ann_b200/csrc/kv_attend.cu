@@ -105,6 +105,7 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
 
     const int start = min(max(a.row_start[row], 0), int(a.T)), n = min(max(a.row_start[row + 1], start), int(a.T)) - start;
     int64_t len = max(a.lens[row], 0);
+    if (int64_t(n) * G <= a.above_cols || int64_t(n) * G > a.most_cols) return;  // another launch's row
     if (len > a.max_len || n > a.max_q) {
         if (split == 0 && hk == 0 && col0 == 0 && tid == 0) atomicOr(a.err, kDecErrRow);
         len = 0;
@@ -162,7 +163,7 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
     };
     copy_stage(warp * (kDecGroup / 16), 0);  // on its way while scales and queries come
     float vmax = 0.f;
-    for (int i = tid; i < sixteens; i += kDecBlock) {
+    for (int i = tid; i < sixteens + 2 * kDecWarps * kDecGroup / 16; i += kDecBlock) {
         const int64_t at = sh.at[i], block = at >> (shift + (D == 128 ? 7 : 6));
         sh.ks[i] = at < 0 ? 0.f : a.c.k_scale[block];
         const float vs = at < 0 ? 0.f : a.c.v_scale[block];
@@ -447,24 +448,39 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
 
 // Join a query head's stretches: groups of D threads take every so many of them each.
 template <typename T, int D, int kJoinBlock>
-__global__ void __launch_bounds__(kJoinBlock) kv_join_kernel(AttendArgs a, int splits, int stretch)
+__global__ void __launch_bounds__(kJoinBlock) kv_join_kernel(AttendArgs a, int splits, int stretch, int per_row)
 {
     constexpr int GROUPS = kJoinBlock / D, kChunk = kJoinBlock;
     __shared__ float s_w[kChunk], s_red[kJoinBlock / 32], s_o[GROUPS][D];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, d = tid % D, group = tid / D;
-    const int64_t unit = blockIdx.x;
-    const int64_t token = unit / a.q_heads, head = unit - token * a.q_heads;
-    int lo = 0, hi = a.R;  // the row holding the token
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (a.row_start[mid + 1] > token) hi = mid;
-        else lo = mid + 1;
+    const int G = a.q_heads / a.c.kv_heads;
+    int lo;
+    int64_t token, head;
+    if (per_row > 0) {  // per_row columns of each row and cache head
+        const int64_t unit = blockIdx.x / per_row;
+        const int col = int(blockIdx.x - unit * per_row);
+        lo = int(unit / a.c.kv_heads);
+        token = int64_t(max(a.row_start[lo], 0)) + col / G;
+        head = (unit - int64_t(lo) * a.c.kv_heads) * G + col % G;
+        if (token >= min(a.row_start[lo + 1], int(a.T))) return;
+    } else {  // the query heads of every token
+        token = blockIdx.x / a.q_heads;
+        head = blockIdx.x - token * a.q_heads;
+        int hi = a.R;  // the row holding the token
+        lo = 0;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (a.row_start[mid + 1] > token) hi = mid;
+            else lo = mid + 1;
+        }
+        if (lo == a.R || a.row_start[lo] > token) return;
     }
-    if (lo == a.R || a.row_start[lo] > token) return;
     const int n = a.row_start[lo + 1] - a.row_start[lo];
+    const int64_t cols = int64_t(n) * G;
     int64_t len = max(a.lens[lo], 0);
-    if (n > a.max_q) return;  // written already
+    if (n > a.max_q || cols <= a.above_cols || cols > a.most_cols) return;  // written already, or another launch's
     if (len > a.max_len) len = 0;
+    const int64_t unit = token * a.q_heads + head;
     const int used = int(max(int64_t(1), (len + stretch - 1) / stretch));
     const float* po = static_cast<const float*>(a.workspace);
     const float* pm = po + a.T * a.q_heads * splits * D + 2 * unit * splits;
@@ -512,6 +528,7 @@ __global__ void __launch_bounds__(kJoinBlock) kv_join_kernel(AttendArgs a, int s
 
 struct DecPlan {
     int splits, stretch, cols, col_blocks;
+    int per_row;  // most columns of a row
 };
 
 // Stretches, multiples of the longest block. One row fills the GPU's places (3 CTAs per SM) once, all with
@@ -521,6 +538,7 @@ static DecPlan dec_plan(const st_kv_cache& c, int32_t q_heads, int32_t R, int32_
 {
     DecPlan p;
     const int64_t cols = int64_t(max_q) * (q_heads / c.kv_heads);
+    p.per_row = int(cols);
     p.cols = cols <= 8 ? 8 : 16;
     p.col_blocks = int((cols + p.cols - 1) / p.cols);
     const int64_t places = 3 * 148;
@@ -541,10 +559,10 @@ static DecPlan dec_plan(const st_kv_cache& c, int32_t q_heads, int32_t R, int32_
     return p;
 }
 
-static int64_t kv_decode_workspace(const st_kv_cache& c, int64_t T, int32_t q_heads, int32_t R, int32_t max_q, int64_t max_len)
+static int64_t kv_decode_workspace(const st_kv_cache& c, int64_t T, int32_t q_heads, const DecPlan& p)
 {
-    const DecPlan p = dec_plan(c, q_heads, R, max_q, max_len);
-    return p.splits == 1 ? 0 : T * q_heads * p.splits * (int64_t(c.head_dim) + 2) * 4;
+    // a multiple of 16 bytes: the prompts' kernel's part may follow
+    return p.splits == 1 ? 0 : (T * q_heads * p.splits * (int64_t(c.head_dim) + 2) * 4 + 15) / 16 * 16;
 }
 
 template <typename T, int D, int NT>
@@ -558,30 +576,32 @@ static cudaError_t launch_decode(const AttendArgs& a, const DecPlan& p, cudaStre
     kv_decode_kernel<T, D, NT><<<unsigned(ctas), kDecBlock, bytes, s>>>(a, p.splits, p.stretch, p.col_blocks);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.splits == 1) return e;
-    return launch_kv_join(a, p.splits, p.stretch, s);
+    return launch_kv_join(a, p.splits, p.stretch, p.per_row, s);
 }
 
 template <typename T, int D>
-static cudaError_t launch_join(const AttendArgs& a, int splits, int stretch, cudaStream_t s)
+static cudaError_t launch_join(const AttendArgs& a, int splits, int stretch, int per_row, int64_t ctas, cudaStream_t s)
 {
-    const dim3 grid{unsigned(a.T * a.q_heads)};
+    const dim3 grid{unsigned(ctas)};
     // few stretches are joined faster by small CTAs, many heads at a time
-    if (splits <= 16) return launch_dep(kv_join_kernel<T, D, 128>, grid, dim3(128), 0, s, a, splits, stretch);
-    return launch_dep(kv_join_kernel<T, D, 512>, grid, dim3(512), 0, s, a, splits, stretch);
+    if (splits <= 16) return launch_dep(kv_join_kernel<T, D, 128>, grid, dim3(128), 0, s, a, splits, stretch, per_row);
+    return launch_dep(kv_join_kernel<T, D, 512>, grid, dim3(512), 0, s, a, splits, stretch, per_row);
 }
 
-cudaError_t launch_kv_join(const AttendArgs& a, int splits, int stretch, cudaStream_t s)
+cudaError_t launch_kv_join(const AttendArgs& a, int splits, int stretch, int per_row, cudaStream_t s)
 {
-    const int64_t units = a.T * a.q_heads;
-    if (units > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    const int64_t ctas = per_row > 0 ? int64_t(a.R) * a.c.kv_heads * per_row : a.T * a.q_heads;
+    if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
     const bool bf = a.dtype == ST_BF16;
-    if (a.c.head_dim == 128) return bf ? launch_join<__nv_bfloat16, 128>(a, splits, stretch, s) : launch_join<__half, 128>(a, splits, stretch, s);
-    return bf ? launch_join<__nv_bfloat16, 64>(a, splits, stretch, s) : launch_join<__half, 64>(a, splits, stretch, s);
+    if (a.c.head_dim == 128)
+        return bf ? launch_join<__nv_bfloat16, 128>(a, splits, stretch, per_row, ctas, s)
+                  : launch_join<__half, 128>(a, splits, stretch, per_row, ctas, s);
+    return bf ? launch_join<__nv_bfloat16, 64>(a, splits, stretch, per_row, ctas, s)
+              : launch_join<__half, 64>(a, splits, stretch, per_row, ctas, s);
 }
 
-static cudaError_t launch_kv_decode(const AttendArgs& a, cudaStream_t s)
+static cudaError_t launch_kv_decode(const AttendArgs& a, const DecPlan& p, cudaStream_t s)
 {
-    const DecPlan p = dec_plan(a.c, a.q_heads, a.R, a.max_q, a.max_len);
     const bool bf = a.dtype == ST_BF16, wide = a.c.head_dim == 128, two = p.cols > 8;
     if (wide && two) return bf ? launch_decode<__nv_bfloat16, 128, 2>(a, p, s) : launch_decode<__half, 128, 2>(a, p, s);
     if (wide) return bf ? launch_decode<__nv_bfloat16, 128, 1>(a, p, s) : launch_decode<__half, 128, 1>(a, p, s);
@@ -589,21 +609,49 @@ static cudaError_t launch_kv_decode(const AttendArgs& a, cudaStream_t s)
     return bf ? launch_decode<__nv_bfloat16, 64, 1>(a, p, s) : launch_decode<__half, 64, 1>(a, p, s);
 }
 
-// Up to this many columns go to the decode kernel.
-static bool few_columns(const st_kv_cache& c, int32_t q_heads, int32_t max_q)
+// Which kernels a call takes: rows of up to kDecMaxCols columns go to the decode kernel, the others to the
+// prompts' kernel; a batch that may hold both kinds takes both.
+struct AttendPlan {
+    bool decode, prefill;
+    DecPlan dec;
+    int64_t dec_bytes;  // of the workspace, before the prompts' kernel's
+};
+
+static AttendPlan attend_plan(const st_kv_cache& c, int64_t T, int32_t q_heads, int32_t R, int32_t max_q, int64_t max_len)
 {
-    return int64_t(max_q) * (q_heads / c.kv_heads) <= kDecMaxCols;
+    const int64_t G = q_heads / c.kv_heads;
+    AttendPlan p;
+    p.prefill = max_q * G > kDecMaxCols;
+    p.decode = !p.prefill || (R > 1 && G <= kDecMaxCols);
+    p.dec = DecPlan{};
+    p.dec_bytes = 0;
+    if (p.decode) {
+        p.dec = dec_plan(c, q_heads, R, p.prefill ? int32_t(kDecMaxCols / G) : max_q, max_len);
+        p.dec_bytes = kv_decode_workspace(c, T, q_heads, p.dec);
+    }
+    return p;
 }
 
 int64_t kv_attend_workspace(const st_kv_cache& c, int64_t T, int32_t q_heads, int32_t R, int32_t max_q, int64_t max_len)
 {
-    return few_columns(c, q_heads, max_q) ? kv_decode_workspace(c, T, q_heads, R, max_q, max_len)
-                                          : kv_prefill_workspace(c, T, q_heads, R, max_q, max_len);
+    const AttendPlan p = attend_plan(c, T, q_heads, R, max_q, max_len);
+    return p.dec_bytes + (p.prefill ? kv_prefill_workspace(c, T, q_heads, R, max_q, max_len) : 0);
 }
 
-cudaError_t launch_kv_attend(const AttendArgs& a, cudaStream_t s)
+cudaError_t launch_kv_attend(const AttendArgs& args, cudaStream_t s)
 {
-    return few_columns(a.c, a.q_heads, a.max_q) ? launch_kv_decode(a, s) : launch_kv_prefill(a, s);
+    const AttendPlan p = attend_plan(args.c, args.T, args.q_heads, args.R, args.max_q, args.max_len);
+    AttendArgs a = args;
+    if (p.prefill) {
+        a.above_cols = p.decode ? kDecMaxCols : 0;
+        a.workspace = static_cast<char*>(args.workspace) + p.dec_bytes;
+        const cudaError_t e = launch_kv_prefill(a, s);
+        if (e != cudaSuccess) return e;
+        a.above_cols = 0;
+        a.most_cols = kDecMaxCols;
+        a.workspace = args.workspace;
+    }
+    return p.decode ? launch_kv_decode(a, p.dec, s) : cudaSuccess;
 }
 
 }  // namespace st

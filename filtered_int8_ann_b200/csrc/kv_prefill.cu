@@ -323,28 +323,35 @@ __device__ __forceinline__ void regs_down()
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kPreBlock, 1)
-kv_prefill_kernel(AttendArgs a, int splits, int stretch, int pairs)
+kv_prefill_kernel(AttendArgs a, int splits, int stretch)
 {
     extern __shared__ unsigned char raw[];
     PreShared<D>& sh = *reinterpret_cast<PreShared<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int hk = blockIdx.y;
     const int unit = blockIdx.x / splits, split = blockIdx.x - unit * splits;
-    const int row = unit / pairs, pair = pairs - 1 - (unit - row * pairs);  // the columns that see most first
     const int G = a.q_heads / a.c.kv_heads, S = a.c.block_size, shift = 31 - __clz(S);
 
+    // Units: row r's pairs of tiles are numbered from floor(row_start[r] G / 256) + r on, which leaves room for all of
+    // them whatever the rows' lengths. This unit's row is the last that begins at or before it.
+    auto begin_of = [&](int r) { return int(int64_t(min(max(a.row_start[r], 0), int(a.T))) * G / kPreCols) + r; };
+    int lo = 0, hi = a.R - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (begin_of(mid) <= unit) lo = mid;
+        else hi = mid - 1;
+    }
+    const int row = lo, nth = unit - begin_of(row);
     const int start = min(max(a.row_start[row], 0), int(a.T)), n = min(max(a.row_start[row + 1], start), int(a.T)) - start;
+    const int64_t all_cols = int64_t(n) * G;
+    const int row_pairs = int((all_cols + kPreCols - 1) / kPreCols), pair = row_pairs - 1 - nth;  // those that see most first
+    if (nth < 0 || pair < 0 || all_cols <= a.above_cols) return;
     int64_t len = max(a.lens[row], 0);
     if (len > a.max_len || n > a.max_q) {
         if (split == 0 && hk == 0 && pair == 0 && tid == 0) atomicOr(a.err, kDecErrRow);
         len = 0;
-        if (n > a.max_q) {  // more tokens than pairs: the first writes all its zeros
-            if (split == 0 && pair == 0) zero_rows<T, D>(a, start, n, hk * G, G);
-            return;
-        }
     }
-    const int64_t col0 = int64_t(pair) * kPreCols, all_cols = int64_t(n) * G;
-    if (col0 >= all_cols) return;
+    const int64_t col0 = int64_t(pair) * kPreCols;
     const int cols = int(min(int64_t(kPreCols), all_cols - col0));
     const int64_t j0 = int64_t(split) * stretch;
     if (j0 >= len && split > 0) return;
@@ -667,11 +674,12 @@ kv_prefill_kernel(AttendArgs a, int splits, int stretch, int pairs)
             give_up();
         } else {
             tc_fence_after();
-            const float scale = splits == 1 ? (l == 0.f ? 0.f : vtop / l) : vtop;
+            const bool direct = splits == 1 || n > a.max_q;  // (the join leaves out rows that are too long)
+            const float scale = direct ? (l == 0.f ? 0.f : vtop / l) : vtop;
             T* out = static_cast<T*>(a.out) + token * a.out_token + head * a.out_head;
             const int64_t part = (token * a.q_heads + head) * splits + split;
             float* po = static_cast<float*>(a.workspace);
-            if (mine && splits > 1) {
+            if (mine && !direct) {
                 float* pm = po + a.T * a.q_heads * splits * D;
                 pm[2 * part] = m;
                 pm[2 * part + 1] = l;
@@ -688,7 +696,7 @@ kv_prefill_kernel(AttendArgs a, int splits, int stretch, int pairs)
                 }
                 if (!mine) {
                     // the loads above are the whole warp's
-                } else if (splits == 1) {
+                } else if (direct) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         T y[8];
@@ -715,17 +723,17 @@ kv_prefill_kernel(AttendArgs a, int splits, int stretch, int pairs)
 }
 
 struct PrePlan {
-    int splits, stretch, pairs;
+    int splits, stretch;
+    int64_t units;
 };
 
 // Stretches: one while the columns alone fill the GPU, else enough for two CTAs per SM, none longer than the
 // table that fits, of at least 1024 tokens.
-static PrePlan pre_plan(const st_kv_cache& c, int32_t q_heads, int32_t R, int32_t max_q, int64_t max_len)
+static PrePlan pre_plan(const st_kv_cache& c, int64_t T, int32_t q_heads, int32_t R, int64_t max_len)
 {
     PrePlan p;
-    const int64_t cols = int64_t(max_q) * (q_heads / c.kv_heads);
-    p.pairs = int((cols + kPreCols - 1) / kPreCols);
-    const int64_t units = int64_t(R) * c.kv_heads * p.pairs, wanted = 2 * 148;
+    p.units = T * (q_heads / c.kv_heads) / kPreCols + R;
+    const int64_t units = p.units * c.kv_heads, wanted = 2 * 148;
     int64_t stretch = max_len;
     if (units < wanted) {
         const int64_t each = (wanted + units - 1) / units;
@@ -739,9 +747,9 @@ static PrePlan pre_plan(const st_kv_cache& c, int32_t q_heads, int32_t R, int32_
     return p;
 }
 
-int64_t kv_prefill_workspace(const st_kv_cache& c, int64_t T, int32_t q_heads, int32_t R, int32_t max_q, int64_t max_len)
+int64_t kv_prefill_workspace(const st_kv_cache& c, int64_t T, int32_t q_heads, int32_t R, int32_t, int64_t max_len)
 {
-    const PrePlan p = pre_plan(c, q_heads, R, max_q, max_len);
+    const PrePlan p = pre_plan(c, T, q_heads, R, max_len);
     return p.splits == 1 ? 0 : T * q_heads * p.splits * (int64_t(c.head_dim) + 2) * 4;
 }
 
@@ -751,17 +759,16 @@ static cudaError_t launch_prefill(const AttendArgs& a, const PrePlan& p, cudaStr
     const int bytes = int(sizeof(PreShared<D>)) + 1024;
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kv_prefill_kernel<T, D>), bytes);
     if (e != cudaSuccess) return e;
-    const int64_t ctas = int64_t(a.R) * p.pairs * p.splits;
-    if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    kv_prefill_kernel<T, D><<<dim3(unsigned(ctas), unsigned(a.c.kv_heads)), kPreBlock, bytes, s>>>(a, p.splits, p.stretch, p.pairs);
+    if (p.units * p.splits > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    kv_prefill_kernel<T, D><<<dim3(unsigned(p.units * p.splits), unsigned(a.c.kv_heads)), kPreBlock, bytes, s>>>(a, p.splits, p.stretch);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.splits == 1) return e;
-    return launch_kv_join(a, p.splits, p.stretch, s);
+    return launch_kv_join(a, p.splits, p.stretch, 0, s);
 }
 
 cudaError_t launch_kv_prefill(const AttendArgs& a, cudaStream_t s)
 {
-    const PrePlan p = pre_plan(a.c, a.q_heads, a.R, a.max_q, a.max_len);
+    const PrePlan p = pre_plan(a.c, a.T, a.q_heads, a.R, a.max_len);
     const bool bf = a.dtype == ST_BF16;
     if (a.c.head_dim == 128) return bf ? launch_prefill<__nv_bfloat16, 128>(a, p, s) : launch_prefill<__half, 128>(a, p, s);
     return bf ? launch_prefill<__nv_bfloat16, 64>(a, p, s) : launch_prefill<__half, 64>(a, p, s);

@@ -159,8 +159,8 @@ def st_kv_plan(table: torch.Tensor, have: torch.Tensor, add: torch.Tensor, num_b
     place), have and add int32 [R], room for T new tokens. Returns (slots int64
     [T], sources int32 [T], row_start int32 [R + 1], lens int32 [R], report
     int32 [4]); see st_kv_plan in include/st.h for what they hold."""
-    if table.dim() != 2:
-        raise ValueError("table must be [R, max_blocks]")
+    if table.dim() != 2 or T < 0:
+        raise ValueError("table must be [R, max_blocks], and T not negative")
     R, width = table.shape
     i32 = torch.int32
     pt, ph, pa = _array(table, i32, (R, width), "table"), _array(have, i32, (R,), "have"), _array(add, i32, (R,), "add")

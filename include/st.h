@@ -404,7 +404,10 @@ st_status st_index_insert(st_index* idx, const int32_t* lists, const int8_t* ite
  * that may overlap need workspaces of their own.
  *
  * A kernel that meets an index outside its arrays skips what it names and
- * sets the device's decode error word (st_decode_check).
+ * sets the device's decode error word (st_decode_check). Arrays that a call
+ * writes must not overlap any other array of the call. The first call of each
+ * function on a device raises kernel limits and looks up the error word: make it before a
+ * stream capture begins.
  */
 
 /* Types of the arrays that hold computed numbers. */
@@ -468,8 +471,8 @@ typedef struct {
  * max_blocks * block_size, or a used entry is outside [0, num_blocks) (this sets the
  * decode error word too).
  *
- * Errors: INVALID_ARG (null or non-device pointer, misaligned arrays, R < 1,
- * max_blocks < 1, T < 0, num_blocks < 1, a block size other than those above),
+ * Errors: INVALID_ARG (null or non-device pointer, misaligned or overlapping
+ * arrays, R < 1, max_blocks < 1, T < 0, num_blocks < 1, a block size other than those above),
  * UNSUPPORTED (R above ST_KV_MAX_ROWS, num_blocks above ST_KV_MAX_BLOCKS,
  * R * max_blocks or max_blocks * block_size at 2^31 or above, T at 2^31 - 1 or above), CUDA. slots and sources may be NULL when T = 0.
  */
@@ -533,7 +536,8 @@ st_status st_kv_append(const st_kv_cache* cache, const void* k, const void* v, s
  * Errors: INVALID_ARG (null or non-device pointer, misaligned arrays or strides,
  * q_heads not a multiple of kv_heads, sizes outside those above, a workspace that is too small),
  * UNSUPPORTED (the cache outside its limits, R above ST_KV_MAX_ROWS,
- * R * max_blocks or T at 2^31 or above, more than 65535 query heads), CUDA. A used table entry outside the cache hides its
+ * R * max_blocks or T at 2^31 or above, more than 65535 query heads, or sizes that
+ * take more than 2^31 CTAs), CUDA. A used table entry outside the cache hides its
  * tokens and sets the decode error word.
  */
 st_status st_kv_attend(const st_kv_cache* cache, const void* q, st_dtype dtype, int64_t T, int32_t q_heads,

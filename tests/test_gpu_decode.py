@@ -105,6 +105,17 @@ def test_plan_largest_sizes(R, width, blocks):
     check_plan(table, have, add, blocks, S, sum(add) + 5)
 
 
+def test_plan_refuses_overlapping_arrays():
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table, have, add = torch.zeros(2, 4, **i32), torch.zeros(2, **i32), torch.ones(2, **i32)
+    for kw in (dict(lens=have), dict(lens=add), dict(report=table.view(-1)[:4])):
+        with pytest.raises(st.StError) as e:
+            st.st_kv_plan(table, have, add, 9, 16, 2, **kw)
+        assert e.value.status == st.ST_ERR_INVALID_ARG
+    with pytest.raises(ValueError):
+        st.st_kv_plan(table, have, add, 9, 16, -1)
+
+
 # ----------------------------------------------------------------- append --
 def check_append(x, cache, slots, sources, bad=False, spread=False):
     """x: [T, 2, heads, D]"""
@@ -273,6 +284,24 @@ def test_attend_long_rows_are_split_and_joined(S, D):
     check_attend(*make_attend(2, [5000, 12], [4, 2], 2, 2, D, S, torch.float16))
 
 
+def test_attend_mixed_batches():
+    """Rows of single tokens beside prompts: each kind in its kernel, both of them split and joined."""
+    check_attend(*make_attend(20, [3000, 40, 2500, 0, 1, 5000], [1, 40, 300, 1, 1, 9], 1, 4, 64, 16, torch.bfloat16))
+    check_attend(*make_attend(21, [700, 2600, 90, 33], [2, 200, 90, 33], 2, 8, 128, 32, torch.float16))
+    check_attend(*make_attend(22, [300] * 40, [1] * 20 + [17] * 20, 1, 3, 64, 64, torch.bfloat16))
+    check_attend(*make_attend(23, [260, 80], [1, 80], 1, 40, 64, 16, torch.float16))  # more heads than the small kernel takes
+
+
+@pytest.mark.parametrize("max_len", [None, 2510])
+def test_attend_rows_with_more_queries_than_said(max_len):
+    """Zeros for them, the others as ever."""
+    q, codes, scales, table, start, lens = make_attend(24, [2500, 60, 100, 50], [70, 3, 40, 50], 1, 4, 64, 16, torch.float16)
+    got = check_attend(q, codes, scales, table, start, lens, max_q=50, max_len=max_len, bad=True, empty=(0,))
+    assert bool((got[:70] == 0).all())
+    got = check_attend(q, codes, scales, table, start, lens, max_q=2, max_len=max_len, bad=True, empty=(0, 1, 2, 3))
+    assert bool((got == 0).all())
+
+
 def test_attend_strided_and_not_causal():
     a = make_attend(5, [100, 31], [9, 31], 2, 3, 64, 16, torch.bfloat16)
     check_attend(*a, strided=True)
@@ -363,6 +392,35 @@ def test_attend_masked_places_may_hold_anything():
     check_attend(q, codes, scales, table, start, lens)
 
 
+def test_attend_and_append_in_a_cache_beyond_32_bit_offsets():
+    """Keys and values of 4.5 GB each, the rows' blocks at both ends."""
+    S, H, D = 128, 8, 128
+    blocks = (9 << 29) // (H * S * D) + 3
+    cache = st.KvCache(torch.empty(blocks, H, S, D, dtype=torch.int8, device="cuda"), torch.empty(blocks, H, S, D, dtype=torch.int8, device="cuda"),
+                       torch.empty(blocks, H, device="cuda"), torch.empty(blocks, H, device="cuda"))
+    pages = [blocks - 1, 0, blocks - 2, 1, blocks // 2]
+    n = 4 * S + 37
+    g = gen(30)
+    x = torch.randn(n, 2, H, D, generator=g).bfloat16()
+    slots = [pages[i // S] * S + i % S for i in range(n)]
+    small = [torch.zeros(5, H, S, D, dtype=torch.int8), torch.zeros(5, H, S, D, dtype=torch.int8), torch.zeros(5, H), torch.zeros(5, H)]
+    for i in range(2):
+        codes, scales = small[i].numpy(), small[2 + i].numpy()
+        ref.append(codes, scales, x[:, i].float().numpy(), [i // S * S + i % S for i in range(n)], None)
+    st.st_kv_append(cache, x[:, 0].cuda(), x[:, 1].cuda(), torch.tensor(slots).cuda())
+    for i, p in enumerate(pages):
+        m = min(S, n - i * S)
+        assert torch.equal(cache.k[p, :, :m].cpu(), small[0][i, :, :m]) and torch.equal(cache.v[p, :, :m].cpu(), small[1][i, :, :m])
+        assert torch.equal(cache.k_scale[p].cpu(), small[2][i]) and torch.equal(cache.v_scale[p].cpu(), small[3][i])
+    for m in (1, 90):
+        q = torch.randn(m, 2 * H, D, generator=g).bfloat16()
+        want, parts = ref.attend(q, small[0], small[1], small[2], small[3], [[0, 1, 2, 3, 4]], [0, m], [n], D ** -0.5)
+        got = st.st_kv_attend(cache, q.cuda(), torch.tensor([pages], dtype=torch.int32).cuda(), torch.tensor([0, m], dtype=torch.int32).cuda(),
+                              torch.tensor([n], dtype=torch.int32).cuda(), m)
+        assert bool(((got.cpu().double() - want).abs() <= ref.attend_tolerance(want, parts, torch.bfloat16, D)).all())
+    assert st.st_decode_check() == st.ST_OK
+
+
 # ----------------------------------------------------------------- select --
 def check_select(logits, scores, keep, allow=None, finished=None, end=0):
     cuda = lambda x: None if x is None else x.cuda()  # noqa: E731
@@ -447,6 +505,20 @@ def test_select_strided_and_unaligned_rows():
             check_select(x.contiguous(), s, 20)
 
 
+def test_select_logits_beyond_32_bit_offsets():
+    g = gen(31)
+    step = (1 << 30) + 12
+    base = torch.zeros(2 * step + 1000, dtype=torch.bfloat16, device="cuda")
+    x = (3 * torch.randn(1, 3, 1000, generator=g)).bfloat16()
+    d = base.as_strided((1, 3, 1000), (3 * step, step, 1))
+    d.copy_(x)
+    s = -torch.rand(1, 3, generator=g)
+    got = st.st_beam_select(d, s.cuda(), 30)
+    want = st.st_beam_select(x.cuda(), s.cuda(), 30)
+    assert all(torch.equal(a, b) for a, b in zip(got[:3], want[:3]))
+    check_select(x, s, 30)
+
+
 def test_select_far_apart_logits():
     """Ranges that overflow fp32, and values next to each other in fp32."""
     x = torch.zeros(1, 3, 40)
@@ -497,6 +569,15 @@ def test_reorder_layers_strides_and_out():
     want = torch.stack([torch.stack([x[:, b, parents[b].long()] for b in range(3)], 1)])[0]
     assert got.data_ptr() == out.data_ptr() and torch.equal(got, want)
     assert bool((hold[..., 24:] == 2.0).all())
+
+
+def test_reorder_beyond_32_bit_offsets():
+    n = (5 << 28) + 16
+    x = torch.zeros(1, 4, n, dtype=torch.int8, device="cuda")
+    for i in range(4):
+        x[0, i, 0], x[0, i, -1] = 10 + i, 20 + i
+    got = st.st_beam_reorder([x], torch.tensor([[3, 0, -1, 2]], dtype=torch.int32).cuda())[0]
+    assert got[0, :, 0].tolist() == [13, 10, 0, 12] and got[0, :, -1].tolist() == [23, 20, 0, 22] and int(got.sum()) == 100
 
 
 def test_reorder_bad_parents_give_zeros_and_the_error_word():

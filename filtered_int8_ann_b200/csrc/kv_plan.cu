@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kPlanBlock) kv_plan_kernel(PlanArgs a, int row
 // The slots of rows that get many tokens: each warp walks a stretch of tokens,
 // its lanes holding the ends of the next 32 rows.
 constexpr int kSlotBlock = 256;
-constexpr int kSlotStretch = 256;  // tokens per warp
+constexpr int kSlotStretch = 64;   // tokens per warp: more of them wait longer for each other than for the row search
 
 __global__ void __launch_bounds__(kSlotBlock) kv_slots_kernel(PlanArgs a)
 {

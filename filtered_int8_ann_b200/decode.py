@@ -27,6 +27,7 @@ from . import _BeamExtras, _BeamState, _KvCache, _check, _stream, lib
 ST_BF16, ST_F16, ST_F32 = 0, 1, 2
 _DTYPES = {torch.bfloat16: ST_BF16, torch.float16: ST_F16, torch.float32: ST_F32}
 _HALVES = (torch.bfloat16, torch.float16)
+_I8, _I32, _I64, _F32, _BOOL = torch.int8, torch.int32, torch.int64, torch.float32, torch.bool
 
 
 def _need(ok: bool, what: str):
@@ -89,10 +90,9 @@ def _select_workspace(B: int, K: int, V: int, keep: int) -> int:
 
 
 @functools.lru_cache(maxsize=256)
-def _attend_workspace(blocks: int, kv_heads: int, size: int, dim: int, T: int, heads: int, R: int, max_q: int,
-                      max_len: int) -> int:
+def _attend_workspace(kv_heads: int, size: int, dim: int, T: int, heads: int, R: int, max_q: int, max_len: int) -> int:
     need = ctypes.c_int64(0)
-    c = _KvCache(None, None, None, None, blocks, kv_heads, size, dim)
+    c = _KvCache(None, None, None, None, 1, kv_heads, size, dim)  # (the number of blocks does not matter)
     _check(lib().st_kv_attend_workspace(ctypes.byref(c), T, heads, R, max_q, max_len, ctypes.byref(need)),
            "st_kv_attend_workspace")
     return need.value
@@ -103,38 +103,24 @@ class KvCache:
     kv_heads, block_size, head_dim] and their scales float32 [num_blocks,
     kv_heads]. KvCache.empty allocates one."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "_c")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "num_blocks", "kv_heads", "block_size", "head_dim", "_c", "_ref")
 
     def __init__(self, k, v, k_scale, v_scale):
         shape = k.shape
         if len(shape) != 4:
             raise ValueError("k must be [num_blocks, kv_heads, block_size, head_dim]")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self._c = _KvCache(_array(k, torch.int8, shape, "k"), _array(v, torch.int8, shape, "v"),
-                           _array(k_scale, torch.float32, shape[:2], "k_scale"),
-                           _array(v_scale, torch.float32, shape[:2], "v_scale"), *shape)
+        self.num_blocks, self.kv_heads, self.block_size, self.head_dim = shape
+        scales = shape[:2]
+        c = self._c = _KvCache(_array(k, _I8, shape, "k"), _array(v, _I8, shape, "v"), _array(k_scale, _F32, scales, "k_scale"),
+                               _array(v_scale, _F32, scales, "v_scale"), *shape)
+        self._ref = ctypes.byref(c)
 
     @classmethod
     def empty(cls, num_blocks: int, kv_heads: int, block_size: int, head_dim: int, device="cuda"):
         shape = (num_blocks, kv_heads, block_size, head_dim)
         return cls(torch.zeros(shape, dtype=torch.int8, device=device), torch.zeros(shape, dtype=torch.int8, device=device),
                    torch.zeros(shape[:2], device=device), torch.zeros(shape[:2], device=device))
-
-    @property
-    def num_blocks(self):
-        return self._c.num_blocks
-
-    @property
-    def kv_heads(self):
-        return self._c.kv_heads
-
-    @property
-    def block_size(self):
-        return self._c.block_size
-
-    @property
-    def head_dim(self):
-        return self._c.head_dim
 
 
 def _vectors(x: torch.Tensor, heads: Optional[int], dim: int, name: str):
@@ -162,23 +148,23 @@ def st_kv_plan(table: torch.Tensor, have: torch.Tensor, add: torch.Tensor, num_b
     if table.dim() != 2 or T < 0:
         raise ValueError("table must be [R, max_blocks], and T not negative")
     R, width = table.shape
-    i32 = torch.int32
-    pt, ph, pa = _array(table, i32, (R, width), "table"), _array(have, i32, (R,), "have"), _array(add, i32, (R,), "add")
+    pt, ph, pa = _array(table, _I32, (R, width), "table"), _array(have, _I32, (R,), "have"), _array(add, _I32, (R,), "add")
     _on_gpu(table, "table")
-    if slots is None:
-        slots = _empty1(T, torch.int64, stream)
-    if sources is None:
-        sources = _empty1(T, i32, stream)
-    if row_start is None:
-        row_start = _empty1(R + 1, i32, stream)
-    if lens is None:
-        lens = _empty1(R, i32, stream)
-    if report is None:
-        report = _empty1(4, i32, stream)
-    _check(lib().st_kv_plan(pt, ph, pa, R, width, num_blocks, block_size, T,
-                            _array(slots, torch.int64, (T,), "slots"), _array(sources, i32, (T,), "sources"),
-                            _array(row_start, i32, (R + 1,), "row_start"), _array(lens, i32, (R,), "lens"),
-                            _array(report, i32, (4,), "report"), _stream(stream)), "st_kv_plan")
+
+    def made(x, n, dtype, name):
+        if x is None:
+            x = _empty1(n, dtype, stream)
+            return x, x.data_ptr()
+        return x, _array(x, dtype, (n,), name)
+
+    slots, p0 = made(slots, T, _I64, "slots")
+    sources, p1 = made(sources, T, _I32, "sources")
+    row_start, p2 = made(row_start, R + 1, _I32, "row_start")
+    lens, p3 = made(lens, R, _I32, "lens")
+    report, p4 = made(report, 4, _I32, "report")
+    status = lib().st_kv_plan(pt, ph, pa, R, width, num_blocks, block_size, T, p0, p1, p2, p3, p4, _stream(stream))
+    if status:
+        _check(status, "st_kv_plan")
     return slots, sources, row_start, lens, report
 
 
@@ -186,15 +172,15 @@ def st_kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.
                  sources: Optional[torch.Tensor] = None, stream=None):
     """Quantise keys and values [T, kv_heads, head_dim] (bfloat16 or float16,
     any multiple-of-8 strides) into the cache's slots int64 [T]."""
-    c = cache._c
-    pk, kt, kh = _vectors(k, c.kv_heads, c.head_dim, "k")
-    pv, vt, vh = _vectors(v, c.kv_heads, c.head_dim, "v")
+    heads, dim = cache.kv_heads, cache.head_dim
+    pk, kt, kh = _vectors(k, heads, dim, "k")
+    pv, vt, vh = _vectors(v, heads, dim, "v")
     T = k.shape[0]
     if v.shape[0] != T or v.dtype is not k.dtype:
         raise ValueError("k and v must have the same tokens and type")
-    _check(lib().st_kv_append(ctypes.byref(c), pk, pv, _DTYPES[k.dtype], T, kt, kh, vt, vh,
-                              _array(slots, torch.int64, (T,), "slots"),
-                              None if sources is None else _array(sources, torch.int32, (T,), "sources"),
+    _check(lib().st_kv_append(cache._ref, pk, pv, _DTYPES[k.dtype], T, kt, kh, vt, vh,
+                              _array(slots, _I64, (T,), "slots"),
+                              None if sources is None else _array(sources, _I32, (T,), "sources"),
                               _stream(stream)), "st_kv_append")
 
 
@@ -205,20 +191,22 @@ def st_kv_attend(cache: KvCache, q: torch.Tensor, table: torch.Tensor, row_start
     tokens (table int32 [R, max_blocks], row_start int32 [R + 1], lens int32 [R]).
     max_q and max_len bound a row's query and cached tokens; scale defaults to
     head_dim ** -0.5. `out` rows behind row_start[R] are left as they were (a new `out` holds anything there)."""
-    c = cache._c
-    dim = c.head_dim
+    dim = cache.head_dim
     pq, qt, qh = _vectors(q, None, dim, "q")
     T, heads, _ = q.shape
     if table.dim() != 2:
         raise ValueError("table must be [R, max_blocks]")
     R, width = table.shape
     if max_len is None:
-        max_len = width * c.block_size
-    pt = _array(table, torch.int32, (R, width), "table")
-    ps, pl = _array(row_start, torch.int32, (R + 1,), "row_start"), _array(lens, torch.int32, (R,), "lens")
+        max_len = width * cache.block_size
+    pt = _array(table, _I32, (R, width), "table")
+    ps, pl = _array(row_start, _I32, (R + 1,), "row_start"), _array(lens, _I32, (R,), "lens")
     if out is None:
         _on_gpu(q, "q")
-        out = _empty(q.shape, q.dtype, stream)
+        if stream is None:
+            out = _empty_strided_cuda((T, heads, dim), (heads * dim, dim, 1), q.dtype)
+        else:
+            out = _empty((T, heads, dim), q.dtype, stream)
         po, ot, oh = out.data_ptr(), heads * dim, dim
     else:
         _need(out.shape == q.shape and out.dtype == q.dtype, "out must be like q")
@@ -226,13 +214,13 @@ def st_kv_attend(cache: KvCache, q: torch.Tensor, table: torch.Tensor, row_start
         # tokens apart from each other, and heads: one inside the other either way
         _need((T <= 1 or ot >= dim) and (heads <= 1 or oh >= dim) and
               (T <= 1 or heads <= 1 or ot >= (heads - 1) * oh + dim or oh >= (T - 1) * ot + dim), "out's vectors must not overlap")
-    need = _attend_workspace(c.num_blocks, c.kv_heads, c.block_size, dim, T, heads, R, max_q, max_len)
+    need = _attend_workspace(cache.kv_heads, cache.block_size, dim, T, heads, R, max_q, max_len)
     room = 0
     if workspace is not None:
         room = workspace.numel() * workspace.element_size()
     elif need:
         workspace, room = _empty1(need, torch.uint8, stream), need
-    _check(lib().st_kv_attend(ctypes.byref(c), pq, _DTYPES[q.dtype], T, heads, qt, qh, pt, width, ps, pl, R, max_q, max_len,
+    _check(lib().st_kv_attend(cache._ref, pq, _DTYPES[q.dtype], T, heads, qt, qh, pt, width, ps, pl, R, max_q, max_len,
                               dim ** -0.5 if scale is None else scale, int(causal), po, ot, oh,
                               None if workspace is None else workspace.data_ptr(), room, _stream(stream)),
            "st_kv_attend")
@@ -258,7 +246,7 @@ def st_beam_select(logits: torch.Tensor, scores: torch.Tensor, keep: int, allow:
     stride = beam if K > 1 else request if B > 1 else V
     if B > 1 and K > 1 and request != K * stride:
         raise ValueError("logits' beams must be evenly spaced")
-    pscores = _array(scores, torch.float32, (B, K), "scores")
+    pscores = _array(scores, _F32, (B, K), "scores")
     ex = out_finished = None
     if allow is not None or finished is not None:
         ex = _BeamExtras()
@@ -268,7 +256,7 @@ def st_beam_select(logits: torch.Tensor, scores: torch.Tensor, keep: int, allow:
             _need(allow.shape[2] <= 1 or allow.stride(2) == 1, "allow must have dense words")
             ex.allow, ex.allow_request_stride, ex.allow_beam_stride = allow.data_ptr(), allow.stride(0), allow.stride(1)
         if finished is not None:
-            pf = _array(finished, torch.bool, (B, K), "finished")
+            pf = _array(finished, _BOOL, (B, K), "finished")
             _on_gpu(finished, "finished")
             out_finished = _empty2(B, keep, torch.bool, stream)
             ex.finished, ex.out_finished = pf, out_finished.data_ptr()
@@ -276,7 +264,7 @@ def st_beam_select(logits: torch.Tensor, scores: torch.Tensor, keep: int, allow:
     _on_gpu(logits, "logits")
     need = _select_workspace(B, K, V, keep)
     out_scores = _empty2(B, keep, torch.float32, stream)
-    out_parents, out_tokens = _empty2(B, keep, torch.int32, stream), _empty2(B, keep, torch.int32, stream)
+    out_parents, out_tokens = _empty2(B, keep, _I32, stream), _empty2(B, keep, _I32, stream)
     room = 0
     if workspace is not None:
         room = workspace.numel() * workspace.element_size()
@@ -315,7 +303,7 @@ def st_beam_reorder(states: Sequence[torch.Tensor], parents: torch.Tensor, out: 
         raise ValueError("parents must be [B, keep], beam_dim 1 or 2, and states not empty")
     B, keep = parents.shape
     K = states[0].shape[beam_dim] if states[0].dim() > beam_dim else -1
-    pp = _array(parents, torch.int32, (B, keep), "parents")
+    pp = _array(parents, _I32, (B, keep), "parents")
     made = []
     table = (_BeamState * len(states))()
     for i, x in enumerate(states):

@@ -55,6 +55,7 @@ struct PreShared {
     alignas(8) uint64_t k_full[kPreStages], k_empty[kPreStages], v_full[kPreStages], v_empty[kPreStages];
     uint64_t s_full[2], p_ready[2], pv_done[2];
     uint64_t drain;
+    float2 joined[kPreTile];  // taking turns: the second tile's maxima and sums (its O goes over the K operands)
     uint32_t tmem;
     int32_t abort;
 };
@@ -360,7 +361,8 @@ kv_prefill_kernel(AttendArgs a, int splits, int stretch)
     if (a.causal) end = min(end, len - n + (col0 + cols - 1) / G + 1);
     const int tokens = int(max(int64_t(0), min(int64_t(stretch), end - j0)));
     const int steps = (tokens + kPreTile - 1) / kPreTile;
-    const int tiles = cols > kPreTile ? 2 : 1;
+    // Up to 128 columns stand in both tiles, which take the steps in turn; their sums are joined at the end.
+    const bool turns = cols <= kPreTile;
 
     if (warp == kPreMmaWarp) {
         tmem_alloc(&sh.tmem, 512);
@@ -408,8 +410,8 @@ kv_prefill_kernel(AttendArgs a, int splits, int stretch)
     }
     // the queries, a column per softmax thread
     const int tile = warp >> 2, r = tid & 127;  // warps 0-7
-    const int64_t col = col0 + tile * kPreTile + r;
-    const bool mine = warp < 8 && tile * kPreTile + r < cols;
+    const int64_t col = col0 + (turns ? 0 : tile * kPreTile) + r;
+    const bool mine = warp < 8 && col < col0 + cols;
     float mult = 0.f;
     int64_t token = 0, head = 0;
     if (warp < 8) {
@@ -491,12 +493,12 @@ kv_prefill_kernel(AttendArgs a, int splits, int stretch)
                     tc_commit(&sh.s_full[x]);
                 }
             };
-            auto values = [&](int x, int j) {  // O += P V
+            auto values = [&](int x, int j, bool first) {  // O += P V
                 if (lead) {
                     const uint64_t v = dv + (j & 1) * (sizeof(sh.v[0]) >> 4);
 #pragma unroll
                     for (int s = 0; s < kPreTile / 16; ++s)
-                        tc_mma_f16_ts(tmem + 256 + x * 128, tmem + x * 128 + s * 8, v + s / 4 * kVHalf + (s & 3) * 2, idO, j > 0 || s > 0);
+                        tc_mma_f16_ts(tmem + 256 + x * 128, tmem + x * 128 + s * 8, v + s / 4 * kVHalf + (s & 3) * 2, idO, !first || s > 0);
                     tc_commit(&sh.pv_done[x]);
                 }
             };
@@ -504,28 +506,55 @@ kv_prefill_kernel(AttendArgs a, int splits, int stretch)
                 if (lead) tc_commit(bar);
             };
             bool ok = wait_or_abort(&sh.k_full[0], 0, abort);
-            if (ok) {
-                tc_fence_after();
+            if (turns) {
 #pragma unroll 1
-                for (int x = 0; x < tiles; ++x) scores(x, 0);
-                done(&sh.k_empty[0]);
-            }
-#pragma unroll 1
-            for (int j = 0; j < steps && ok; ++j) {
-                const int st = j & 1, nx = st ^ 1;
-                ok = wait_or_abort(&sh.v_full[st], j >> 1 & 1, abort);
-                if (ok && j + 1 < steps) ok = wait_or_abort(&sh.k_full[nx], (j + 1) >> 1 & 1, abort);
-#pragma unroll 1
-                for (int x = 0; x < tiles && ok; ++x) {
-                    ok = wait_or_abort(&sh.p_ready[x], j & 1, abort);
+                for (int j = 0; j < 2 && j < steps && ok; ++j) {
+                    ok = wait_or_abort(&sh.k_full[j], 0, abort);
                     if (!ok) break;
                     tc_fence_after();
-                    values(x, j);
-                    if (j + 1 < steps) scores(x, j + 1);
+                    scores(j, j);
+                    done(&sh.k_empty[j]);
                 }
-                if (ok) {
+#pragma unroll 1
+                for (int j = 0; j < steps && ok; ++j) {
+                    const int st = j & 1;
+                    ok = wait_or_abort(&sh.v_full[st], j >> 1 & 1, abort) && wait_or_abort(&sh.p_ready[st], j >> 1 & 1, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    values(st, j, j < 2);
                     done(&sh.v_empty[st]);
-                    if (j + 1 < steps) done(&sh.k_empty[nx]);
+                    if (j + 2 < steps) {
+                        ok = wait_or_abort(&sh.k_full[st], (j + 2) >> 1 & 1, abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        scores(st, j + 2);
+                        done(&sh.k_empty[st]);
+                    }
+                }
+            } else {
+                if (ok) {
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int x = 0; x < 2; ++x) scores(x, 0);
+                    done(&sh.k_empty[0]);
+                }
+#pragma unroll 1
+                for (int j = 0; j < steps && ok; ++j) {
+                    const int st = j & 1, nx = st ^ 1;
+                    ok = wait_or_abort(&sh.v_full[st], j >> 1 & 1, abort);
+                    if (ok && j + 1 < steps) ok = wait_or_abort(&sh.k_full[nx], (j + 1) >> 1 & 1, abort);
+#pragma unroll 1
+                    for (int x = 0; x < 2 && ok; ++x) {
+                        ok = wait_or_abort(&sh.p_ready[x], j & 1, abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        values(x, j, j == 0);
+                        if (j + 1 < steps) scores(x, j + 1);
+                    }
+                    if (ok) {
+                        done(&sh.v_empty[st]);
+                        if (j + 1 < steps) done(&sh.k_empty[nx]);
+                    }
                 }
             }
             if (!__all_sync(0xffffffffu, ok)) give_up();
@@ -632,14 +661,14 @@ kv_prefill_kernel(AttendArgs a, int splits, int stretch)
     } else {
         // ------------------------------------------------------------- softmax --
         regs_up<kPreSoftmaxRegs>();
-        if (tile < tiles) {
         const uint32_t lanes = uint32_t(warp & 3) << 21;  // TMEM lane 32 (warp % 4) in bits 16 on
         const uint32_t ts = tmem + lanes + tile * 128, to = tmem + lanes + 256 + tile * 128;
         int see = tokens;  // tokens of the stretch that this column sees
         if (mine && a.causal) see = int(max(int64_t(0), min(int64_t(tokens), len - n + col / G + 1 - j0)));
         const int least = __reduce_min_sync(0xffffffffu, see);
         bool ok = true;
-        for (int j = 0; j < steps && ok; ++j) {
+        int i = 0;  // steps of this tile
+        for (int j = turns ? tile : 0; j < steps && ok; j += turns ? 2 : 1, ++i) {
             const int left = see - j * kPreTile;
             const float *ks = sh.ks + j * 8, *vs = sh.vs + j * 8;
             float sc[8], vf[8];  // before the wait: shared memory is slow while products read it
@@ -655,13 +684,13 @@ kv_prefill_kernel(AttendArgs a, int splits, int stretch)
                 whole = whole && sc[b] >= 0.f;
                 sc[b] *= mult;
             }
-            ok = wait_or_abort(&sh.s_full[tile], j & 1, abort);
+            ok = wait_or_abort(&sh.s_full[tile], i & 1, abort);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            tc_fence_after();  // the products of the step before are done too
+            tc_fence_after();  // the products of the tile's step before are done too
             const float top = whole ? step_max(ts, sc) : step_max_masked(ts, ks, mult, left);
             if (m == -INFINITY) m = top;  // nothing seen before: l and O are 0
-            if (__any_sync(0xffffffffu, top > m + kPreRaise)) raise<D>(to, top > m + kPreRaise ? top - m : 0.f, j > 0, m, l);
+            if (__any_sync(0xffffffffu, top > m + kPreRaise)) raise<D>(to, top > m + kPreRaise ? top - m : 0.f, i > 0, m, l);
             const float base = m > -INFINITY ? m : 0.f;
             l += whole ? step_weights(ts, sc, vf, base) : step_weights_masked(ts, ks, vs, mult, base, left);
             tmem_wait_st();
@@ -669,11 +698,39 @@ kv_prefill_kernel(AttendArgs a, int splits, int stretch)
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.p_ready[tile]);
         }
-        if (ok && steps > 0) ok = wait_or_abort(&sh.pv_done[tile], (steps - 1) & 1, abort);
-        if (!__all_sync(0xffffffffu, ok)) {
-            give_up();
-        } else {
-            tc_fence_after();
+        if (ok && i > 0) ok = wait_or_abort(&sh.pv_done[tile], (i - 1) & 1, abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) give_up();
+        tc_fence_after();
+        float z0 = 1.f, z1 = 0.f;  // weights of this tile's sums and the other's
+        float* const other = reinterpret_cast<float*>(sh.k);  // [dim][column]
+        if (turns) {
+            if (tile == 1) {
+                // Every score product is done when one of the last two steps' value products is, so the K operands'
+                // memory is free by now (or, without a step, left alone: nothing was seen then).
+                sh.joined[r] = make_float2(m, l);
+                if (ok && i > 0) {
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        float o[32];
+                        tmem_ld32(to + 32 * c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int d = 0; d < 32; ++d) other[(32 * c + d) * kPreTile + r] = o[d];
+                    }
+                }
+            }
+            named_barrier(1, 256);
+            if (tile == 0) {
+                const float2 y = sh.joined[r];
+                const float top = fmaxf(m, y.x);
+                z0 = m > -INFINITY ? ex2(m - top) : 0.f;
+                z1 = y.x > -INFINITY ? ex2(y.x - top) : 0.f;
+                l = l * z0 + y.y * z1;
+                m = top;
+            }
+        }
+        if (ok && !*abort && (tile == 0 || !turns)) {
             const bool direct = splits == 1 || n > a.max_q;  // (the join leaves out rows that are too long)
             const float scale = direct ? (l == 0.f ? 0.f : vtop / l) : vtop;
             T* out = static_cast<T*>(a.out) + token * a.out_token + head * a.out_head;
@@ -692,26 +749,32 @@ kv_prefill_kernel(AttendArgs a, int splits, int stretch)
                     tmem_wait_ld();
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                    for (int d = 0; d < 32; ++d) o[d] = 0.f;
+                }
+                if (turns) {
+#pragma unroll
+                    for (int d = 0; d < 32; ++d) {
+                        o[d] *= z0;
+                        if (z1 > 0.f) o[d] = fmaf(other[(32 * c + d) * kPreTile + r], z1, o[d]);
+                    }
                 }
                 if (!mine) {
                     // the loads above are the whole warp's
                 } else if (direct) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int k = 0; k < 4; ++k) {
                         T y[8];
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) y[u] = from_float<T>(l == 0.f ? 0.f : o[8 * i + u] * scale);
-                        *reinterpret_cast<uint4*>(out + 32 * c + 8 * i) = *reinterpret_cast<const uint4*>(y);
+                        for (int u = 0; u < 8; ++u) y[u] = from_float<T>(l == 0.f ? 0.f : o[8 * k + u] * scale);
+                        *reinterpret_cast<uint4*>(out + 32 * c + 8 * k) = *reinterpret_cast<const uint4*>(y);
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        *reinterpret_cast<float4*>(po + part * D + 32 * c + 4 * i) =
-                            make_float4(o[4 * i] * scale, o[4 * i + 1] * scale, o[4 * i + 2] * scale, o[4 * i + 3] * scale);
+                    for (int k = 0; k < 8; ++k)
+                        *reinterpret_cast<float4*>(po + part * D + 32 * c + 4 * k) =
+                            make_float4(o[4 * k] * scale, o[4 * k + 1] * scale, o[4 * k + 2] * scale, o[4 * k + 3] * scale);
                 }
             }
-        }
         }
     }
     tc_fence_before();

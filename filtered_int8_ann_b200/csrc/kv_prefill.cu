@@ -608,10 +608,10 @@ kv_prefill_kernel(AttendArgs a, int splits, int stretch)
                     *reinterpret_cast<uint4*>(to + (i * 32 + u) * 128 + ((vc ^ u) << 4)) =
                         make_uint4(out[u][0], out[u][1], out[u][2], out[u][3]);
             }
-            if (j + 1 < steps) load(j + 1);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.v_full[j & 1]);
+            if (j + 1 < steps) load(j + 1);  // (behind the fence, which would wait for these loads)
         }
         if (!ok) give_up();
     } else if (warp >= 8) {
@@ -652,10 +652,10 @@ kv_prefill_kernel(AttendArgs a, int splits, int stretch)
                 *reinterpret_cast<uint4*>(to + i * ROWS * 128 + k0) = swap ? hi : lo;
                 *reinterpret_cast<uint4*>(to + i * ROWS * 128 + k1) = swap ? lo : hi;
             }
-            if (j + 1 < steps) load(j + 1);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.k_full[j & 1]);
+            if (j + 1 < steps) load(j + 1);  // (behind the fence, which would wait for these loads)
         }
         if (!ok) give_up();
     } else {

@@ -80,7 +80,7 @@ def _declare_decode(L: ctypes.CDLL):
     L.st_kv_attend_workspace.argtypes = [cache, i64, i32, i32, i32, i64, ctypes.POINTER(i64)]
     L.st_beam_select.argtypes = [P, i32, i64, P, i32, i32, i32, i32, P, P, P, ctypes.POINTER(_BeamExtras), P, i64, P]
     L.st_beam_select_workspace.argtypes = [i32, i32, i32, i32, ctypes.POINTER(i64)]
-    L.st_beam_reorder.argtypes = [ctypes.POINTER(_BeamState), i32, P, i32, i32, i32, P]
+    L.st_beam_reorder.argtypes = [P, i32, P, i32, i32, i32, P]
     L.st_decode_check.argtypes = [P]
     for f in ("st_kv_plan", "st_kv_append", "st_kv_attend", "st_kv_attend_workspace", "st_beam_select",
               "st_beam_select_workspace", "st_beam_reorder", "st_decode_check"):

@@ -22,7 +22,7 @@ from typing import Optional, Sequence
 
 import torch
 
-from . import _BeamExtras, _BeamState, _KvCache, _check, _stream, lib
+from . import _BeamExtras, _KvCache, _check, _stream, lib
 
 ST_BF16, ST_F16, ST_F32 = 0, 1, 2
 _DTYPES = {torch.bfloat16: ST_BF16, torch.float16: ST_F16, torch.float32: ST_F32}
@@ -304,12 +304,21 @@ def st_beam_reorder(states: Sequence[torch.Tensor], parents: torch.Tensor, out: 
     B, keep = parents.shape
     K = states[0].shape[beam_dim] if states[0].dim() > beam_dim else -1
     pp = _array(parents, _I32, (B, keep), "parents")
-    made = []
-    table = (_BeamState * len(states))()
+    rows = B * K
+    made, words = [], []  # words: the eight of each st_beam_state
     for i, x in enumerate(states):
         shape = x.shape
         if len(shape) <= beam_dim or shape[beam_dim - 1] != B or shape[beam_dim] != K:
             raise ValueError(f"state {i} must have {B} requests of {K} beams at dimension {beam_dim}")
+        size = x.element_size()
+        if out is None and beam_dim == 1 and stream is None and rows and x.is_contiguous():  # the usual case
+            _on_gpu(x, f"state {i}")
+            n = x.numel() // rows
+            y = _empty_strided_cuda((B, keep, *shape[2:]), (keep * n, n, *x.stride()[2:]), x.dtype)
+            made.append(y)
+            n *= size
+            words += (x.data_ptr(), y.data_ptr(), n, n, n, 1, 0, 0)
+            continue
         new = shape[:beam_dim] + (keep,) + shape[beam_dim + 1:]
         step = _rows(x, beam_dim, f"state {i}")
         if out is None:
@@ -317,14 +326,15 @@ def st_beam_reorder(states: Sequence[torch.Tensor], parents: torch.Tensor, out: 
             y = _empty(new, x.dtype, stream)
         else:
             y = out[i]
-        if out is not None and (y.shape != new or y.dtype != x.dtype):
-            raise ValueError(f"out {i} must be {tuple(new)} {x.dtype}")
-        size = x.element_size()
+            if y.shape != new or y.dtype != x.dtype:
+                raise ValueError(f"out {i} must be {tuple(new)} {x.dtype}")
         layers = (shape[0], size * x.stride(0), size * y.stride(0)) if beam_dim == 2 else (1, 0, 0)
-        table[i] = (x.data_ptr(), y.data_ptr(), size * math.prod(shape[beam_dim + 1:]), size * step,
-                    size * _rows(y, beam_dim, f"out {i}"), *layers)
+        words += (x.data_ptr(), y.data_ptr(), size * math.prod(shape[beam_dim + 1:]), size * step,
+                  size * _rows(y, beam_dim, f"out {i}"), *layers)
         made.append(y)
-    _check(lib().st_beam_reorder(table, len(states), pp, B, K, keep, _stream(stream)), "st_beam_reorder")
+    status = lib().st_beam_reorder((ctypes.c_int64 * len(words))(*words), len(states), pp, B, K, keep, _stream(stream))
+    if status:
+        _check(status, "st_beam_reorder")
     return made
 
 

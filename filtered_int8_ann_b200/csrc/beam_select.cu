@@ -10,9 +10,10 @@
 // The order has to be that of the numbers themselves, so everything that
 // decides between beams is held in 64 bits: with scores near -20 an error of one fp32 rounding
 // (2e-6) would swap neighbours of different beams once in a few hundred kept pairs. exp is
-//   exp(d) = 2^(k/32) * (1 + r + r^2/2 + r^3/6 + r^4/24),  d = (k + f) ln2/32, r = f ln2/32, |r| <= ln2/64
-// in fp64 (relative error below 2e-12 of a term): nine fp64 operations and two
-// shuffles (the 32 powers sit one per lane).
+//   exp(x) = 2^(n/32) * (1 + r + r^2/2 + r^3/6 + r^4/24),  n = rint(32 x / ln2), r = x - n ln2/32, |r| <= ln2/64
+// with r and all that follows in fp64 (relative error below 2e-12 of a term): six fp64 operations, two
+// conversions and two shuffles (the 32 powers sit one per lane). n is taken in fp32, which may only make
+// |r| a few percent larger.
 //
 // Best entries of a stretch: its threads' maxima go into a histogram between
 // their least and largest; the bin edge with `keep` of them at or above it bounds
@@ -20,6 +21,7 @@
 // written. Where equal logits make them too many, a bisection over
 // (logit, index) finds the exact border.
 #include <cfloat>
+#include <type_traits>
 
 #include "decode.cuh"
 
@@ -35,6 +37,7 @@ constexpr int kMergeCap = 2048;   // pairs sorted at the end
 constexpr int kMergeRank = kMergeThreads / 4;  // up to this many are ordered by counting
 constexpr int kMergeUnits = 4096; // stretches listed as holding such pairs
 constexpr int kHistBins = 256;
+constexpr float kSelNear = 16384.f;  // stretches of larger logits are summed the plain way
 
 // One stretch's result.
 struct Stretch {
@@ -69,7 +72,7 @@ __device__ __forceinline__ uint32_t float_key(float x)
 }
 __device__ __forceinline__ uint64_t double_key(double x)
 {
-    const uint64_t u = uint64_t(__double_as_longlong(x));
+    const uint64_t u = uint64_t(__double_as_longlong(x + 0.0));  // -0 becomes 0
     return u ^ (u >> 63 ? ~0ull : 1ull << 63);
 }
 
@@ -197,6 +200,31 @@ __device__ __forceinline__ float edge_of(float m, float inv, int bin)
 __device__ __forceinline__ uint64_t entry_key(float x, uint32_t index) { return uint64_t(float_key(x)) << 32 | (0xffffffffu - index); }
 __device__ __forceinline__ float key_float(uint32_t key) { return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key); }
 
+// The 16 bytes that begin SHIFT bytes behind the 16-byte boundary p, from aligned loads.
+template <int SHIFT>
+__device__ __forceinline__ void load_shifted(const void* p, uint32_t* out)
+{
+    constexpr int Q = SHIFT / 4, ODD = SHIFT % 4 != 0, MORE = Q + ODD;  // words taken from the next 16 bytes
+    const uint4* q = static_cast<const uint4*>(p);
+    const uint4 lo = __ldcs(q);
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, 0, 0, 0, 0};
+    if (MORE == 1) {
+        w[4] = __ldcs(reinterpret_cast<const uint32_t*>(q + 1));
+    } else if (MORE == 2) {
+        const uint2 hi = __ldcs(reinterpret_cast<const uint2*>(q + 1));
+        w[4] = hi.x;
+        w[5] = hi.y;
+    } else if (MORE > 2) {
+        const uint4 hi = __ldcs(q + 1);
+        w[4] = hi.x;
+        w[5] = hi.y;
+        w[6] = hi.z;
+        w[7] = hi.w;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) out[k] = ODD ? __funnelshift_r(w[k + Q], w[k + Q + (ODD ? 1 : 0)], 16) : w[k + Q];
+}
+
 // What a CTA of the first launch shares.
 struct StretchShared {
     uint2 list[2][kListCap];  // entries (logit, token), in one of the two buffers
@@ -301,34 +329,53 @@ beam_stretch_kernel(SelectArgs a, int stretches, int chunks, int cap, Stretch* r
         return;
     }
 
-    // Vectors of 16 aligned bytes; the first may begin before the row, the last end behind it. Chunk j's first element is
-    // the row's element first + j kSelChunk.
+    // Chunk j's first element is the row's element first + j kSelChunk. Which thread takes an element depends on its
+    // index in the row alone, not on the row's alignment, so that equal rows have equal sums to the last bit and their
+    // pairs stand in the order of the beams.
     const T* x = static_cast<const T*>(a.logits) + row * a.stride;
-    const int before = int((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
-    const int first = int(blockIdx.x) * chunks * kSelChunk - before;
+    const int before = int((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));  // elements behind a 16-byte boundary
+    const int first = int(blockIdx.x) * chunks * kSelChunk;
     const uint32_t* allow = nullptr;
     if (a.ex.allow) {
         const int b = row / a.K;
         allow = a.ex.allow + b * a.ex.allow_request_stride + (row - b * a.K) * a.ex.allow_beam_stride;
     }
-    auto load = [&](int c, uint32_t(&v)[WORDS]) {
+    // This thread's elements of the chunk at c, from a row that begins `shift` elements behind a 16-byte boundary; -inf
+    // for those whose vectors are not all of the row.
+    auto load_as = [&](auto shift, int c, uint32_t(&v)[WORDS]) {
+        constexpr int SHIFT = decltype(shift)::value;
 #pragma unroll
         for (int j = 0; j < VECS; ++j) {
             const int e = c + (j * kSelThreads + tid) * PER;
-            if (e >= 0 && e + PER <= a.V) {
-                const uint4 w = __ldcs(reinterpret_cast<const uint4*>(x + e));
-                v[4 * j] = w.x;
-                v[4 * j + 1] = w.y;
-                v[4 * j + 2] = w.z;
-                v[4 * j + 3] = w.w;
-            } else {
+            v[4 * j] = v[4 * j + 1] = v[4 * j + 2] = v[4 * j + 3] = L::kNone;
+            if (e >= SHIFT && e + (SHIFT ? 2 * PER - SHIFT : PER) <= a.V) load_shifted<SHIFT * int(sizeof(T))>(x + e - SHIFT, &v[4 * j]);
+        }
+    };
+    const int reach = before ? 2 * PER - before : PER;
+    auto load = [&](int c, uint32_t(&v)[WORDS]) {
+        switch (before) {
+            case 0: load_as(std::integral_constant<int, 0>{}, c, v); break;
+            case 1: load_as(std::integral_constant<int, 1>{}, c, v); break;
+            case 2: load_as(std::integral_constant<int, 2>{}, c, v); break;
+            case 3: load_as(std::integral_constant<int, 3>{}, c, v); break;
+            case 4: load_as(std::integral_constant<int, 4 % PER>{}, c, v); break;
+            case 5: load_as(std::integral_constant<int, 5 % PER>{}, c, v); break;
+            case 6: load_as(std::integral_constant<int, 6 % PER>{}, c, v); break;
+            default: load_as(std::integral_constant<int, 7 % PER>{}, c, v); break;
+        }
+        const int e0 = c + tid * PER;
+        if (e0 < before || e0 + (VECS - 1) * kSelThreads * PER + reach > a.V) {  // the rest, one by one
+#pragma unroll
+            for (int j = 0; j < VECS; ++j) {
+                const int e = e0 + j * kSelThreads * PER;
+                if (e >= a.V || (e >= before && e + reach <= a.V)) continue;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     uint32_t w = L::kNone;
 #pragma unroll
                     for (int u = 0; u < IN; ++u) {
                         const int at = e + k * IN + u;
-                        if (at >= 0 && at < a.V) {
+                        if (at < a.V) {
                             if (IN == 1) w = L::bits(x, at);
                             else w = (w & (u ? 0xffffu : 0xffff0000u)) | L::bits(x, at) << (16 * u);
                         }
@@ -346,14 +393,17 @@ beam_stretch_kernel(SelectArgs a, int stretches, int chunks, int cap, Stretch* r
     }
     __syncthreads();
     const uint32_t keep = uint32_t(a.keep);
+    // the lane's power of two 2^(lane/32) as two words, the high one less what adding n << 15 brings from n's low bits
     const double power = kPowers32.v[lane];
-    const int power_hi = __double2hiint(power), power_lo = __double2loint(power);
-    constexpr double kC = 46.166241308446828384;  // 32 / ln 2
-    constexpr double kMagic = 6755399441055744.0; // 1.5 * 2^52: adding it leaves the nearest integer in the low bits
-    constexpr double z = 0.0216608493924982908;   // ln 2 / 32
+    int power_hi = __double2hiint(power) - (lane << 15);
+    const int power_lo = __double2loint(power);
+    constexpr float kC = 46.166241308446828384f;  // 32 / ln 2
+    constexpr float kMagic = 12582912.f;          // 1.5 * 2^23: adding it leaves the nearest integer in the low bits
+    constexpr double kStep = 0.0216608493924982908;   // ln 2 / 32
     bool known = false;          // a reference for the exponentials: the maximum of the first chunk that has any
     float ref = 0.f, most = -INFINITY;
-    double mc = 0.0, part[2] = {0.0, 0.0};
+    int ref_exp = 0;             // the exponentials are held over 2^ref_exp, about exp(ref)
+    double part[2] = {0.0, 0.0};
     uint32_t floor2 = 0;
     float edge = -FLT_MAX;       // entries from here up are candidates (`above`: only those above it)
     bool above = false;
@@ -376,15 +426,11 @@ beam_stretch_kernel(SelectArgs a, int stretches, int chunks, int cap, Stretch* r
         // the row's index of element u of this thread's word k
         auto index_of = [&](int k, int u) { return c0 + ((k / 4) * kSelThreads + tid) * PER + (k % 4) * IN + u; };
         if (allow) {
-            const int words = (a.V + 31) / 32;
 #pragma unroll
             for (int i = 0; i < VECS; ++i) {
-                const int e = c0 + (i * kSelThreads + tid) * PER;
-                if (e + PER <= 0 || e >= a.V) continue;
-                const int at = e < 0 ? 0 : e;  // bits of elements at .. at + PER
-                const int w = at >> 5;
-                const uint32_t lo = allow[w], hi = w + 1 < words ? allow[w + 1] : 0u;
-                const uint32_t bits = __funnelshift_r(lo, hi, uint32_t(at & 31)) << uint32_t(at - e);
+                const int e = c0 + (i * kSelThreads + tid) * PER;  // a multiple of 8 or 4: the bits are one word's
+                if (e >= a.V) continue;
+                const uint32_t bits = allow[e >> 5] >> (e & 31);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[4 * i + k] = L::keep(v[4 * i + k], bits >> (k * IN));
             }
@@ -429,9 +475,10 @@ beam_stretch_kernel(SelectArgs a, int stretches, int chunks, int cap, Stretch* r
             }
             known = true;
             ref = m;
-            mc = double(m) * -kC;
+            ref_exp = __float2int_rn(fminf(fmaxf(m, -kSelNear), kSelNear) * 1.44269504f);
+            power_hi -= ref_exp << 20;
             floor2 = L::both(m - 700.f);  // exp(-700) is nothing next to 1; takes the place of -inf and NaN
-            if (fabsf(m) > 0x1p20f && tid == 0) sh.slow = 1;  // m - 700 is not a number near m
+            if (fabsf(m) > kSelNear && tid == 0) sh.slow = 1;
             // The edge: the chunk's threads' (or, for many, vectors') maxima in a histogram; the bin that `keep` of them
             // reach bounds the chunk's keep-th logit from below.
             const float inv = bin_scale(m - least, kHistBins);
@@ -479,13 +526,12 @@ beam_stretch_kernel(SelectArgs a, int stretches, int chunks, int cap, Stretch* r
                 const uint32_t w = L::max2(v[4 * i + k], floor2);
 #pragma unroll
                 for (int u = 0; u < IN; ++u) {
-                    const double y = fma(double(L::get(w, u)), kC, mc);
-                    const double t = y + kMagic;
-                    const double r = y - (t - kMagic);
-                    const int n = __double2loint(t);
+                    const float y = L::get(w, u), t = fmaf(y, kC, kMagic);
+                    const int n = __float_as_int(t);
+                    const double r = fma(double(t - kMagic), -kStep, double(y));
                     const int hi = __shfl_sync(0xffffffffu, power_hi, n), lo = __shfl_sync(0xffffffffu, power_lo, n);
-                    const double scaled = __hiloint2double(hi + ((n >> 5) << 20), lo);
-                    const double p = fma(r, fma(r, fma(r, fma(r, z * z * z * z / 24, z * z * z / 6), z * z / 2), z), 1.0);
+                    const double scaled = __hiloint2double(hi + (n << 15), lo);
+                    const double p = fma(r, fma(r, fma(r, fma(r, 1.0 / 24, 1.0 / 6), 0.5), 1.0), 1.0);
                     part[(k + u) & 1] = fma(scaled, p, part[(k + u) & 1]);
                 }
             }
@@ -569,7 +615,7 @@ beam_stretch_kernel(SelectArgs a, int stretches, int chunks, int cap, Stretch* r
         double s = 0.0;
         const int end = min(a.V, first + chunks * kSelChunk);
 #pragma unroll 1
-        for (int e = max(first, 0) + tid; e < end; e += kSelThreads) {
+        for (int e = first + tid; e < end; e += kSelThreads) {
             const float y = L::one(x, e);
             const double d = double(y) - double(m);
             if ((!allow || (allow[e >> 5] >> (e & 31) & 1u)) && y < INFINITY && d >= -700.0) s += exp(d);
@@ -584,7 +630,7 @@ beam_stretch_kernel(SelectArgs a, int stretches, int chunks, int cap, Stretch* r
     } else {
 #pragma unroll
         for (int w = 0; w < kSelThreads / 32; ++w) total += sh.sum[w];
-        total *= exp(double(ref) - double(m));
+        total *= exp(ref_exp * 0.693147180559945309417 - double(m));
     }
     // the entries: no more than a list holds
     __syncthreads();
@@ -923,11 +969,11 @@ beam_merge_kernel(SelectArgs a, int stretches, int cap, const Stretch* res, cons
 }
 
 // Chunks per stretch: as many as leave the GPU three CTAs per place (kSelPlaces), and their candidates (keep and a
-// few more each) the list's room, at most 16. A stretch begins at a 16-byte boundary, up to 7 elements before the row.
+// few more each) the list's room, at most 16. 
 static int select_chunks(int64_t rows, int32_t V, int32_t keep, int size)
 {
     const int chunk = kSelChunkBytes / size;
-    const int64_t all = (V + 7 + chunk - 1) / chunk;
+    const int64_t all = (V + chunk - 1) / chunk;
     int64_t chunks = rows * all / (3 * kSelPlaces);
     if (chunks > kListCap / 2 / keep) chunks = kListCap / 2 / keep;
     return int(chunks < 1 ? 1 : chunks > 16 ? 16 : chunks > all ? all : chunks);
@@ -935,7 +981,7 @@ static int select_chunks(int64_t rows, int32_t V, int32_t keep, int size)
 static int select_stretches(int64_t rows, int32_t V, int32_t keep, int size)
 {
     const int64_t stretch = int64_t(select_chunks(rows, V, keep, size)) * (kSelChunkBytes / size);
-    return int((V + 7 + stretch - 1) / stretch);
+    return int((V + stretch - 1) / stretch);
 }
 // Entries a stretch may write: room for the bin that holds the border.
 static int select_cap(int32_t V, int32_t keep)

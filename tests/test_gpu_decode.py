@@ -530,6 +530,28 @@ def test_select_far_apart_logits():
     check_select(x, torch.tensor([[-3e38, -1e-3, 3e38]]), 60)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("K,V,pad,shift", [(7, 3001, 0, 0), (9, 70003, 0, 1), (5, 20000, 3, 2), (256, 33, 0, 0)])
+def test_select_equal_beams_stand_in_order(K, V, pad, shift, dtype):
+    """Beams with the same logits and scores have the same normaliser to the last bit, however their rows are aligned."""
+    g = gen(V + K)
+    row = (3 * torch.randn(V, generator=g)).to(dtype)
+    base = torch.zeros(K * (V + pad) + shift, dtype=dtype)
+    x = base[shift:].view(1, K, V + pad)[..., :V]
+    x.copy_(row.expand(1, K, V))
+    keep = min(512, 3 * K)
+    want = torch.sort(row.float().repeat(K), descending=True, stable=True).indices[:keep]
+    scores, parents, tokens, _ = st.st_beam_select(base.cuda()[shift:].view(1, K, V + pad)[..., :V], torch.full((1, K), -2.5).cuda(), keep)
+    assert parents[0].tolist() == (want // V).tolist() and tokens[0].tolist() == (want % V).tolist()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("centre", [300.0, -16000.0, 16600.0, 60000.0])
+def test_select_logits_far_from_zero(centre, dtype):
+    x = (torch.linspace(-9, 3, 2 * 3 * 9001)[torch.randperm(2 * 3 * 9001, generator=gen(int(abs(centre))))].view(2, 3, 9001) + centre).to(dtype)
+    check_select(x, -torch.rand(2, 3, generator=gen(3)), 40)
+
+
 def test_select_many_rows_go_in_several_launches():
     g = gen(1)
     logits = torch.randn(4400, 16, 8, generator=g)

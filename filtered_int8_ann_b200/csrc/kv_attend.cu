@@ -456,13 +456,15 @@ __global__ void __launch_bounds__(kJoinBlock) kv_join_kernel(AttendArgs a, int s
     const int G = a.q_heads / a.c.kv_heads;
     int lo;
     int64_t token, head;
+    // Every CTA waits for the stretches' launch, those without work too: what follows this launch then follows that one.
+    auto wait = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
     if (per_row > 0) {  // per_row columns of each row and cache head
         const int64_t unit = blockIdx.x / per_row;
         const int col = int(blockIdx.x - unit * per_row);
         lo = int(unit / a.c.kv_heads);
         token = int64_t(max(a.row_start[lo], 0)) + col / G;
         head = (unit - int64_t(lo) * a.c.kv_heads) * G + col % G;
-        if (token >= min(a.row_start[lo + 1], int(a.T))) return;
+        if (token >= min(a.row_start[lo + 1], int(a.T))) return wait();
     } else {  // the query heads of every token
         token = blockIdx.x / a.q_heads;
         head = blockIdx.x - token * a.q_heads;
@@ -473,19 +475,19 @@ __global__ void __launch_bounds__(kJoinBlock) kv_join_kernel(AttendArgs a, int s
             if (a.row_start[mid + 1] > token) hi = mid;
             else lo = mid + 1;
         }
-        if (lo == a.R || a.row_start[lo] > token) return;
+        if (lo == a.R || a.row_start[lo] > token) return wait();
     }
     const int n = a.row_start[lo + 1] - a.row_start[lo];
     const int64_t cols = int64_t(n) * G;
     int64_t len = max(a.lens[lo], 0);
-    if (n > a.max_q || cols <= a.above_cols || cols > a.most_cols) return;  // written already, or another launch's
+    if (n > a.max_q || cols <= a.above_cols || cols > a.most_cols) return wait();  // written already, or another launch's
     if (len > a.max_len) len = 0;
     const int64_t unit = token * a.q_heads + head;
     const int used = int(max(int64_t(1), (len + stretch - 1) / stretch));
     const float* po = static_cast<const float*>(a.workspace);
     const float* pm = po + a.T * a.q_heads * splits * D + 2 * unit * splits;
     po += unit * splits * D + d;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // what the stretches' launch wrote is read from here on
+    wait();  // what the stretches' launch wrote is read from here on
     float top = -INFINITY;
     for (int i = tid; i < used; i += kJoinBlock) top = fmaxf(top, pm[2 * i]);
 #pragma unroll

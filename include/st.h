@@ -519,7 +519,8 @@ st_status st_kv_append(const st_kv_cache* cache, const void* k, const void* v, s
  * NaN in its output, if it sees anything.
  *
  *   q, out     device bf16 or f16 [T][q_heads][head_dim], strides as in st_kv_append;
- *              out rows behind row_start[R] are left as they were
+ *              out rows behind row_start[R] are left as they were; out may be q itself (same
+ *              address and strides), else it shares no memory with what the call reads
  *   table      device int32 [R][max_blocks], row_start device int32 [R+1] (nondecreasing,
  *              within [0, T]), lens device int32 [R]
  *   max_q      most query tokens of a row (1 to 2^20); max_len: most cached tokens of a

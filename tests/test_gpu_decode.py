@@ -421,6 +421,18 @@ def test_attend_and_append_in_a_cache_beyond_32_bit_offsets():
     assert st.st_decode_check() == st.ST_OK
 
 
+@pytest.mark.parametrize("qs", [[1, 1], [3, 90, 1], [200]])
+def test_attend_in_place(qs):
+    """The output may take the queries' place."""
+    q, codes, scales, table, start, lens = make_attend(41, [3000 + m for m in qs], qs, 2, 4, 64, 16, torch.bfloat16)
+    cache = st.KvCache(codes[0].cuda(), codes[1].cuda(), scales[0].cuda(), scales[1].cuda())
+    q = q.cuda()
+    args = [torch.tensor(x, dtype=torch.int32).cuda() for x in (table, start, lens)] + [max(qs)]
+    want = st.st_kv_attend(cache, q, *args)
+    got = st.st_kv_attend(cache, q, *args, out=q)
+    assert got.data_ptr() == q.data_ptr() and torch.equal(got, want)
+
+
 # ----------------------------------------------------------------- select --
 def check_select(logits, scores, keep, allow=None, finished=None, end=0):
     cuda = lambda x: None if x is None else x.cuda()  # noqa: E731

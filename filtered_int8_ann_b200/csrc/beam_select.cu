@@ -20,6 +20,11 @@
 // the stretch's keep-th logit from below, so only the few logits above it are
 // written. Where equal logits make them too many, a bisection over
 // (logit, index) finds the exact border.
+//
+// 1024 beams of 100003 bf16 logits, a fifth of the beams finished (160 MB are read): 117 us and 11 for the second launch,
+// which hides a part of its 20 behind the first; 24 us would be the bytes'. Bound by instructions: 28 per logit (six of
+// them in fp64), 60% of the issue slots busy; the exponentials are about half of the time. 128 beams of 1021
+// logits: 14.5 us, each launch's chain of barriers.
 #include <cfloat>
 #include <type_traits>
 
@@ -30,11 +35,11 @@ namespace st {
 constexpr int kSelThreads = 256;
 constexpr int kSelVecs = 4;        // 16-byte vectors of a chunk per thread
 constexpr int kSelChunkBytes = kSelThreads * kSelVecs * 16;
-constexpr int kSelPlaces = 4 * 148; // CTAs of the first launch that the GPU holds
+constexpr int kSelPlaces = 4 * 148; // CTAs of the first launch that the GPU holds (three per SM with more registers: 129 us, not 122)
 constexpr int kListCap = 2048;     // entries that a stretch collects
 constexpr int kMergeThreads = 1024;
 constexpr int kMergeCap = 2048;   // pairs sorted at the end
-constexpr int kMergeRank = kMergeThreads / 4;  // up to this many are ordered by counting
+constexpr int kMergeRank = kMergeThreads / 4;  // up to this many are ordered by counting: one pass, no barriers
 constexpr int kMergeUnits = 4096; // stretches listed as holding such pairs
 constexpr int kHistBins = 256;
 constexpr float kSelNear = 16384.f;  // stretches of larger logits are summed the plain way
@@ -419,178 +424,178 @@ beam_stretch_kernel(SelectArgs a, int stretches, int chunks, int cap, Stretch* r
     // holds (equal logits, as a rule), pass 1 goes through them again, a chunk at a time.
     uint32_t v[WORDS];
     for (int pass = 0; pass < 2; ++pass) {
-    for (int j = 0; j < chunks; ++j) {
-        const int c0 = first + j * kSelChunk;
-        if (c0 >= a.V) break;
-        load(c0, v);
-        // the row's index of element u of this thread's word k
-        auto index_of = [&](int k, int u) { return c0 + ((k / 4) * kSelThreads + tid) * PER + (k % 4) * IN + u; };
-        if (allow) {
-#pragma unroll
-            for (int i = 0; i < VECS; ++i) {
-                const int e = c0 + (i * kSelThreads + tid) * PER;  // a multiple of 8 or 4: the bits are one word's
-                if (e >= a.V) continue;
-                const uint32_t bits = allow[e >> 5] >> (e & 31);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[4 * i + k] = L::keep(v[4 * i + k], bits >> (k * IN));
-            }
-        }
-        // this thread's maximum (NaN takes no part); +inf leaves
-        uint32_t top = v[0];
-#pragma unroll
-        for (int k = 1; k < WORDS; ++k) top = L::max2(top, v[k]);
-        float tmax = IN == 1 ? L::get(top, 0) : fmaxf(L::get(top, 0), L::get(top, 1));
-        if (tmax == INFINITY) {
-            tmax = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < WORDS; ++k) {
-                uint32_t on = 0;
-#pragma unroll
-                for (int u = 0; u < IN; ++u) {
-                    const float y = L::get(v[k], u);
-                    on |= (y < INFINITY ? 1u : 0u) << u;
-                    if (y < INFINITY) tmax = fmaxf(tmax, y);
-                }
-                v[k] = L::keep(v[k], on);
-            }
-        }
-        most = fmaxf(most, tmax);
-        if (!known) {
-            sh.hist[tid] = 0;
-            const float wm = warp_max(tmax), wl = warp_min(tmax > -INFINITY ? tmax : INFINITY);
-            if (lane == 0) {
-                sh.max[warp] = wm;
-                sh.min[warp] = wl;
-            }
-            __syncthreads();
-            float m = sh.max[0], least = sh.min[0];
-#pragma unroll
-            for (int w = 1; w < kSelThreads / 32; ++w) {
-                m = fmaxf(m, sh.max[w]);
-                least = fminf(least, sh.min[w]);
-            }
-            if (!(m > -INFINITY)) {  // nothing allowed in this chunk
-                __syncthreads();
-                continue;
-            }
-            known = true;
-            ref = m;
-            ref_exp = __float2int_rn(fminf(fmaxf(m, -kSelNear), kSelNear) * 1.44269504f);
-            power_hi -= ref_exp << 20;
-            floor2 = L::both(m - 700.f);  // exp(-700) is nothing next to 1; takes the place of -inf and NaN
-            if (fabsf(m) > kSelNear && tid == 0) sh.slow = 1;
-            // The edge: the chunk's threads' (or, for many, vectors') maxima in a histogram; the bin that `keep` of them
-            // reach bounds the chunk's keep-th logit from below.
-            const float inv = bin_scale(m - least, kHistBins);
-            if (keep <= kSelThreads / 2) {
-                if (tmax > -INFINITY) atomicAdd(&sh.hist[min(kHistBins - 1, int((m - tmax) * inv))], 1u);
-            } else {
+        for (int j = 0; j < chunks; ++j) {
+            const int c0 = first + j * kSelChunk;
+            if (c0 >= a.V) break;
+            load(c0, v);
+            // the row's index of element u of this thread's word k
+            auto index_of = [&](int k, int u) { return c0 + ((k / 4) * kSelThreads + tid) * PER + (k % 4) * IN + u; };
+            if (allow) {
 #pragma unroll
                 for (int i = 0; i < VECS; ++i) {
-                    const uint32_t w = L::max2(L::max2(v[4 * i], v[4 * i + 1]), L::max2(v[4 * i + 2], v[4 * i + 3]));
-                    const float y = IN == 1 ? L::get(w, 0) : fmaxf(L::get(w, 0), L::get(w, 1));
-                    if (y >= least) atomicAdd(&sh.hist[min(kHistBins - 1, int((m - y) * inv))], 1u);
+                    const int e = c0 + (i * kSelThreads + tid) * PER;  // a multiple of 8 or 4: the bits are one word's
+                    if (e >= a.V) continue;
+                    const uint32_t bits = allow[e >> 5] >> (e & 31);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[4 * i + k] = L::keep(v[4 * i + k], bits >> (k * IN));
                 }
             }
+            // this thread's maximum (NaN takes no part); +inf leaves
+            uint32_t top = v[0];
+#pragma unroll
+            for (int k = 1; k < WORDS; ++k) top = L::max2(top, v[k]);
+            float tmax = IN == 1 ? L::get(top, 0) : fmaxf(L::get(top, 0), L::get(top, 1));
+            if (tmax == INFINITY) {
+                tmax = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < WORDS; ++k) {
+                    uint32_t on = 0;
+#pragma unroll
+                    for (int u = 0; u < IN; ++u) {
+                        const float y = L::get(v[k], u);
+                        on |= (y < INFINITY ? 1u : 0u) << u;
+                        if (y < INFINITY) tmax = fmaxf(tmax, y);
+                    }
+                    v[k] = L::keep(v[k], on);
+                }
+            }
+            most = fmaxf(most, tmax);
+            if (!known) {
+                sh.hist[tid] = 0;
+                const float wm = warp_max(tmax), wl = warp_min(tmax > -INFINITY ? tmax : INFINITY);
+                if (lane == 0) {
+                    sh.max[warp] = wm;
+                    sh.min[warp] = wl;
+                }
+                __syncthreads();
+                float m = sh.max[0], least = sh.min[0];
+#pragma unroll
+                for (int w = 1; w < kSelThreads / 32; ++w) {
+                    m = fmaxf(m, sh.max[w]);
+                    least = fminf(least, sh.min[w]);
+                }
+                if (!(m > -INFINITY)) {  // nothing allowed in this chunk
+                    __syncthreads();
+                    continue;
+                }
+                known = true;
+                ref = m;
+                ref_exp = __float2int_rn(fminf(fmaxf(m, -kSelNear), kSelNear) * 1.44269504f);
+                power_hi -= ref_exp << 20;
+                floor2 = L::both(m - 700.f);  // exp(-700) is nothing next to 1; takes the place of -inf and NaN
+                if (fabsf(m) > kSelNear && tid == 0) sh.slow = 1;
+                // The edge: the chunk's threads' (or, for many, vectors') maxima in a histogram; the bin that `keep` of them
+                // reach bounds the chunk's keep-th logit from below.
+                const float inv = bin_scale(m - least, kHistBins);
+                if (keep <= kSelThreads / 2) {
+                    if (tmax > -INFINITY) atomicAdd(&sh.hist[min(kHistBins - 1, int((m - tmax) * inv))], 1u);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < VECS; ++i) {
+                        const uint32_t w = L::max2(L::max2(v[4 * i], v[4 * i + 1]), L::max2(v[4 * i + 2], v[4 * i + 3]));
+                        const float y = IN == 1 ? L::get(w, 0) : fmaxf(L::get(w, 0), L::get(w, 1));
+                        if (y >= least) atomicAdd(&sh.hist[min(kHistBins - 1, int((m - y) * inv))], 1u);
+                    }
+                }
+                __syncthreads();
+                find_bin<kHistBins>(sh.hist, keep, &sh.bin);
+                __syncthreads();
+                edge = edge_of(m, inv, sh.bin);
+            }
+            // candidates: their indexes go behind the list
+            const uint32_t old = count;
+            if (edge <= tmax) {  // (false where this thread has none)
+                const uint32_t e2 = L::both(edge);
+                // above the edge, which is an entry's value then; or from it on, a step further down where the type rounds it up
+                const uint32_t from = above ? L::up(e2) : L::get(e2, 0) <= edge ? e2 : L::both(edge - fabsf(edge) * 0.01f - FLT_MIN);
+                uint32_t found = 0;
+#pragma unroll
+                for (int k = 0; k < WORDS; ++k) found |= L::reach(v[k], from, k);
+                if (found) {
+                    uint32_t at = old + atomicAdd(&sh.count[pass == 0 ? 0 : j & 3], uint32_t(__popc(found)));
+                    while (found) {
+                        const int bit = __ffs(found) - 1;
+                        found &= found - 1;
+                        if (at < kListCap) sh.list[buf][at].y = uint32_t(index_of(L::word_of(bit), L::part_of(bit)));
+                        ++at;
+                    }
+                }
+            }
+            // exp(x - ref)
+            if (tmax - ref > 600.f) sh.slow = 1;
+#pragma unroll
+            for (int i = 0; i < VECS; ++i) {
+                if (pass > 0 || i * kSelThreads * PER >= a.V - c0) break;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t w = L::max2(v[4 * i + k], floor2);
+#pragma unroll
+                    for (int u = 0; u < IN; ++u) {
+                        const float y = L::get(w, u), t = fmaf(y, kC, kMagic);
+                        const int n = __float_as_int(t);
+                        const double r = fma(double(t - kMagic), -kStep, double(y));
+                        const int hi = __shfl_sync(0xffffffffu, power_hi, n), lo = __shfl_sync(0xffffffffu, power_lo, n);
+                        const double scaled = __hiloint2double(hi + (n << 15), lo);
+                        const double p = fma(r, fma(r, fma(r, fma(r, 1.0 / 24, 1.0 / 6), 0.5), 1.0), 1.0);
+                        part[(k + u) & 1] = fma(scaled, p, part[(k + u) & 1]);
+                    }
+                }
+            }
+            if (pass == 0) continue;
             __syncthreads();
-            find_bin<kHistBins>(sh.hist, keep, &sh.bin);
-            __syncthreads();
-            edge = edge_of(m, inv, sh.bin);
-        }
-        // candidates: their indexes go behind the list
-        const uint32_t old = count;
-        if (edge <= tmax) {  // (false where this thread has none)
-            const uint32_t e2 = L::both(edge);
-            // above the edge, which is an entry's value then; or from it on, a step further down where the type rounds it up
-            const uint32_t from = above ? L::up(e2) : L::get(e2, 0) <= edge ? e2 : L::both(edge - fabsf(edge) * 0.01f - FLT_MIN);
-            uint32_t found = 0;
+            count = old + sh.count[j & 3];
+            if (tid == 0) sh.count[(j + 2) & 3] = 0;  // read last two barriers ago
+            if (count > kListCap) {
+                // Too many: exactly the best `keep` of the list and this chunk's candidates (the logit's order first, then
+                // the lower index). Later entries that equal the last of them come behind it.
+                count = old;
+                fetch();
+                const uint64_t border = list_border<true>(sh, sh.list[buf], old, keep, [&](auto&& f) {
 #pragma unroll
-            for (int k = 0; k < WORDS; ++k) found |= L::reach(v[k], from, k);
-            if (found) {
-                uint32_t at = old + atomicAdd(&sh.count[pass == 0 ? 0 : j & 3], uint32_t(__popc(found)));
-                while (found) {
-                    const int bit = __ffs(found) - 1;
-                    found &= found - 1;
-                    if (at < kListCap) sh.list[buf][at].y = uint32_t(index_of(L::word_of(bit), L::part_of(bit)));
-                    ++at;
-                }
-            }
-        }
-        // exp(x - ref)
-        if (tmax - ref > 600.f) sh.slow = 1;
+                    for (int k = 0; k < WORDS; ++k)
 #pragma unroll
-        for (int i = 0; i < VECS; ++i) {
-            if (pass > 0 || i * kSelThreads * PER >= a.V - c0) break;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t w = L::max2(v[4 * i + k], floor2);
-#pragma unroll
-                for (int u = 0; u < IN; ++u) {
-                    const float y = L::get(w, u), t = fmaf(y, kC, kMagic);
-                    const int n = __float_as_int(t);
-                    const double r = fma(double(t - kMagic), -kStep, double(y));
-                    const int hi = __shfl_sync(0xffffffffu, power_hi, n), lo = __shfl_sync(0xffffffffu, power_lo, n);
-                    const double scaled = __hiloint2double(hi + (n << 15), lo);
-                    const double p = fma(r, fma(r, fma(r, fma(r, 1.0 / 24, 1.0 / 6), 0.5), 1.0), 1.0);
-                    part[(k + u) & 1] = fma(scaled, p, part[(k + u) & 1]);
-                }
-            }
-        }
-        if (pass == 0) continue;
-        __syncthreads();
-        count = old + sh.count[j & 3];
-        if (tid == 0) sh.count[(j + 2) & 3] = 0;  // read last two barriers ago
-        if (count > kListCap) {
-            // Too many: exactly the best `keep` of the list and this chunk's candidates (the logit's order first, then
-            // the lower index). Later entries that equal the last of them come behind it.
-            count = old;
-            fetch();
-            const uint64_t border = list_border<true>(sh, sh.list[buf], old, keep, [&](auto&& f) {
+                        for (int u = 0; u < IN; ++u) {
+                            const float y = L::get(v[k], u);
+                            if (y > -INFINITY && (above ? y > edge : y >= edge)) f(entry_key(y, uint32_t(index_of(k, u))));
+                        }
+                });
+                if (tid == 0) sh.total = 0;
+                __syncthreads();
+                auto take = [&](uint64_t key) {
+                    if (key >= border) {
+                        const uint32_t at = atomicAdd(&sh.total, 1u);
+                        if (at < kListCap) sh.list[buf ^ 1][at] = make_uint2(__float_as_uint(key_float(uint32_t(key >> 32))), 0xffffffffu - uint32_t(key));
+                    }
+                };
+                for (uint32_t k = tid; k < old; k += kSelThreads) take(entry_key(__uint_as_float(sh.list[buf][k].x), sh.list[buf][k].y));
 #pragma unroll
                 for (int k = 0; k < WORDS; ++k)
 #pragma unroll
                     for (int u = 0; u < IN; ++u) {
                         const float y = L::get(v[k], u);
-                        if (y > -INFINITY && (above ? y > edge : y >= edge)) f(entry_key(y, uint32_t(index_of(k, u))));
+                        if (y > -INFINITY && (above ? y > edge : y >= edge)) take(entry_key(y, uint32_t(index_of(k, u))));
                     }
-            });
-            if (tid == 0) sh.total = 0;
-            __syncthreads();
-            auto take = [&](uint64_t key) {
-                if (key >= border) {
-                    const uint32_t at = atomicAdd(&sh.total, 1u);
-                    if (at < kListCap) sh.list[buf ^ 1][at] = make_uint2(__float_as_uint(key_float(uint32_t(key >> 32))), 0xffffffffu - uint32_t(key));
-                }
-            };
-            for (uint32_t k = tid; k < old; k += kSelThreads) take(entry_key(__uint_as_float(sh.list[buf][k].x), sh.list[buf][k].y));
-#pragma unroll
-            for (int k = 0; k < WORDS; ++k)
-#pragma unroll
-                for (int u = 0; u < IN; ++u) {
-                    const float y = L::get(v[k], u);
-                    if (y > -INFINITY && (above ? y > edge : y >= edge)) take(entry_key(y, uint32_t(index_of(k, u))));
-                }
-            buf ^= 1;
-            edge = key_float(uint32_t(border >> 32));
-            above = true;
-            __syncthreads();
-            count = fetched = min(sh.total, uint32_t(kListCap));
-            __syncthreads();
-            if (tid == 0) sh.total = 0;
-        } else if (count > kListCap / 2 && j + 1 < chunks) {
-            fetch();
-            if (list_trim(sh, buf, count, keep, edge, above)) buf ^= 1;
-            fetched = count;
+                buf ^= 1;
+                edge = key_float(uint32_t(border >> 32));
+                above = true;
+                __syncthreads();
+                count = fetched = min(sh.total, uint32_t(kListCap));
+                __syncthreads();
+                if (tid == 0) sh.total = 0;
+            } else if (count > kListCap / 2 && j + 1 < chunks) {
+                fetch();
+                if (list_trim(sh, buf, count, keep, edge, above)) buf ^= 1;
+                fetched = count;
+            }
         }
-    }
-    if (pass > 0) break;
-    __syncthreads();
-    count = sh.count[0];
-    if (count <= kListCap) break;
-    count = 0;
-    __syncthreads();
-    if (tid == 0) sh.count[0] = 0;
-    __syncthreads();
+        if (pass > 0) break;
+        __syncthreads();
+        count = sh.count[0];
+        if (count <= kListCap) break;
+        count = 0;
+        __syncthreads();
+        if (tid == 0) sh.count[0] = 0;
+        __syncthreads();
     }
     if (!known) {  // nothing allowed here
         if (tid == 0) res[unit] = Stretch{0.0, -INFINITY, 0};
@@ -968,8 +973,8 @@ beam_merge_kernel(SelectArgs a, int stretches, int cap, const Stretch* res, cons
     }
 }
 
-// Chunks per stretch: as many as leave the GPU three CTAs per place (kSelPlaces), and their candidates (keep and a
-// few more each) the list's room, at most 16. 
+// Chunks per stretch: as many as leave the GPU three CTAs per place (kSelPlaces; a stretch's first chunk and its end
+// cost about a chunk more), and their candidates (keep and a few more each) the list's room, at most 16. 
 static int select_chunks(int64_t rows, int32_t V, int32_t keep, int size)
 {
     const int chunk = kSelChunkBytes / size;

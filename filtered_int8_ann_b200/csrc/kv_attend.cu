@@ -17,8 +17,11 @@
 //                  the tokens' bytes with byte permutes; B = P^T is S^T's accumulator transposed by movmatrix
 // Each warp copies its next 32 tokens (cp.async, 16 bytes a lane) while it works on
 // the last: 12 warps per SM keep 96 KB of codes under way, where loads to registers kept too
-// few (64 rows of up to 16384 tokens: 404 us). The 16-byte pieces of a 128-byte line are permuted
-// by the token so that both kinds of loads are free of bank conflicts.
+// few (64 rows of up to 16384 tokens, 8 cache heads of 128, 4 query heads each: 404 us; 236 so). The 16-byte pieces of
+// a 128-byte line are permuted by the token so that both kinds of loads are free of bank conflicts.
+// That case reads 1.33 GB at 5.6 TB/s, 86% of a plain copy's rate: blocks of 32 tokens are pieces of 4 KB anywhere in
+// memory, which costs about 7% against neighbouring ones, and the last wave of CTAs is not full. One row of 100003
+// tokens (205 MB): 49 us against 31 at that rate; each CTA's way to its first product and the join are 12 of them.
 // A code becomes fp16 exactly: with the sign bit flipped it is the low byte of 1024 + 128 + code.
 // A query is scaled by a power of two to below 2 (exact in fp16 down to 2^-24 of
 // its largest element). The weights' V factor is p_j vs_j / max vs, at most 1, so fp16's
@@ -29,11 +32,12 @@ namespace st {
 
 constexpr int kDecWarps = 4;
 constexpr int kDecBlock = 32 * kDecWarps;
-constexpr int kDecMaxCols = 32;            // columns (query tokens x heads per cache head) up to which this kernel is taken
+// Columns (query tokens x heads per cache head) up to which this kernel is taken, 16 at a time: with 24 to 32 it takes
+// 256 to 270 us for 32 rows of 8192 tokens and the prompts' kernel 340, with 40 it takes 380 and that one 297.
+constexpr int kDecMaxCols = 32;
 constexpr int kDecGroup = 32;             // tokens a warp takes at a time
 constexpr int kDecSixteens = 4096 / 16 + 2 * kDecWarps * kDecGroup / 16;  // of the longest stretch, and of the stages copied past it
 constexpr int kDecMaxStretch = 4096;      // tokens
-
 
 template <int D, int NT>
 struct DecShared {
@@ -534,7 +538,8 @@ struct DecPlan {
 };
 
 // Stretches, multiples of the longest block. One row fills the GPU's places (3 CTAs per SM) once, all with
-// the same work. Several rows, which may be uneven, get about three CTAs per place, of 256 to 1024 tokens.
+// the same work (100003 tokens: 49 us; in two to four turns 52 to 62). Several rows, which may be uneven, get about
+// three CTAs per place, of 256 to 1024 tokens, so that the long ones' stretches fill in behind the short ones.
 // A short row is one stretch, which needs no join.
 static DecPlan dec_plan(const st_kv_cache& c, int32_t q_heads, int32_t R, int32_t max_q, int64_t max_len)
 {
@@ -585,7 +590,8 @@ template <typename T, int D>
 static cudaError_t launch_join(const AttendArgs& a, int splits, int stretch, int per_row, int64_t ctas, cudaStream_t s)
 {
     const dim3 grid{unsigned(ctas)};
-    // few stretches are joined faster by small CTAs, many heads at a time
+    // few stretches are joined faster by small CTAs, many heads at a time (2048 heads of up to 16: the call takes 236 us, by
+    // 512 threads 256), many by large ones (64 heads of 53: 49 us, by 128 threads 51)
     if (splits <= 16) return launch_dep(kv_join_kernel<T, D, 128>, grid, dim3(128), 0, s, a, splits, stretch, per_row);
     return launch_dep(kv_join_kernel<T, D, 512>, grid, dim3(512), 0, s, a, splits, stretch, per_row);
 }

@@ -101,7 +101,8 @@ def _attend_workspace(kv_heads: int, size: int, dim: int, T: int, heads: int, R:
 class KvCache:
     """An int8 paged cache over caller-owned tensors: k, v int8 [num_blocks,
     kv_heads, block_size, head_dim] and their scales float32 [num_blocks,
-    kv_heads]. KvCache.empty allocates one."""
+    kv_heads]. KvCache.empty allocates one. The calls read the tensors' addresses here, so its fields do not change:
+    other tensors need another KvCache."""
 
     __slots__ = ("k", "v", "k_scale", "v_scale", "num_blocks", "kv_heads", "block_size", "head_dim", "_c", "_ref")
 
@@ -109,12 +110,14 @@ class KvCache:
         shape = k.shape
         if len(shape) != 4:
             raise ValueError("k must be [num_blocks, kv_heads, block_size, head_dim]")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.num_blocks, self.kv_heads, self.block_size, self.head_dim = shape
         scales = shape[:2]
-        c = self._c = _KvCache(_array(k, _I8, shape, "k"), _array(v, _I8, shape, "v"), _array(k_scale, _F32, scales, "k_scale"),
-                               _array(v_scale, _F32, scales, "v_scale"), *shape)
-        self._ref = ctypes.byref(c)
+        c = _KvCache(_array(k, _I8, shape, "k"), _array(v, _I8, shape, "v"), _array(k_scale, _F32, scales, "k_scale"),
+                     _array(v_scale, _F32, scales, "v_scale"), *shape)
+        for name, value in zip(self.__slots__, (k, v, k_scale, v_scale, *shape, c, ctypes.byref(c))):
+            object.__setattr__(self, name, value)
+
+    def __setattr__(self, name, value):
+        raise AttributeError("a KvCache's fields do not change: make another")
 
     @classmethod
     def empty(cls, num_blocks: int, kv_heads: int, block_size: int, head_dim: int, device="cuda"):

@@ -157,3 +157,11 @@ def test_binding_refuses_host_tensors():
         st.st_beam_reorder([logits], z(2, 3, dtype=i32), out=[z(2, 3, 50)])
     with pytest.raises(st.StError):
         st.st_kv_append(c, x, x, z(3, dtype=torch.int64))
+
+
+def test_cache_fields_do_not_change():
+    c = st.KvCache.empty(4, 1, 16, 64, device="cpu")
+    assert (c.num_blocks, c.kv_heads, c.block_size, c.head_dim) == (4, 1, 16, 64) and c.k.shape == c.v.shape == (4, 1, 16, 64)
+    for name in ("k", "v_scale", "num_blocks"):
+        with pytest.raises(AttributeError):
+            setattr(c, name, None)

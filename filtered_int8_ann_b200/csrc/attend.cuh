@@ -56,6 +56,9 @@ __device__ __forceinline__ float pow2_up(float big)
     return __uint_as_float(uint32_t(127 + e) << 23);
 }
 
+// A little above x, so that no product rounded to x exceeds it (and -inf for -inf).
+__device__ __forceinline__ float just_above(float x) { return fmaxf(x, fmaf(fabsf(x), 0x1p-22f, x)); }
+
 // Bytes 128 + code (a code with its sign bit flipped) to fp16 codes, two per
 // register: 0x64 above a byte b is 1024 + b.
 __device__ __forceinline__ void biased_to_half(uint32_t x, uint32_t& lo, uint32_t& hi)

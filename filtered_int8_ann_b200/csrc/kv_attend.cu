@@ -24,8 +24,9 @@
 // tokens (205 MB): 49 us against 31 at that rate; each CTA's way to its first product and the join are 12 of them.
 // A code becomes fp16 exactly: with the sign bit flipped it is the low byte of 1024 + 128 + code.
 // A query is scaled by a power of two to below 2 (exact in fp16 down to 2^-24 of
-// its largest element). The weights' V factor is p_j vs_j / max vs, at most 1, so fp16's
-// 11 bits hold it whatever the scales; maxima, sums and O stay in fp32.
+// its largest element). The V operand's weight is 2^15 p_j vs_j / max vs: p_j is at most 1, so that fp16 holds
+// it with 11 bits down to 2^-29 of the largest and to 2^-40 of it below (many small weights may make up a
+// sum); maxima, sums and O stay in fp32.
 #include "attend.cuh"
 
 namespace st {
@@ -38,6 +39,7 @@ constexpr int kDecMaxCols = 32;
 constexpr int kDecGroup = 32;             // tokens a warp takes at a time
 constexpr int kDecSixteens = 4096 / 16 + 2 * kDecWarps * kDecGroup / 16;  // of the longest stretch, and of the stages copied past it
 constexpr int kDecMaxStretch = 4096;      // tokens
+constexpr float kDecUp = 0x1p15f;         // of the weights in fp16
 
 template <int D, int NT>
 struct DecShared {
@@ -234,8 +236,7 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
 #pragma unroll
     for (int w = 1; w < kDecWarps; ++w) vtop = fmaxf(vtop, s_vmax[w]);
     {
-        const float vinv = vtop > 0.f ? 1.f / vtop : 0.f;
-        for (int i = tid; i < sixteens; i += kDecBlock) sh.vs[i] *= vinv;
+        for (int i = tid; i < sixteens; i += kDecBlock) sh.vs[i] = vtop > 0.f ? __fdiv_rn(sh.vs[i], vtop) * kDecUp : 0.f;
     }
     __syncthreads();
     int least_seen = 0x7fffffff;  // of the whole warp's columns: tiles below it need no mask
@@ -342,8 +343,9 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
                 float shrink[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    shrink[i] = mx[nt][i] > m[nt][i] ? ex2(m[nt][i] - mx[nt][i]) : 1.f;
-                    m[nt][i] = mx[nt][i];
+                    const float up = mx[nt][i] > m[nt][i] ? just_above(mx[nt][i]) : m[nt][i];
+                    shrink[i] = up > m[nt][i] ? ex2(m[nt][i] - up) : 1.f;
+                    m[nt][i] = up;
                     l[nt][i] *= shrink[i];
                 }
 #pragma unroll
@@ -436,12 +438,12 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
         const int64_t token = start + col / G, head = hk * G + col % G;
         if (splits == 1) {
             static_cast<T*>(a.out)[token * a.out_token + head * a.out_head + d] =
-                from_float<T>(sum == 0.f ? 0.f : val * vtop / sum);
+                from_float<T>(sum == 0.f ? 0.f : val / (kDecUp * sum) * vtop);
         } else {
             const int64_t part = (token * a.q_heads + head) * splits + split;
             float* po = static_cast<float*>(a.workspace);
             float* pm = po + a.T * a.q_heads * splits * D;
-            po[part * D + d] = val * vtop;
+            po[part * D + d] = val * (1.f / kDecUp) * vtop;
             if (d == 0) {
                 pm[2 * part] = top;
                 pm[2 * part + 1] = sum;

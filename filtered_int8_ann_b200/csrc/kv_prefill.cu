@@ -18,7 +18,7 @@
 // Codes are exact in fp16; a block's K scale multiplies its scores, and its V scale (over the
 // largest of the stretch) the weights, both in fp32. A weight is p = 2^(s - M) with M
 // raised only when a score exceeds it by 8 (then O is rescaled in TMEM): p
-// stays below 2^8, fine for fp16 and for the fp32 sum.
+// is at most 2^8, and 2^7 times it and its V factor fits into fp16 and is held with 11 bits down to 2^-21.
 //
 // 4 rows of 2048 queries over up to 8192 tokens, 8 cache heads of 128 and 4 query heads each (0.28 PFLOP): 456 us, 0.62
 // PFLOP/s. A pair of tiles takes 4500 to 5600 cycles per 128 tokens, of which the products are 2570: a tile's S, its
@@ -49,6 +49,7 @@ constexpr int kPreMaxBlocks = kPreMaxStretch / 16;
 constexpr int kPreStages = 2;  // of K and V operands
 constexpr uint32_t kPreWaitLimit = 1u << 22;
 constexpr float kPreRaise = 8.f;  // a score this far above the reference raises it
+constexpr float kPreUp = 0x1p7f;  // of the weights in fp16
 
 template <int D>
 struct PreShared {
@@ -472,8 +473,7 @@ kv_prefill_kernel(AttendArgs a, int splits, int stretch)
 #pragma unroll
     for (int w = 0; w < kPreBlock / 32; ++w) vtop = fmaxf(vtop, sh.vtop[w]);
     {
-        const float vinv = vtop > 0.f ? 1.f / vtop : 0.f;
-        for (int i = tid; i < steps * (kPreTile / 16); i += kPreBlock) sh.vs[i] *= vinv;
+        for (int i = tid; i < steps * (kPreTile / 16); i += kPreBlock) sh.vs[i] = vtop > 0.f ? __fdiv_rn(sh.vs[i], vtop) * kPreUp : 0.f;
     }
     __syncthreads();
     volatile int32_t* abort = &sh.abort;
@@ -697,7 +697,7 @@ kv_prefill_kernel(AttendArgs a, int splits, int stretch)
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();  // the products of the tile's step before are done too
-            const float top = whole ? step_max(ts, sc) : step_max_masked(ts, ks, mult, left);
+            const float top = just_above(whole ? step_max(ts, sc) : step_max_masked(ts, ks, mult, left));
             if (m == -INFINITY) m = top;  // nothing seen before: l and O are 0
             if (__any_sync(0xffffffffu, top > m + kPreRaise)) raise<D>(to, top > m + kPreRaise ? top - m : 0.f, i > 0, m, l);
             const float base = m > -INFINITY ? m : 0.f;
@@ -741,7 +741,7 @@ kv_prefill_kernel(AttendArgs a, int splits, int stretch)
         }
         if (ok && !*abort && (tile == 0 || !turns)) {
             const bool direct = splits == 1 || n > a.max_q;  // (the join leaves out rows that are too long)
-            const float scale = direct ? (l == 0.f ? 0.f : vtop / l) : vtop;
+            const float scale = direct ? (l == 0.f ? 0.f : 1.f / (kPreUp * l)) : 1.f / kPreUp;  // vtop may be next to nothing
             T* out = static_cast<T*>(a.out) + token * a.out_token + head * a.out_head;
             const int64_t part = (token * a.q_heads + head) * splits + split;
             float* po = static_cast<float*>(a.workspace);
@@ -774,14 +774,15 @@ kv_prefill_kernel(AttendArgs a, int splits, int stretch)
                     for (int k = 0; k < 4; ++k) {
                         T y[8];
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) y[u] = from_float<T>(l == 0.f ? 0.f : o[8 * k + u] * scale);
+                        for (int u = 0; u < 8; ++u) y[u] = from_float<T>(l == 0.f ? 0.f : o[8 * k + u] * scale * vtop);
                         *reinterpret_cast<uint4*>(out + 32 * c + 8 * k) = *reinterpret_cast<const uint4*>(y);
                     }
                 } else {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         *reinterpret_cast<float4*>(po + part * D + 32 * c + 4 * k) =
-                            make_float4(o[4 * k] * scale, o[4 * k + 1] * scale, o[4 * k + 2] * scale, o[4 * k + 3] * scale);
+                            make_float4(o[4 * k] * scale * vtop, o[4 * k + 1] * scale * vtop, o[4 * k + 2] * scale * vtop,
+                                        o[4 * k + 3] * scale * vtop);
                 }
             }
         }

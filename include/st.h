@@ -531,8 +531,9 @@ st_status st_kv_append(const st_kv_cache* cache, const void* k, const void* v, s
  *              st_kv_attend_workspace gives (NULL when that is 0)
  *
  * Products are taken in fp16 with fp32 sums: codes are exact there, a query is
- * scaled by a power of two to its largest element first, and softmax weights
- * carry 11 bits; maxima, sums and outputs are held in fp32 and rounded once.
+ * scaled by a power of two to its largest element first, and a softmax weight times its
+ * block's V scale carries 11 bits, or is off by 2^-32 of the largest; maxima, sums and
+ * outputs are held in fp32 and rounded once.
  *
  * Errors: INVALID_ARG (null or non-device pointer, misaligned arrays or strides,
  * q_heads not a multiple of kv_heads, sizes outside those above, a workspace that is too small),

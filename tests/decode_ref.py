@@ -134,7 +134,7 @@ def attend(q, codes_k, codes_v, scale_k, scale_v, table, start, lens, scale, cau
 
 
 def attend_tolerance(out, parts, dtype, D):
-    """Output rounding (half a step); each weight's rounding to 11 bits, half a
+    """Output rounding (half a step: eps / 2 of the value, tiny * eps / 2 below the normal numbers); each weight's rounding to 11 bits, half a
     step 2^-11 of it or 2^-25 of the largest (which is 1 before the division by
     a sum of at least 1); scores off by D + 8 fp32 roundings of their terms'
     sizes (the part of a query lost below fp16's range is within them), which
@@ -142,8 +142,9 @@ def attend_tolerance(out, parts, dtype, D):
     exponentials and sums."""
     mass, peak, big, keys = parts
     half = torch.finfo(dtype).eps / 2
+    least = torch.finfo(dtype).tiny * half  # steps of subnormals are tiny * eps
     score = (D + 8) * 2.0 ** -24 * big
-    return half * out.abs() + mass * (2.0 ** -11 + 2.0 ** -20 + 2 * score) * (1 + half) + keys * 2.0 ** -25 * peak * 2 + 1e-7 * (dtype == torch.float16)
+    return half * out.abs() + least + mass * (2.0 ** -11 + 2.0 ** -20 + 2 * score) * (1 + half) + keys * 2.0 ** -25 * peak * 2 + 1e-7 * (dtype == torch.float16)
 
 
 def select(logits, scores, keep, allow=None, finished=None, end=0):

@@ -337,6 +337,35 @@ def test_attend_one_weight_takes_all():
     check_attend(*a)
 
 
+@pytest.mark.parametrize("queries", [1, 40])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_many_small_weights_make_up_the_sum(queries, D):
+    """One key takes all of the softmax but its value is 0; each of the others weighs 2^-22 of it. Tolerance: the output's
+    half step, the weights' rounding to 11 bits or 2^-32 (2^-10 of 2^-22), 2^-16 for fp32 scores near 22 and sums."""
+    n, S = 40000, 64
+    blocks = n // S
+    codes = [torch.zeros(blocks, 1, S, D, dtype=torch.int8) for _ in range(2)]
+    codes[0][3, 0, 5, 0] = 100
+    codes[1][:] = 100
+    codes[1][3, 0, 5] = 0
+    scales = [torch.full((blocks, 1), 0.25) for _ in range(2)]
+    q = torch.zeros(queries, 1, D)
+    q[..., 0] = 1.0
+    got = st.st_kv_attend(st.KvCache(*(x.cuda() for x in codes), *(x.cuda() for x in scales)), q.half().cuda(),
+                          torch.arange(blocks, dtype=torch.int32)[None].cuda(), torch.tensor([0, queries], dtype=torch.int32).cuda(),
+                          torch.tensor([n], dtype=torch.int32).cuda(), queries, scale=22 * math.log(2) / 25, causal=False)
+    want = 25.0 * (n - 1) * 2.0 ** -22 / (1 + (n - 1) * 2.0 ** -22)
+    assert bool(((got.cpu().double() - want).abs() <= want * (2.0 ** -11 + 2.0 ** -10 + 2.0 ** -16)).all())
+
+
+def test_attend_tiny_value_scales():
+    """V scales below fp32's normal numbers, as a caller's own cache may hold."""
+    q, codes, scales, table, start, lens = make_attend(14, [300, 90], [1, 40], 1, 2, 64, 16, torch.bfloat16)
+    scales[1][:] = 2.0 ** -140
+    got = check_attend(q, codes, scales, table, start, lens)
+    assert bool(got.isfinite().all())
+
+
 def test_attend_scales_of_blocks_far_apart_and_zero():
     q, codes, scales, table, start, lens = make_attend(10, [400, 90], [1, 5], 2, 4, 64, 16, torch.float16)
     for i in range(2):

@@ -104,7 +104,7 @@ class KvCache:
     kv_heads]. KvCache.empty allocates one. The calls read the tensors' addresses here, so its fields do not change:
     other tensors need another KvCache."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "num_blocks", "kv_heads", "block_size", "head_dim", "_c", "_ref")
+    __slots__ = ("_tensors", "_shape", "_c", "_ref")
 
     def __init__(self, k, v, k_scale, v_scale):
         shape = k.shape
@@ -113,11 +113,19 @@ class KvCache:
         scales = shape[:2]
         c = _KvCache(_array(k, _I8, shape, "k"), _array(v, _I8, shape, "v"), _array(k_scale, _F32, scales, "k_scale"),
                      _array(v_scale, _F32, scales, "v_scale"), *shape)
-        for name, value in zip(self.__slots__, (k, v, k_scale, v_scale, *shape, c, ctypes.byref(c))):
-            object.__setattr__(self, name, value)
+        self._tensors = k, v, k_scale, v_scale
+        self._shape = shape
+        self._c = c
+        self._ref = ctypes.byref(c)
 
-    def __setattr__(self, name, value):
-        raise AttributeError("a KvCache's fields do not change: make another")
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    k_scale = property(lambda self: self._tensors[2])
+    v_scale = property(lambda self: self._tensors[3])
+    num_blocks = property(lambda self: self._shape[0])
+    kv_heads = property(lambda self: self._shape[1])
+    block_size = property(lambda self: self._shape[2])
+    head_dim = property(lambda self: self._shape[3])
 
     @classmethod
     def empty(cls, num_blocks: int, kv_heads: int, block_size: int, head_dim: int, device="cuda"):
@@ -175,7 +183,7 @@ def st_kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.
                  sources: Optional[torch.Tensor] = None, stream=None):
     """Quantise keys and values [T, kv_heads, head_dim] (bfloat16 or float16,
     any multiple-of-8 strides) into the cache's slots int64 [T]."""
-    heads, dim = cache.kv_heads, cache.head_dim
+    _, heads, _, dim = cache._shape
     pk, kt, kh = _vectors(k, heads, dim, "k")
     pv, vt, vh = _vectors(v, heads, dim, "v")
     T = k.shape[0]
@@ -194,14 +202,14 @@ def st_kv_attend(cache: KvCache, q: torch.Tensor, table: torch.Tensor, row_start
     tokens (table int32 [R, max_blocks], row_start int32 [R + 1], lens int32 [R]).
     max_q and max_len bound a row's query and cached tokens; scale defaults to
     head_dim ** -0.5. `out` rows behind row_start[R] are left as they were (a new `out` holds anything there)."""
-    dim = cache.head_dim
+    _, kv_heads, size, dim = cache._shape
     pq, qt, qh = _vectors(q, None, dim, "q")
     T, heads, _ = q.shape
     if table.dim() != 2:
         raise ValueError("table must be [R, max_blocks]")
     R, width = table.shape
     if max_len is None:
-        max_len = width * cache.block_size
+        max_len = width * size
     pt = _array(table, _I32, (R, width), "table")
     ps, pl = _array(row_start, _I32, (R + 1,), "row_start"), _array(lens, _I32, (R,), "lens")
     if out is None:
@@ -217,16 +225,17 @@ def st_kv_attend(cache: KvCache, q: torch.Tensor, table: torch.Tensor, row_start
         # tokens apart from each other, and heads: one inside the other either way
         _need((T <= 1 or ot >= dim) and (heads <= 1 or oh >= dim) and
               (T <= 1 or heads <= 1 or ot >= (heads - 1) * oh + dim or oh >= (T - 1) * ot + dim), "out's vectors must not overlap")
-    need = _attend_workspace(cache.kv_heads, cache.block_size, dim, T, heads, R, max_q, max_len)
+    need = _attend_workspace(kv_heads, size, dim, T, heads, R, max_q, max_len)
     room = 0
     if workspace is not None:
         room = workspace.numel() * workspace.element_size()
     elif need:
         workspace, room = _empty1(need, torch.uint8, stream), need
-    _check(lib().st_kv_attend(cache._ref, pq, _DTYPES[q.dtype], T, heads, qt, qh, pt, width, ps, pl, R, max_q, max_len,
-                              dim ** -0.5 if scale is None else scale, int(causal), po, ot, oh,
-                              None if workspace is None else workspace.data_ptr(), room, _stream(stream)),
-           "st_kv_attend")
+    status = lib().st_kv_attend(cache._ref, pq, _DTYPES[q.dtype], T, heads, qt, qh, pt, width, ps, pl, R, max_q, max_len,
+                                dim ** -0.5 if scale is None else scale, int(causal), po, ot, oh,
+                                None if workspace is None else workspace.data_ptr(), room, _stream(stream))
+    if status:
+        _check(status, "st_kv_attend")
     return out
 
 

@@ -18,8 +18,8 @@
 // launch over the whole GPU, since the cluster's SMs alone store too slowly.
 //
 // Bound by latency: a dozen steps that wait for one another, each a barrier and one or two loads; the bytes (a few
-// hundred KB at most) take under 1 us. 64 rows of 2000 tokens get one more in 8.2 us on the device, 1024 prompts of 1000
-// tokens their slots in 22 us (two launches).
+// hundred KB at most) take under 1 us. 64 rows of 2000 tokens get one more in 8.2 us on the device, 1024 prompts of up to 1000
+// tokens their slots in 20 us (two launches).
 #include <cooperative_groups.h>
 
 #include "decode.cuh"
@@ -31,7 +31,7 @@ namespace st {
 constexpr int kPlanCtas = 8;      // CTAs of the cluster for large calls
 constexpr int kPlanBlock = 1024;
 // Calls up to these sizes take one CTA (64 rows of 2000 tokens: 8.2 us, a cluster 15.7), larger ones the cluster (1024
-// rows: 22 us, one CTA 35).
+// rows: 20 us, one CTA 33).
 constexpr int kPlanSmallRows = 256;
 constexpr int kPlanSmallBlocks = 131072;
 constexpr int64_t kPlanSmallEntries = 32768;
@@ -318,15 +318,18 @@ constexpr int kSlotStretch = 64;   // tokens per warp: more of them wait longer 
 __global__ void __launch_bounds__(kSlotBlock) kv_slots_kernel(PlanArgs a)
 {
     dep_enter();
-    const int lane = threadIdx.x & 31, S = a.block_size;
+    const int lane = threadIdx.x & 31, S = a.block_size, shift = 31 - __clz(S);
     const int64_t t0 = (int64_t(blockIdx.x) * (kSlotBlock / 32) + (threadIdx.x >> 5)) * kSlotStretch;
     const int64_t t1 = min(a.T, t0 + kSlotStretch);
     if (t0 >= t1) return;
-    int lo = 0, hi = a.R;  // first row that ends behind t0 (R: none)
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (a.row_start[mid + 1] > t0) hi = mid;
-        else lo = mid + 1;
+    // first row that ends behind t0 (R: none), among lo .. lo + n: 32 rows are looked at a time, since each look waits for
+    // memory
+    int lo = 0;
+    for (int n = a.R; n > 0;) {
+        const int step = (n + 31) / 32, at = lo + (lane + 1) * step - 1;
+        const int before = __popc(__ballot_sync(0xffffffffu, at < lo + n && a.row_start[at + 1] <= t0));
+        n = min(step - 1, n - before * step);
+        lo += before * step;
     }
     constexpr int64_t kNever = int64_t(1) << 40;
     int base = lo;  // lane i: the end of row base + i
@@ -357,11 +360,11 @@ __global__ void __launch_bounds__(kSlotBlock) kv_slots_kernel(PlanArgs a)
             bool mine = true;
             if (row < a.R && a.lens[row] >= 0) {
                 const int have = a.have[row];
-                const int p = have + int(t - a.row_start[row]), c = p / S;
-                mine = have % S == 0 || c != have / S;
+                const int p = have + int(t - a.row_start[row]), c = p >> shift;
+                mine = (have & (S - 1)) == 0 || c != have >> shift;
                 if (mine) {
                     src = a.table[int64_t(row) * a.max_blocks + c];
-                    slot = int64_t(src) * S + (p - c * S);
+                    slot = (int64_t(src) << shift) + (p & (S - 1));
                 }
             }
             if (mine) {
@@ -401,7 +404,7 @@ static cudaError_t launch_plan(const PlanArgs& a, bool all_slots, cudaStream_t s
 cudaError_t launch_kv_plan(const PlanArgs& a, cudaStream_t s)
 {
     // Few tokens per row need no second launch (64 rows of one token: 8.2 us, with it 13.1); many do (1024 rows of 1000:
-    // 22 us, without it 48).
+    // 20 us, without it 48).
     const bool all_slots = a.T <= 4 * int64_t(a.R) + 1024;
     const bool small = a.R <= kPlanSmallRows && a.num_blocks <= kPlanSmallBlocks &&
                        int64_t(a.R) * a.max_blocks <= kPlanSmallEntries;

@@ -10,12 +10,12 @@
 // its warps one each; longer ones (prompts) take the whole CTA, and every
 // element is read once: it waits in registers while the run's maximum is
 // found. Maxima are taken on the 16-bit patterns, two at a time, and codes rounded by adding 1.5 * 2^23:
-// conversions to integers one by one took the prompts' case from 24 to 65 us.
+// with conversions to integers one by one the prompts' case below took 65 us.
 //
 // Bound by bytes: 2 read and 1 written per new element, and the earlier codes
-// of the blocks whose scale grew. 14343 tokens of 8 heads of 128 (88 MB): 24 us, 3.7 TB/s of them; the wait between a
-// run's loads and its stores, and the instructions of the conversion (issue slots 55% busy), keep it from the copy's
-// rate. A step of 256 rows: 8 us, two dependent loads and a launch.
+// of the blocks whose scale grew. 14343 tokens of 8 heads of 128 (88 MB): 20.6 us, 4.3 TB/s of them; the wait between a
+// run's loads and its stores, and the instructions of the conversion (issue slots over half busy), keep it from the
+// copy's rate. A step of 256 rows: 8 us, two dependent loads and a launch.
 #include "decode.cuh"
 
 namespace st {
@@ -193,9 +193,13 @@ __device__ __forceinline__ void append_run(const T* x, int64_t token_stride, int
     if (me == 0) scales[to] = s;
 }
 
+// CTAs that an SM shall hold: eight where a thread holds up to eight vectors of a long run (64 registers are enough then:
+// 14343 tokens 20.6 us, with the five of 84 registers 24), else as many as come.
+constexpr int append_ctas(int D, int S, int per) { return per > 4 && S * D / 8 <= 8 * kAppendBlock ? 8 : 0; }
+
 // PER: tokens whose runs a CTA takes.
 template <typename T, int D, int S, int PER>
-__global__ void __launch_bounds__(kAppendBlock) kv_append_kernel(AppendArgs a)
+__global__ void __launch_bounds__(kAppendBlock, append_ctas(D, S, PER)) kv_append_kernel(AppendArgs a)
 {
     constexpr int WINDOW = (PER + S + 31) / 32 * 32;  // tokens that runs starting here can reach, and more
     __shared__ int64_t s_slot[WINDOW];
@@ -273,7 +277,7 @@ template <typename T, int D, int S>
 static cudaError_t launch_append(const AppendArgs& a, cudaStream_t s)
 {
     // Tokens per CTA: 4 while that leaves the CTAs few (a decode step: a run per warp; 256 tokens of 8 heads 8 us, with a
-    // block's tokens per CTA 12), else a block's, so that a prompt's CTAs have one run each (14343 tokens: 24 us, with 4
+    // block's tokens per CTA 12), else a block's, so that a prompt's CTAs have one run each (14343 tokens: 20.6 us, with 4
     // tokens per CTA 70).
     const bool few = a.T * a.c.kv_heads <= 32768;
     const int per = few ? 4 : S;

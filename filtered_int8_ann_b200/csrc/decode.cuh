@@ -69,6 +69,10 @@ struct AttendArgs {
     // rows that a launch takes, by their columns (query tokens x heads per cache head): more than the first, up to
     // the second
     int32_t above_cols = 0, most_cols = 0x7fffffff;
+    // the columns that have partial sums in the workspace: T * q_heads, numbered by token and head, or, with row_cols > 0,
+    // that many for each row and cache head
+    int64_t parts = 0;
+    int32_t row_cols = 0;
 };
 int64_t kv_attend_workspace(const st_kv_cache& c, int64_t T, int32_t q_heads, int32_t R, int32_t max_q,
                             int64_t max_len);

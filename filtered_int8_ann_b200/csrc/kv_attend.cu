@@ -39,6 +39,7 @@ constexpr int kDecMaxCols = 32;
 constexpr int kDecGroup = 32;             // tokens a warp takes at a time
 constexpr int kDecSixteens = 4096 / 16 + 2 * kDecWarps * kDecGroup / 16;  // of the longest stretch, and of the stages copied past it
 constexpr int kDecMaxStretch = 4096;      // tokens
+constexpr int64_t kDecRoom = int64_t(128) << 20;  // bytes of partial sums beside prompts
 constexpr float kDecUp = 0x1p15f;         // of the weights in fp16
 
 template <int D, int NT>
@@ -440,9 +441,10 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
             static_cast<T*>(a.out)[token * a.out_token + head * a.out_head + d] =
                 from_float<T>(sum == 0.f ? 0.f : val / (kDecUp * sum) * vtop);
         } else {
-            const int64_t part = (token * a.q_heads + head) * splits + split;
+            const int64_t of = a.row_cols > 0 ? (int64_t(row) * a.c.kv_heads + hk) * a.row_cols + col : token * a.q_heads + head;
+            const int64_t part = of * splits + split;
             float* po = static_cast<float*>(a.workspace);
-            float* pm = po + a.T * a.q_heads * splits * D;
+            float* pm = po + a.parts * splits * D;
             po[part * D + d] = val * (1.f / kDecUp) * vtop;
             if (d == 0) {
                 pm[2 * part] = top;
@@ -488,10 +490,10 @@ __global__ void __launch_bounds__(kJoinBlock) kv_join_kernel(AttendArgs a, int s
     int64_t len = max(a.lens[lo], 0);
     if (n > a.max_q || cols <= a.above_cols || cols > a.most_cols) return wait();  // written already, or another launch's
     if (len > a.max_len) len = 0;
-    const int64_t unit = token * a.q_heads + head;
+    const int64_t unit = a.row_cols > 0 ? int64_t(blockIdx.x) : token * a.q_heads + head;  // (the CTAs are numbered so)
     const int used = int(max(int64_t(1), (len + stretch - 1) / stretch));
     const float* po = static_cast<const float*>(a.workspace);
-    const float* pm = po + a.T * a.q_heads * splits * D + 2 * unit * splits;
+    const float* pm = po + a.parts * splits * D + 2 * unit * splits;
     po += unit * splits * D + d;
     wait();  // what the stretches' launch wrote is read from here on
     float top = -INFINITY;
@@ -536,14 +538,21 @@ __global__ void __launch_bounds__(kJoinBlock) kv_join_kernel(AttendArgs a, int s
 
 struct DecPlan {
     int splits, stretch, cols, col_blocks;
-    int per_row;  // most columns of a row
+    int per_row;    // most columns of a row
+    int64_t parts;  // columns with partial sums, and how they are numbered (AttendArgs)
+    int row_cols;
+    int64_t bytes;  // of the workspace: a multiple of 16, the prompts' kernel's part may follow
 };
 
 // Stretches, multiples of the longest block. One row fills the GPU's places (3 CTAs per SM) once, all with
 // the same work (100003 tokens: 49 us; in two to four turns 52 to 62). Several rows, which may be uneven, get about
 // three CTAs per place, of 256 to 1024 tokens, so that the long ones' stretches fill in behind the short ones.
 // A short row is one stretch, which needs no join.
-static DecPlan dec_plan(const st_kv_cache& c, int32_t q_heads, int32_t R, int32_t max_q, int64_t max_len)
+// Partial sums are numbered by token, or by row where that takes less room: beside prompts, and with tokens behind the
+// last row's. Where short rows stand beside prompts, the host knows only that each of them may have kDecMaxCols columns:
+// a workspace above kDecRoom then takes longer stretches (63 rows of up to 65536 tokens beside a prompt of 2048, 8 cache
+// heads of 128, 4 query heads each: 130 MiB and, prompt included, 1198 us; with stretches of 1024 520 MiB and 1504 us).
+static DecPlan dec_plan(const st_kv_cache& c, int64_t T, int32_t q_heads, int32_t R, int32_t max_q, int64_t max_len, bool mixed)
 {
     DecPlan p;
     const int64_t cols = int64_t(max_q) * (q_heads / c.kv_heads);
@@ -563,15 +572,17 @@ static DecPlan dec_plan(const st_kv_cache& c, int32_t q_heads, int32_t R, int32_
     }
     stretch = (stretch + 127) / 128 * 128;
     if (max_len <= 512) stretch = 512;
-    p.splits = int((max_len + stretch - 1) / stretch);
+    const int64_t by_token = T * q_heads, by_row = int64_t(R) * c.kv_heads * cols;
+    p.row_cols = by_row < by_token ? int(cols) : 0;
+    p.parts = by_row < by_token ? by_row : by_token;
+    while (true) {
+        p.splits = int((max_len + stretch - 1) / stretch);
+        p.bytes = p.splits == 1 ? 0 : (p.parts * p.splits * (int64_t(c.head_dim) + 2) * 4 + 15) / 16 * 16;
+        if (!mixed || p.bytes <= kDecRoom || 2 * stretch > kDecMaxStretch) break;
+        stretch *= 2;
+    }
     p.stretch = int(stretch);
     return p;
-}
-
-static int64_t kv_decode_workspace(const st_kv_cache& c, int64_t T, int32_t q_heads, const DecPlan& p)
-{
-    // a multiple of 16 bytes: the prompts' kernel's part may follow
-    return p.splits == 1 ? 0 : (T * q_heads * p.splits * (int64_t(c.head_dim) + 2) * 4 + 15) / 16 * 16;
 }
 
 template <typename T, int D, int NT>
@@ -624,7 +635,6 @@ static cudaError_t launch_kv_decode(const AttendArgs& a, const DecPlan& p, cudaS
 struct AttendPlan {
     bool decode, prefill;
     DecPlan dec;
-    int64_t dec_bytes;  // of the workspace, before the prompts' kernel's
 };
 
 static AttendPlan attend_plan(const st_kv_cache& c, int64_t T, int32_t q_heads, int32_t R, int32_t max_q, int64_t max_len)
@@ -634,18 +644,14 @@ static AttendPlan attend_plan(const st_kv_cache& c, int64_t T, int32_t q_heads, 
     p.prefill = max_q * G > kDecMaxCols;
     p.decode = !p.prefill || (R > 1 && G <= kDecMaxCols);
     p.dec = DecPlan{};
-    p.dec_bytes = 0;
-    if (p.decode) {
-        p.dec = dec_plan(c, q_heads, R, p.prefill ? int32_t(kDecMaxCols / G) : max_q, max_len);
-        p.dec_bytes = kv_decode_workspace(c, T, q_heads, p.dec);
-    }
+    if (p.decode) p.dec = dec_plan(c, T, q_heads, R, p.prefill ? int32_t(kDecMaxCols / G) : max_q, max_len, p.prefill);
     return p;
 }
 
 int64_t kv_attend_workspace(const st_kv_cache& c, int64_t T, int32_t q_heads, int32_t R, int32_t max_q, int64_t max_len)
 {
     const AttendPlan p = attend_plan(c, T, q_heads, R, max_q, max_len);
-    return p.dec_bytes + (p.prefill ? kv_prefill_workspace(c, T, q_heads, R, max_q, max_len) : 0);
+    return p.dec.bytes + (p.prefill ? kv_prefill_workspace(c, T, q_heads, R, max_q, max_len) : 0);
 }
 
 cudaError_t launch_kv_attend(const AttendArgs& args, cudaStream_t s)
@@ -654,13 +660,16 @@ cudaError_t launch_kv_attend(const AttendArgs& args, cudaStream_t s)
     AttendArgs a = args;
     if (p.prefill) {
         a.above_cols = p.decode ? kDecMaxCols : 0;
-        a.workspace = static_cast<char*>(args.workspace) + p.dec_bytes;
+        a.workspace = static_cast<char*>(args.workspace) + p.dec.bytes;
+        a.parts = args.T * args.q_heads;
         const cudaError_t e = launch_kv_prefill(a, s);
         if (e != cudaSuccess) return e;
         a.above_cols = 0;
         a.most_cols = kDecMaxCols;
         a.workspace = args.workspace;
     }
+    a.parts = p.dec.parts;
+    a.row_cols = p.dec.row_cols;
     return p.decode ? launch_kv_decode(a, p.dec, s) : cudaSuccess;
 }
 

@@ -746,7 +746,7 @@ kv_prefill_kernel(AttendArgs a, int splits, int stretch)
             const int64_t part = (token * a.q_heads + head) * splits + split;
             float* po = static_cast<float*>(a.workspace);
             if (mine && !direct) {
-                float* pm = po + a.T * a.q_heads * splits * D;
+                float* pm = po + a.parts * splits * D;
                 pm[2 * part] = m;
                 pm[2 * part + 1] = l;
             }

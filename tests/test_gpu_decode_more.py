@@ -1,0 +1,33 @@
+"""The decode operators on the GPU, further calls: batches whose partial sums are numbered by row or by token."""
+import pytest
+import torch
+
+import filtered_int8_ann_b200 as st
+from test_gpu_decode import check_attend, make_attend
+
+pytestmark = pytest.mark.gpu
+
+
+def widen(table, width):
+    return [row + [-9] * (width - len(row)) for row in table]
+
+
+@pytest.mark.parametrize("lens,qs,heads,group", [
+    ([1300, 40, 900, 2000, 700], [1, 40, 8, 3, 50], 2, 4),     # numbered by row
+    ([1300] + [60] * 19, [33] + [1] * 19, 1, 1),               # by token: few of the columns that the rows may have
+    ([1300, 600, 1], [1, 1, 1], 2, 3)])
+def test_attend_partial_sums(lens, qs, heads, group):
+    """Stretches joined, with tokens behind the last row's and bounds above the rows' own."""
+    q, codes, scales, table, start, lens = make_attend(50, lens, qs, heads, group, 64, 16, torch.float16)
+    for spare in (0, 70):
+        more = torch.cat([q, torch.zeros(spare, *q.shape[1:], dtype=q.dtype)])
+        check_attend(more, codes, scales, table, start, lens)
+        check_attend(more, codes, scales, table, start, lens, max_q=max(qs) + 5)
+
+
+def test_attend_long_stretches_beside_prompts():
+    """Rows that might be long, so many that their partial sums take longer stretches than 1024 tokens."""
+    lens, qs = [2100, 70, 4500, 1030] + [20] * 60, [2, 40, 1, 3] + [1] * 60
+    q, codes, scales, table, start, lens = make_attend(51, lens, qs, 8, 4, 128, 16, torch.bfloat16)
+    for width in (4096, 8192):  # 65536 tokens: stretches of 2048; 131072: of 4096
+        check_attend(q, codes, scales, widen(table, width), start, lens, max_len=16 * width)

@@ -74,6 +74,7 @@ struct AttendArgs {
     int64_t parts = 0;
     int32_t row_cols = 0;
 };
+constexpr int64_t kAttendMaxBytes = int64_t(1) << 48;  // of workspace: sizes that need more are refused
 int64_t kv_attend_workspace(const st_kv_cache& c, int64_t T, int32_t q_heads, int32_t R, int32_t max_q,
                             int64_t max_len);
 cudaError_t launch_kv_attend(const AttendArgs& a, cudaStream_t s);

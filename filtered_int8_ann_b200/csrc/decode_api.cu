@@ -196,8 +196,11 @@ st_status st_kv_attend_workspace(const st_kv_cache* cache, int64_t T, int32_t q_
     if (bytes == nullptr) return ST_ERR_INVALID_ARG;
     *bytes = 0;
     const st_status s = attend_sizes(cache, T, q_heads, R, max_q, max_len);
-    if (s == ST_OK) *bytes = st::kv_attend_workspace(*cache, T, q_heads, R, max_q, max_len);
-    return s;
+    if (s != ST_OK) return s;
+    const int64_t need = st::kv_attend_workspace(*cache, T, q_heads, R, max_q, max_len);
+    if (need > st::kAttendMaxBytes) return ST_ERR_UNSUPPORTED;
+    *bytes = need;
+    return ST_OK;
 }
 
 st_status st_kv_attend(const st_kv_cache* cache, const void* q, st_dtype dtype, int64_t T, int32_t q_heads,
@@ -222,6 +225,7 @@ st_status st_kv_attend(const st_kv_cache* cache, const void* q, st_dtype dtype, 
             !on_device(row_start, dev, 4) || !on_device(lens, dev, 4))
             return ST_ERR_INVALID_ARG;
         const int64_t need = st::kv_attend_workspace(*cache, T, q_heads, R, max_q, max_len);
+        if (need > st::kAttendMaxBytes) return ST_ERR_UNSUPPORTED;
         if (need > 0 && (workspace_bytes < need || !on_device(workspace, dev, 16))) return ST_ERR_INVALID_ARG;
         st::AttendArgs a{*cache, q, dtype, T, q_heads, q_token_stride, q_head_stride, table, max_blocks, row_start, lens,
                          R, max_q, max_len, scale * 1.44269504088896340736f, causal, out, out_token_stride, out_head_stride,

@@ -823,7 +823,10 @@ static PrePlan pre_plan(const st_kv_cache& c, int64_t T, int32_t q_heads, int32_
 int64_t kv_prefill_workspace(const st_kv_cache& c, int64_t T, int32_t q_heads, int32_t R, int32_t, int64_t max_len)
 {
     const PrePlan p = pre_plan(c, T, q_heads, R, max_len);
-    return p.splits == 1 ? 0 : T * q_heads * p.splits * (int64_t(c.head_dim) + 2) * 4;
+    if (p.splits == 1) return 0;
+    // T q_heads is below 2^47, its multiples need not be within 64 bits
+    const int64_t parts = T * q_heads, each = p.splits * (int64_t(c.head_dim) + 2) * 4;
+    return parts > kAttendMaxBytes / each ? kAttendMaxBytes + 1 : parts * each;
 }
 
 template <typename T, int D>

@@ -539,7 +539,7 @@ st_status st_kv_append(const st_kv_cache* cache, const void* k, const void* v, s
  * q_heads not a multiple of kv_heads, sizes outside those above, a workspace that is too small),
  * UNSUPPORTED (the cache outside its limits, R above ST_KV_MAX_ROWS,
  * R * max_blocks or T at 2^31 or above, more than 65535 query heads, or sizes that
- * take more than 2^31 CTAs), CUDA. A used table entry outside the cache hides its
+ * take more than 2^31 CTAs or 2^48 bytes of workspace), CUDA. A used table entry outside the cache hides its
  * tokens and sets the decode error word.
  */
 st_status st_kv_attend(const st_kv_cache* cache, const void* q, st_dtype dtype, int64_t T, int32_t q_heads,

@@ -36,3 +36,12 @@ def test_attend_workspace_of_mixed_batches(lib, T, R, max_q, max_len, group):
 def test_attend_workspace_of_single_tokens(lib):
     """Tokens behind the last row's take no part."""
     assert attend_bytes(lib, 64, 64, 1, 16384) == attend_bytes(lib, 5000, 64, 1, 16384)
+
+
+@pytest.mark.parametrize("T,R,max_q,max_len,heads,group", [
+    (2**31 - 1, 1, 2**20, 2**31 - 1, 1, 65535), (2**31 - 1, 7, 2**20, 2**31 - 1, 1000, 65), (2**31 - 1, 32768, 33, 2**31 - 1, 1024, 1),
+    (2**31 - 1, 32768, 2**20, 2**27, 15, 4369), (2**30, 1, 2**20, 2**30, 4, 16380)])
+def test_attend_workspace_that_no_memory_holds(lib, T, R, max_q, max_len, heads, group):
+    """Sizes whose workspace would be more than 2^48 bytes (and more than 64 bits count) are refused."""
+    assert T * heads * group * -(-max_len // 16384) * 4 * 130 > 2**48
+    assert attend_bytes(lib, T, R, max_q, max_len, heads, group) == (st.ST_ERR_UNSUPPORTED, 0)

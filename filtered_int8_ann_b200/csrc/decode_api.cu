@@ -3,6 +3,7 @@
 #include <cmath>
 #include <mutex>
 #include <new>
+#include <numeric>
 
 #include "decode.cuh"
 
@@ -78,6 +79,57 @@ bool overlap(const void* p, int64_t n, const void* q, int64_t m)
     return n > 0 && m > 0 && a < b + uintptr_t(m) && b < a + uintptr_t(n);
 }
 
+// n0 x n1 vectors of `bytes` bytes, the strides between them in bytes (not negative).
+struct Vectors {
+    const void* p;
+    int64_t n0, s0, n1, s1, bytes;
+    __int128 at() const { return reinterpret_cast<uintptr_t>(p); }
+    __int128 inner() const { return (n1 > 1 ? __int128(n1 - 1) * s1 : 0) + bytes; }  // what the vectors of one n0 span
+    __int128 span() const { return (n0 > 1 ? __int128(n0 - 1) * s0 : 0) + inner(); }
+    Vectors swapped() const { return {p, n1, s1, n0, s0, bytes}; }
+};
+Vectors dense(const void* p, int64_t bytes) { return {p, 1, 0, 1, 0, bytes}; }
+
+// The vectors do not share a byte among themselves: one dimension inside the other.
+bool separate(const Vectors& v)
+{
+    const Vectors w = v.swapped();
+    return (v.n0 <= 1 || v.s0 >= v.bytes) && (v.n1 <= 1 || v.s1 >= v.bytes) &&
+           (v.n0 <= 1 || v.n1 <= 1 || v.s0 >= v.inner() || w.s0 >= w.inner());
+}
+
+// Do a and b lie in different bytes of each turn of length `turn`?
+bool apart_in_turns(const Vectors& a, __int128 na, const Vectors& b, __int128 nb, __int128 turn)
+{
+    const __int128 d = ((b.at() - a.at()) % turn + turn) % turn;
+    return d >= na && d + nb <= turn;
+}
+
+// a and b share no byte: their spans do not, or they are interleaved with equal outer strides (slices of one
+// projection), or with strides that are multiples of a length in which both have their place (every other head).
+bool apart(const Vectors& a, const Vectors& b)
+{
+    if (a.span() <= 0 || b.span() <= 0 || a.at() >= b.at() + b.span() || b.at() >= a.at() + a.span()) return true;
+    const auto outer = [](const Vectors& x, const Vectors& y) {
+        return x.n0 > 1 && y.n0 > 1 && x.s0 == y.s0 && x.s0 > 0 && x.inner() <= x.s0 && y.inner() <= y.s0 &&
+               apart_in_turns(x, x.inner(), y, y.inner(), x.s0);
+    };
+    if (outer(a, b) || outer(a.swapped(), b.swapped())) return true;
+    int64_t g = 0;
+    for (const Vectors& v : {a, b}) {
+        if (v.n0 > 1) g = std::gcd(g, v.s0);
+        if (v.n1 > 1) g = std::gcd(g, v.s1);
+    }
+    return g > 0 && apart_in_turns(a, a.bytes, b, b.bytes, g);
+}
+
+// The same vectors in the same places.
+bool same(const Vectors& a, const Vectors& b)
+{
+    return a.p == b.p && a.n0 == b.n0 && a.n1 == b.n1 && a.bytes == b.bytes && (a.n0 <= 1 || a.s0 == b.s0) &&
+           (a.n1 <= 1 || a.s1 == b.s1);
+}
+
 // No exception leaves the library: what the host side's containers and locks may throw becomes a status.
 template <typename F>
 st_status guarded(F&& f) noexcept
@@ -104,6 +156,9 @@ st_status cache_sizes(const st_kv_cache* c)
     return ST_OK;
 }
 
+int64_t code_bytes(const st_kv_cache* c) { return int64_t(c->num_blocks) * c->kv_heads * c->block_size * c->head_dim; }
+int64_t scale_bytes(const st_kv_cache* c) { return int64_t(c->num_blocks) * c->kv_heads * 4; }
+
 bool cache_arrays(const st_kv_cache* c, int dev)
 {
     return on_device(c->k, dev, 16) && on_device(c->v, dev, 16) && on_device(c->k_scale, dev, 4) &&
@@ -111,7 +166,11 @@ bool cache_arrays(const st_kv_cache* c, int dev)
 }
 
 // Strides (elements of 16 bits) of an array of 16-byte vectors.
-bool strides_ok(int64_t token, int64_t head) { return token >= 0 && head >= 0 && token % 8 == 0 && head % 8 == 0; }
+bool strides_ok(int64_t token, int64_t head)
+{
+    constexpr int64_t far = int64_t(1) << 56;
+    return token >= 0 && head >= 0 && token % 8 == 0 && head % 8 == 0 && token < far && head < far;
+}
 
 st_status attend_sizes(const st_kv_cache* c, int64_t T, int32_t q_heads, int32_t R, int32_t max_q, int64_t max_len)
 {
@@ -219,13 +278,21 @@ st_status st_kv_attend(const st_kv_cache* cache, const void* q, st_dtype dtype, 
         if (s != ST_OK) return s;
         if (int64_t(R) * max_blocks >= kLimit31) return ST_ERR_UNSUPPORTED;
         if (T == 0) return ST_OK;
+        const int64_t need = st::kv_attend_workspace(*cache, T, q_heads, R, max_q, max_len);
+        if (need > st::kAttendMaxBytes) return ST_ERR_UNSUPPORTED;
+        // out and the workspace are written while the rest is read; out may be q itself
+        const Vectors vq{q, T, q_token_stride * 2, q_heads, q_head_stride * 2, cache->head_dim * 2};
+        const Vectors vo{out, T, out_token_stride * 2, q_heads, out_head_stride * 2, cache->head_dim * 2}, vw = dense(workspace, need);
+        if (!separate(vo) || !(same(vo, vq) || apart(vo, vq)) || !apart(vw, vq) || !apart(vw, vo)) return ST_ERR_INVALID_ARG;
+        for (const Vectors& x : {dense(cache->k, code_bytes(cache)), dense(cache->v, code_bytes(cache)), dense(cache->k_scale, scale_bytes(cache)),
+                                 dense(cache->v_scale, scale_bytes(cache)), dense(table, int64_t(R) * max_blocks * 4),
+                                 dense(row_start, (int64_t(R) + 1) * 4), dense(lens, int64_t(R) * 4)})
+            if (!apart(vo, x) || !apart(vw, x)) return ST_ERR_INVALID_ARG;
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess) return ST_ERR_CUDA;
         if (!cache_arrays(cache, dev) || !on_device(q, dev, 16) || !on_device(out, dev, 16) || !on_device(table, dev, 4) ||
             !on_device(row_start, dev, 4) || !on_device(lens, dev, 4))
             return ST_ERR_INVALID_ARG;
-        const int64_t need = st::kv_attend_workspace(*cache, T, q_heads, R, max_q, max_len);
-        if (need > st::kAttendMaxBytes) return ST_ERR_UNSUPPORTED;
         if (need > 0 && (workspace_bytes < need || !on_device(workspace, dev, 16))) return ST_ERR_INVALID_ARG;
         st::AttendArgs a{*cache, q, dtype, T, q_heads, q_token_stride, q_head_stride, table, max_blocks, row_start, lens,
                          R, max_q, max_len, scale * 1.44269504088896340736f, causal, out, out_token_stride, out_head_stride,

@@ -520,7 +520,9 @@ st_status st_kv_append(const st_kv_cache* cache, const void* k, const void* v, s
  *
  *   q, out     device bf16 or f16 [T][q_heads][head_dim], strides as in st_kv_append;
  *              out rows behind row_start[R] are left as they were; out may be q itself (same
- *              address and strides), else it shares no memory with what the call reads
+ *              address and strides), else it shares no memory with what the call reads. Slices of one
+ *              array may interleave where their token (or head) strides are equal, or where all their strides are
+ *              multiples of a length in which each has its own place; other arrays stay out of what out spans
  *   table      device int32 [R][max_blocks], row_start device int32 [R+1] (nondecreasing,
  *              within [0, T]), lens device int32 [R]
  *   max_q      most query tokens of a row (1 to 2^20); max_len: most cached tokens of a
@@ -536,7 +538,8 @@ st_status st_kv_append(const st_kv_cache* cache, const void* k, const void* v, s
  * outputs are held in fp32 and rounded once.
  *
  * Errors: INVALID_ARG (null or non-device pointer, misaligned arrays or strides,
- * q_heads not a multiple of kv_heads, sizes outside those above, a workspace that is too small),
+ * q_heads not a multiple of kv_heads, sizes outside those above, a workspace that is too small, an out whose
+ * vectors overlap each other or another array, a workspace that overlaps one),
  * UNSUPPORTED (the cache outside its limits, R above ST_KV_MAX_ROWS,
  * R * max_blocks or T at 2^31 or above, more than 65535 query heads, or sizes that
  * take more than 2^31 CTAs or 2^48 bytes of workspace), CUDA. A used table entry outside the cache hides its

@@ -45,3 +45,82 @@ def test_attend_workspace_that_no_memory_holds(lib, T, R, max_q, max_len, heads,
     """Sizes whose workspace would be more than 2^48 bytes (and more than 64 bits count) are refused."""
     assert T * heads * group * -(-max_len // 16384) * 4 * 130 > 2**48
     assert attend_bytes(lib, T, R, max_q, max_len, heads, group) == (st.ST_ERR_UNSUPPORTED, 0)
+
+
+MEG = 1 << 20
+BAD = st.ST_ERR_INVALID_ARG
+
+
+def through(status):
+    """Nothing was refused before the pointers were looked up: there is no GPU here, or the addresses are not its memory."""
+    import torch
+    return status == (BAD if torch.cuda.is_available() else st.ST_ERR_CUDA)
+
+
+def attend_at(lib, T=6, heads=4, R=2, width=4, blocks=8, kv_heads=2, S=16, D=64, max_len=64, strides=(256, 64), out_strides=(256, 64), room=1 << 20, **at):
+    """A call with every array in a megabyte of its own, but for those in `at`."""
+    names = ("k", "v", "k_scale", "v_scale", "q", "out", "table", "start", "lens", "work")
+    p = {n: (i + 16) * 64 * MEG for i, n in enumerate(names)}
+    p.update(at)
+    c = st._KvCache(p["k"], p["v"], p["k_scale"], p["v_scale"], blocks, kv_heads, S, D)
+    return lib.st_kv_attend(ctypes.byref(c), p["q"], 0, T, heads, *strides, p["table"], width, p["start"], p["lens"], R, 3, max_len, 1.0, 1, p["out"], *out_strides, p["work"], room, None)
+
+
+def test_attend_arrays_that_share_memory(lib):
+    base = 16 * 64 * MEG
+    q, out = base + 4 * 64 * MEG, base + 5 * 64 * MEG
+    assert through(attend_at(lib)) and through(attend_at(lib, out=q))
+    assert through(attend_at(lib, out=q + 6 * 512)) and attend_at(lib, out=q + 6 * 512 - 16) == BAD
+    assert attend_at(lib, out=q + 512) == BAD and attend_at(lib, out=q, out_strides=(512, 64)) == BAD
+    sizes = dict(k=8 * 2 * 16 * 64, v=8 * 2 * 16 * 64, k_scale=64, v_scale=64, table=32, start=12, lens=8)
+    for n, size in sizes.items():
+        assert attend_at(lib, **{n: out}) == BAD, n
+        assert attend_at(lib, **{n: out + 6 * 512 - 16}) == BAD, n
+        assert through(attend_at(lib, **{n: out + 6 * 512})) and through(attend_at(lib, **{n: out - size // 16 * 16 - 16})), n
+    # the vectors of out among themselves
+    for bad in ((0, 64), (256, 0), (256, 56), (192, 64), (64, 256)):
+        assert attend_at(lib, out_strides=bad) == BAD, bad
+    assert through(attend_at(lib, out_strides=(64, 6 * 64))) and through(attend_at(lib, T=1, out_strides=(0, 64)))
+    # slices of one array: heads beside heads, every other head, every other token, heads outside
+    assert through(attend_at(lib, strides=(1024, 64), out_strides=(1024, 64), out=q + 512))
+    assert attend_at(lib, strides=(1024, 64), out_strides=(1024, 64), out=q + 496) == BAD
+    assert through(attend_at(lib, strides=(512, 128), out_strides=(512, 128), out=q + 128))
+    assert attend_at(lib, strides=(512, 128), out_strides=(512, 128), out=q + 64) == BAD
+    assert through(attend_at(lib, strides=(512, 64), out_strides=(512, 64), out=q - 512))
+    assert through(attend_at(lib, strides=(64, 1024), out_strides=(64, 1024), out=q + 6 * 128))
+    assert attend_at(lib, strides=(64, 1024), out_strides=(64, 1024), out=q + 5 * 128) == BAD
+
+
+def test_attend_workspace_that_shares_memory(lib):
+    base = 16 * 64 * MEG
+    long = dict(width=400, max_len=6400, room=8 * MEG)
+    status, need = attend_bytes(lib, 6, 2, 3, 6400, 2, 2, 64)
+    assert status == st.ST_OK and need > 0
+    assert through(attend_at(lib, **long))
+    for i, n in enumerate(("k", "v", "k_scale", "v_scale", "q", "out", "table", "start", "lens")):
+        assert attend_at(lib, **long, work=base + i * 64 * MEG) == BAD, n
+        assert attend_at(lib, **long, work=base + i * 64 * MEG - need + 16) == BAD, n
+        assert through(attend_at(lib, **long, work=base + i * 64 * MEG - need)), n
+    assert through(attend_at(lib, work=base))  # none is used
+
+
+def test_attend_outputs_that_pass_share_no_byte(lib):
+    """Random strides and places near the queries: what is let through is the queries' place or disjoint from them."""
+    import random
+    r = random.Random(1)
+    q, passed = (16 + 4) * 64 * MEG, 0
+    if not through(attend_at(lib)) or through(BAD):
+        pytest.skip("refusals by the pointers' memory look like those for overlap")
+    for _ in range(4000):
+        T, heads = r.randint(1, 4), 2 * r.randint(1, 2)
+        pick = lambda: r.choice([(64 * heads, 64), (64, 64 * T), (r.choice([128, 256, 512, 640]), r.choice([0, 64, 72, 128, 256]))])  # noqa: E731
+        a = pick()
+        b = r.choice([a, a, pick()])
+        at = q + 16 * r.randint(-80, 80)
+        places = lambda base, s: [base + 2 * (t * s[0] + h * s[1]) for t in range(T) for h in range(heads)]  # noqa: E731
+        own, other = places(q, a), places(at, b)
+        if through(attend_at(lib, T=T, heads=heads, strides=a, out_strides=b, out=at)):
+            passed += 1
+            assert all(abs(x - y) >= 128 for i, x in enumerate(other) for y in other[:i]), (T, heads, b)
+            assert own == other or all(abs(x - y) >= 128 for x in own for y in other), (T, heads, a, b, at - q)
+    assert passed > 500

@@ -31,3 +31,20 @@ def test_attend_long_stretches_beside_prompts():
     q, codes, scales, table, start, lens = make_attend(51, lens, qs, 8, 4, 128, 16, torch.bfloat16)
     for width in (4096, 8192):  # 65536 tokens: stretches of 2048; 131072: of 4096
         check_attend(q, codes, scales, widen(table, width), start, lens, max_len=16 * width)
+
+
+@pytest.mark.parametrize("qs", [[1], [1, 1], [3, 90, 1]])
+def test_attend_output_beside_the_queries(qs):
+    """Output and queries as slices of one array: heads beside heads, every other head; further over is refused."""
+    q, codes, scales, table, start, lens = make_attend(52, [2000 + m for m in qs], qs, 2, 4, 64, 16, torch.bfloat16)
+    cache = st.KvCache(codes[0].cuda(), codes[1].cuda(), scales[0].cuda(), scales[1].cuda())
+    args = [torch.tensor(x, dtype=torch.int32).cuda() for x in (table, start, lens)] + [max(qs)]
+    want = st.st_kv_attend(cache, q.cuda(), *args)
+    for a, b in ((slice(0, 8), slice(8, 16)), (slice(0, 16, 2), slice(1, 16, 2))):
+        hold = torch.zeros(q.shape[0], 16, 64, dtype=q.dtype, device="cuda")
+        hold[:, a] = q.cuda()
+        got = st.st_kv_attend(cache, hold[:, a], *args, out=hold[:, b])
+        assert torch.equal(got, want) and torch.equal(hold[:, a], q.cuda())
+    with pytest.raises(st.StError) as e:
+        st.st_kv_attend(cache, hold[:, :8], *args, out=hold[:, 4:12])
+    assert e.value.status == st.ST_ERR_INVALID_ARG

@@ -237,6 +237,15 @@ st_status st_kv_append(const st_kv_cache* cache, const void* k, const void* v, s
             return ST_ERR_INVALID_ARG;
         if (cache_sizes(cache) != ST_OK || T >= kLimit31) return ST_ERR_UNSUPPORTED;
         if (T == 0) return ST_OK;
+        // the cache's arrays are written while the others are read
+        const int64_t row = cache->head_dim * 2;
+        const Vectors part[] = {dense(cache->k, code_bytes(cache)), dense(cache->v, code_bytes(cache)), dense(cache->k_scale, scale_bytes(cache)),
+                                dense(cache->v_scale, scale_bytes(cache)), {k, T, k_token_stride * 2, cache->kv_heads, k_head_stride * 2, row},
+                                {v, T, v_token_stride * 2, cache->kv_heads, v_head_stride * 2, row}, dense(slots, T * 8),
+                                dense(sources, sources ? T * 4 : 0)};
+        for (int i = 0; i < 4; ++i)
+            for (int j = i + 1; j < 8; ++j)
+                if (!apart(part[i], part[j])) return ST_ERR_INVALID_ARG;
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess) return ST_ERR_CUDA;
         if (!cache_arrays(cache, dev) || !on_device(k, dev, 16) || !on_device(v, dev, 16) || !on_device(slots, dev, 8) ||

@@ -500,7 +500,8 @@ st_status st_kv_plan(int32_t* table, const int32_t* have, const int32_t* add, in
  * the run are left as they were: they belong to no token.
  *
  * Errors: INVALID_ARG (null or non-device pointer, bad strides or alignment, a type other than
- * those, T < 0), UNSUPPORTED (the cache outside its limits, T at 2^31 or above), CUDA. A slot or
+ * those, T < 0, a cache array that overlaps another array of the call), UNSUPPORTED (the cache outside its
+ * limits, T at 2^31 or above), CUDA. A slot or
  * source outside the cache is skipped and sets the decode error word.
  */
 st_status st_kv_append(const st_kv_cache* cache, const void* k, const void* v, st_dtype dtype, int64_t T,

@@ -124,3 +124,25 @@ def test_attend_outputs_that_pass_share_no_byte(lib):
             assert all(abs(x - y) >= 128 for i, x in enumerate(other) for y in other[:i]), (T, heads, b)
             assert own == other or all(abs(x - y) >= 128 for x in own for y in other), (T, heads, a, b, at - q)
     assert passed > 500
+
+
+def append_at(lib, T=6, blocks=8, heads=2, S=16, D=64, strides=(128, 64), **at):
+    p = {n: (i + 16) * 64 * MEG for i, n in enumerate(("k", "v", "k_scale", "v_scale", "new_k", "new_v", "slots", "sources"))}
+    p.update(at)
+    c = st._KvCache(p["k"], p["v"], p["k_scale"], p["v_scale"], blocks, heads, S, D)
+    return lib.st_kv_append(ctypes.byref(c), p["new_k"], p["new_v"], 0, T, *strides, *strides, p["slots"], p["sources"], None)
+
+
+def test_append_arrays_that_share_memory(lib):
+    assert through(append_at(lib)) and through(append_at(lib, sources=None))
+    codes = 8 * 2 * 16 * 64
+    sizes = dict(k=codes, v=codes, k_scale=64, v_scale=64, new_k=6 * 256, new_v=6 * 256, slots=48, sources=24)
+    base = {n: (i + 16) * 64 * MEG for i, n in enumerate(sizes)}
+    for a in ("k", "v", "k_scale", "v_scale"):
+        for b in sizes:
+            if a != b:
+                assert append_at(lib, **{a: base[b]}) == BAD, (a, b)
+                assert append_at(lib, **{a: base[b] + sizes[b] // 16 * 16 - 8}) == BAD, (a, b)
+                assert through(append_at(lib, **{a: base[b] + sizes[b] + 8})) and through(append_at(lib, **{a: base[b] - sizes[a]})), (a, b)
+    assert through(append_at(lib, new_v=base["new_k"])) and through(append_at(lib, strides=(0, 0)))  # both are only read
+    assert append_at(lib, strides=(2**40, 64), k=base["new_k"] + 2**41) == BAD

@@ -332,11 +332,24 @@ st_status st_beam_select(const void* logits, st_dtype dtype, int64_t logits_stri
         if ((dtype != ST_BF16 && dtype != ST_F16 && dtype != ST_F32) || logits_stride < V) return ST_ERR_INVALID_ARG;
         st::SelectArgs a{logits, dtype, logits_stride, scores, B, K, V, keep, out_scores, out_parents, out_tokens, {}, workspace};
         if (extras) a.ex = *extras;
-        if (a.ex.allow_request_stride < 0 || a.ex.allow_beam_stride < 0 ||
+        constexpr int64_t far = int64_t(1) << 56;
+        if (a.ex.allow_request_stride < 0 || a.ex.allow_beam_stride < 0 || logits_stride >= far || a.ex.allow_request_stride >= far ||
+            a.ex.allow_beam_stride >= far ||
             (a.ex.finished == nullptr) != (a.ex.out_finished == nullptr) ||
             (a.ex.finished && (a.ex.end_token < 0 || a.ex.end_token >= V)))
             return ST_ERR_INVALID_ARG;
         if (s != ST_OK) return s;
+        const int64_t need = st::beam_select_workspace(B, K, V, keep);
+        // the outputs and the workspace are written while the rest is read
+        const int64_t pairs = int64_t(B) * keep, size = dtype == ST_F32 ? 4 : 2;
+        const Vectors part[] = {dense(out_scores, pairs * 4), dense(out_parents, pairs * 4), dense(out_tokens, pairs * 4),
+                                dense(a.ex.out_finished, a.ex.out_finished ? pairs : 0), dense(workspace, need),
+                                {logits, 1, 0, int64_t(B) * K, logits_stride * size, V * size}, dense(scores, int64_t(B) * K * 4),
+                                {a.ex.allow, B, a.ex.allow_request_stride * 4, K, a.ex.allow_beam_stride * 4, a.ex.allow ? (V + 31) / 32 * 4 : 0},
+                                dense(a.ex.finished, a.ex.finished ? int64_t(B) * K : 0)};
+        for (int i = 0; i < 5; ++i)
+            for (int j = i + 1; j < 9; ++j)
+                if (part[i].bytes > 0 && part[j].bytes > 0 && !apart(part[i], part[j])) return ST_ERR_INVALID_ARG;
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess) return ST_ERR_CUDA;
         if (!on_device(logits, dev, dtype == ST_F32 ? 4 : 2) || !on_device(scores, dev, 4) ||
@@ -344,7 +357,6 @@ st_status st_beam_select(const void* logits, st_dtype dtype, int64_t logits_stri
             (a.ex.allow && !on_device(a.ex.allow, dev, 4)) || (a.ex.finished && !on_device(a.ex.finished, dev, 1)) ||
             (a.ex.out_finished && !on_device(a.ex.out_finished, dev, 1)))
             return ST_ERR_INVALID_ARG;
-        const int64_t need = st::beam_select_workspace(B, K, V, keep);
         if (need > 0 && (workspace_bytes < need || !on_device(workspace, dev, 16))) return ST_ERR_INVALID_ARG;
         return to_status(st::launch_beam_select(a, stream));
     });

@@ -585,7 +585,7 @@ typedef struct {
  *
  * Errors: INVALID_ARG (null or non-device pointer, misaligned arrays, sizes below 1, logits_stride
  * below V, one of finished and out_finished alone, end_token outside [0, V), negative allow strides, a workspace too
- * small or not 16-byte aligned), UNSUPPORTED (B above ST_MAX_B, K, keep or V above the limits), CUDA.
+ * small or not 16-byte aligned, an output or workspace that overlaps another array), UNSUPPORTED (B above ST_MAX_B, K, keep or V above the limits), CUDA.
  */
 st_status st_beam_select(const void* logits, st_dtype dtype, int64_t logits_stride, const float* scores,
                          int32_t B, int32_t K, int32_t V, int32_t keep, float* out_scores, int32_t* out_parents,

@@ -146,3 +146,35 @@ def test_append_arrays_that_share_memory(lib):
                 assert through(append_at(lib, **{a: base[b] + sizes[b] + 8})) and through(append_at(lib, **{a: base[b] - sizes[a]})), (a, b)
     assert through(append_at(lib, new_v=base["new_k"])) and through(append_at(lib, strides=(0, 0)))  # both are only read
     assert append_at(lib, strides=(2**40, 64), k=base["new_k"] + 2**41) == BAD
+
+
+def select_at(lib, B=2, K=3, V=100, keep=4, stride=100, allow_strides=(12, 4), extras=True, **at):
+    names = ("logits", "scores", "out_scores", "out_parents", "out_tokens", "work", "allow", "finished", "out_finished")
+    p = {n: (i + 16) * 64 * MEG for i, n in enumerate(names)}
+    p.update(at)
+    ex = st._BeamExtras(p["allow"], *allow_strides, p["finished"], p["out_finished"], 0)
+    return lib.st_beam_select(p["logits"], 2, stride, p["scores"], B, K, V, keep, p["out_scores"], p["out_parents"], p["out_tokens"],
+                              ctypes.byref(ex) if extras else None, p["work"], 1 << 20, None)
+
+
+def test_select_arrays_that_share_memory(lib):
+    need = ctypes.c_int64(0)
+    assert lib.st_beam_select_workspace(2, 3, 100, 4, ctypes.byref(need)) == st.ST_OK
+    sizes = dict(logits=2400, scores=24, out_scores=32, out_parents=32, out_tokens=32, work=need.value, allow=96, finished=6, out_finished=8)
+    base = {n: (i + 16) * 64 * MEG for i, n in enumerate(sizes)}
+    assert need.value > 0 and through(select_at(lib)) and through(select_at(lib, extras=False))
+    for a in ("out_scores", "out_parents", "out_tokens", "work", "out_finished"):
+        for b in sizes:
+            if a != b:
+                assert select_at(lib, **{a: base[b]}) == BAD, (a, b)
+                assert select_at(lib, **{a: base[b] - sizes[a] + 1}) == BAD, (a, b)
+                assert through(select_at(lib, **{a: base[b] + sizes[b]})) and through(select_at(lib, **{a: base[b] - sizes[a]})), (a, b)
+    assert through(select_at(lib, logits=base["allow"], scores=base["finished"])) and through(select_at(lib, allow_strides=(0, 0)))  # only read
+    assert through(select_at(lib, extras=False, out_scores=base["allow"], out_tokens=base["finished"]))
+    assert select_at(lib, stride=2**57) == BAD and select_at(lib, allow_strides=(2**57, 4)) == BAD
+
+
+def test_select_scores_may_stand_behind_the_logits(lib):
+    """Outputs in the room between the beams' logits."""
+    base = 16 * 64 * MEG
+    assert through(select_at(lib, stride=300, out_scores=base + 400, K=1, B=1)) and select_at(lib, stride=300, out_scores=base + 396, K=1, B=1) == BAD

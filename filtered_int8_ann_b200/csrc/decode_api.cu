@@ -376,9 +376,6 @@ st_status st_beam_reorder(const st_beam_state* states, int32_t n_states, const i
                 return ST_ERR_INVALID_ARG;
         }
         if (n_states > ST_BEAM_MAX_STATES || n_src >= kLimit31 || n_dst >= kLimit31) return ST_ERR_UNSUPPORTED;
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess) return ST_ERR_CUDA;
-        if (!on_device(parents, dev, 4)) return ST_ERR_INVALID_ARG;
         // the bytes that each array's rows span, for the overlap checks
         struct Span {
             __int128 lo, hi;
@@ -387,7 +384,6 @@ st_status st_beam_reorder(const st_beam_state* states, int32_t n_states, const i
             const st_beam_state& x = states[i];
             src[i] = dst[i] = Span{0, 0};
             if (x.row_bytes == 0 || x.outer == 0) continue;
-            if (!on_device(x.src, dev, 1) || !on_device(x.dst, dev, 1)) return ST_ERR_INVALID_ARG;
             const __int128 ls = __int128(x.outer - 1) * x.src_outer_stride + __int128(n_src - 1) * x.src_row_stride + x.row_bytes;
             const __int128 ld = __int128(x.outer - 1) * x.dst_outer_stride + __int128(n_dst - 1) * x.dst_row_stride + x.row_bytes;
             if (ls > far || ld > far) return ST_ERR_INVALID_ARG;
@@ -402,11 +398,20 @@ st_status st_beam_reorder(const st_beam_state* states, int32_t n_states, const i
             dst[i].lo = reinterpret_cast<uintptr_t>(x.dst);
             dst[i].hi = dst[i].lo + ld;
         }
+        const Span by{__int128(reinterpret_cast<uintptr_t>(parents)), __int128(reinterpret_cast<uintptr_t>(parents)) + n_dst * 4};
+        for (int i = 0; i < n_states; ++i)
+            if (dst[i].lo < by.hi && by.lo < dst[i].hi) return ST_ERR_INVALID_ARG;
         for (int i = 0; i < n_states; ++i)
             for (int j = 0; j < n_states; ++j) {
                 if (dst[i].lo < src[j].hi && src[j].lo < dst[i].hi) return ST_ERR_INVALID_ARG;
                 if (i < j && dst[i].lo < dst[j].hi && dst[j].lo < dst[i].hi) return ST_ERR_INVALID_ARG;
             }
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return ST_ERR_CUDA;
+        if (!on_device(parents, dev, 4)) return ST_ERR_INVALID_ARG;
+        for (int i = 0; i < n_states; ++i)
+            if (states[i].row_bytes > 0 && states[i].outer > 0 && (!on_device(states[i].src, dev, 1) || !on_device(states[i].dst, dev, 1)))
+                return ST_ERR_INVALID_ARG;
         uint32_t* err = nullptr;
         cudaError_t e = st::decode_error_address(&err);
         if (e == cudaSuccess) e = st::launch_beam_reorder(states, n_states, parents, B, K, keep, err, stream);

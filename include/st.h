@@ -405,7 +405,7 @@ st_status st_index_insert(st_index* idx, const int32_t* lists, const int8_t* ite
  *
  * A kernel that meets an index outside its arrays skips what it names and
  * sets the device's decode error word (st_decode_check). Arrays that a call
- * writes must not overlap any other array of the call. The first call of each
+ * writes must not overlap any other array of the call (INVALID_ARG). The first call of each
  * function on a device raises kernel limits and looks up the error word: make it before a
  * stream capture begins.
  */
@@ -608,8 +608,8 @@ typedef struct {
  *   states   HOST array of n_states (1 to ST_BEAM_MAX_STATES)
  *   parents  device int32 [B][keep]
  * A parent outside [-1, K) gives zeros and sets the decode error word. src and dst must not
- * overlap: a beam may be the parent of several (INVALID_ARG where their ranges do, or where dst
- * rows would overlap). An array with row_bytes = 0 or outer = 0 is skipped.
+ * overlap: a beam may be the parent of several (INVALID_ARG where their ranges do, where dst
+ * rows would overlap, or where a dst range overlaps parents). An array with row_bytes = 0 or outer = 0 is skipped.
  * Errors: INVALID_ARG (null or non-device pointers, negative sizes, overlap), UNSUPPORTED
  * (more than ST_BEAM_MAX_STATES arrays, B * K or B * keep at 2^31 or above), CUDA.
  */

@@ -178,3 +178,20 @@ def test_select_scores_may_stand_behind_the_logits(lib):
     """Outputs in the room between the beams' logits."""
     base = 16 * 64 * MEG
     assert through(select_at(lib, stride=300, out_scores=base + 400, K=1, B=1)) and select_at(lib, stride=300, out_scores=base + 396, K=1, B=1) == BAD
+
+
+def test_reorder_arrays_that_share_memory(lib):
+    base = 16 * MEG
+
+    def call(parents=base, src=2 * base, dst=3 * base, src2=4 * base, dst2=5 * base, bytes2=40):
+        s = (st._BeamState * 2)(st._BeamState(src, dst, 16, 16, 20, 2, 200, 300), st._BeamState(src2, dst2, bytes2, 40, 40, 1, 0, 0))
+        return lib.st_beam_reorder(s, 2, parents, 2, 3, 4, None)
+
+    assert through(call()) and through(call(src2=2 * base)) and through(call(src=base))  # only read
+    span, parents = 300 + 7 * 20 + 16, 2 * 4 * 4
+    for a in ("dst", "dst2"):
+        size = span if a == "dst" else 8 * 40
+        assert call(**{a: base}) == BAD and call(**{a: base + parents - 1}) == BAD and call(**{a: base - size + 1}) == BAD
+        assert through(call(**{a: base + parents})) and through(call(**{a: base - size}))
+    assert through(call(dst2=base, bytes2=0))  # skipped
+    assert call(dst=2 * base) == BAD and call(dst=4 * base) == BAD and call(dst2=3 * base) == BAD

@@ -48,3 +48,13 @@ def test_attend_output_beside_the_queries(qs):
     with pytest.raises(st.StError) as e:
         st.st_kv_attend(cache, hold[:, :8], *args, out=hold[:, 4:12])
     assert e.value.status == st.ST_ERR_INVALID_ARG
+
+
+def test_reorder_outputs_beside_the_parents():
+    x = torch.arange(24, dtype=torch.int32, device="cuda").view(2, 3, 4)
+    beside = torch.zeros(30, dtype=torch.int32, device="cuda")
+    got = st.st_beam_reorder([x], beside[24:].view(2, 3), out=[beside[:24].view(2, 3, 4)])
+    assert torch.equal(got[0], x[:, :1].expand(2, 3, 4))
+    with pytest.raises(st.StError) as e:
+        st.st_beam_reorder([x], beside[:6].view(2, 3), out=[beside[:24].view(2, 3, 4)])
+    assert e.value.status == st.ST_ERR_INVALID_ARG

@@ -5,10 +5,11 @@ package; every step runs in the library's CUDA kernels.
 A step, for R rows (beams) with `have` tokens each:
 
     slots, sources, start, lens, report = st_kv_plan(table, have, add, num_blocks, block_size, T)
+    assert report[2:].tolist() == [0, 0]                           # else some rows got no slots: see st_kv_plan
     st_kv_append(cache, k, v, slots, sources)                      # per layer
     out = st_kv_attend(cache, q, table, start, lens, max_q)        # per layer
     scores, parents, tokens, finished = st_beam_select(logits, scores, keep)
-    table, lens = (x.flatten(0, 1) for x in st_beam_reorder([table.view(B, K, -1), lens.view(B, K)], parents))
+    table, have = (x.flatten(0, 1) for x in st_beam_reorder([table.view(B, K, -1), lens.view(B, K)], parents))
 
 Tensors are on the current CUDA device; work goes to the current stream, or to
 `stream`. Nothing waits. Call each function once before capturing it in a graph.
@@ -155,7 +156,10 @@ def st_kv_plan(table: torch.Tensor, have: torch.Tensor, add: torch.Tensor, num_b
     """Blocks for the rows' next tokens: table int32 [R, max_blocks] (written in
     place), have and add int32 [R], room for T new tokens. Returns (slots int64
     [T], sources int32 [T], row_start int32 [R + 1], lens int32 [R], report
-    int32 [4]); see st_kv_plan in include/st.h for what they hold."""
+    int32 [4]); see st_kv_plan in include/st.h for what they hold. Rows that
+    could not be served (report[2] of them) have lens -1 and no slots: append
+    the others' tokens, free blocks, and plan again with have = torch.where(lens
+    < 0, have, lens) and no tokens for the rows served."""
     if table.dim() != 2 or T < 0:
         raise ValueError("table must be [R, max_blocks], and T not negative")
     R, width = table.shape

@@ -469,7 +469,10 @@ typedef struct {
  * block_size, or when its tokens end behind T; its table row is left as it was.
  * A row is refused, and served like those, when have or add is negative, have exceeds
  * max_blocks * block_size, or a used entry is outside [0, num_blocks) (this sets the
- * decode error word too).
+ * decode error word too). A row whose have is negative holds no block: those that no other row uses are free.
+ * So the lens of a row that was not served is no have for another plan: it keeps the have that it had, and gets its
+ * slots by another plan, with add = 0 for the rows that were served (their have is lens now), once there are blocks. A plan's tokens are
+ * appended before the next plan: blocks named by its sources alone are free then.
  *
  * Errors: INVALID_ARG (null or non-device pointer, misaligned or overlapping
  * arrays, R < 1, max_blocks < 1, T < 0, num_blocks < 1, a block size other than those above),

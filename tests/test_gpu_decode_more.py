@@ -58,3 +58,40 @@ def test_reorder_outputs_beside_the_parents():
     with pytest.raises(st.StError) as e:
         st.st_beam_reorder([x], beside[:6].view(2, 3), out=[beside[:24].view(2, 3, 4)])
     assert e.value.status == st.ST_ERR_INVALID_ARG
+
+
+def test_rows_not_served_are_planned_again():
+    """The pool runs out in a step, a row ends, and the others are planned again: what the cache then holds is what a
+    larger pool has (the prompt of each pair of rows is shared, so that blocks are replaced too)."""
+    S, H, D, R, width = 16, 2, 64, 6, 4
+    g = torch.Generator().manual_seed(60)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    prompt = torch.randn(3 * 20, 2, H, D, generator=g).half().cuda()
+    step = torch.randn(R, 2, H, D, generator=g).half().cuda()
+    outs = []
+    for blocks in (40, 8):  # 6 blocks hold the prompts; a step needs one block for each row
+        cache = st.KvCache.empty(blocks, H, S, D)
+        table, have = torch.full((R, width), -1, **i32), torch.zeros(R, **i32)
+        slots, sources, start, lens, report = st.st_kv_plan(table, have, torch.tensor([20, 0] * 3, **i32), blocks, S, 60)
+        assert report[2:].tolist() == [0, 0]
+        st.st_kv_append(cache, prompt[:, 0], prompt[:, 1], slots, sources)
+        table, have = table[::2].repeat_interleave(2, 0).contiguous(), lens[::2].repeat_interleave(2).contiguous()
+        add, left, plans = torch.ones(R, **i32), torch.arange(R, device="cuda"), 0
+        while True:
+            slots, sources, start, lens, report = st.st_kv_plan(table, have, add, blocks, S, len(left))
+            st.st_kv_append(cache, step[left, 0], step[left, 1], slots, sources)
+            plans += 1
+            unserved = lens < 0
+            have, add = torch.where(unserved, have, lens), torch.where(unserved, add, 0)
+            left = unserved.nonzero()[:, 0]
+            if not len(left):
+                break
+            assert plans < 4 and int(report[2]) == len(left)
+            if plans == 1:
+                have[4:], add[4:] = 0, 0  # the last pair ends
+                left = left[left < 4]
+        assert plans == (1 if blocks == 40 else 2)
+        assert have[:4].tolist() == [21] * 4 and len({int(table[r, 1]) for r in range(4)}) == 4
+        q = torch.randn(4, 2 * H, D, generator=torch.Generator().manual_seed(61)).half().cuda()
+        outs.append(st.st_kv_attend(cache, q, table[:4].contiguous(), torch.arange(5, **i32), have[:4].contiguous(), 1))
+    assert torch.equal(*outs) and st.st_decode_check() == st.ST_OK

@@ -12,7 +12,9 @@ A step, for R rows (beams) with `have` tokens each:
     table, have = (x.flatten(0, 1) for x in st_beam_reorder([table.view(B, K, -1), lens.view(B, K)], parents))
 
 Tensors are on the current CUDA device; work goes to the current stream, or to
-`stream`. Nothing waits. Call each function once before capturing it in a graph.
+`stream`. Nothing waits. There are no backward passes: tensors that require a
+gradient are refused outside torch.no_grad(). Call each function once before
+capturing it in a graph.
 """
 from __future__ import annotations
 
@@ -68,6 +70,12 @@ def _empty(shape, dtype, stream):
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
     with torch.cuda.stream(s):
         return _empty_strided_cuda(shape, strides, dtype)
+
+
+def _no_gradient(x: torch.Tensor, name: str):
+    """What the calls write is not recorded: a gradient through it would be lost."""
+    if x.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient and the decode calls have none: make them under torch.no_grad()")
 
 
 def _on_gpu(x: torch.Tensor, name: str):
@@ -142,6 +150,7 @@ def _vectors(x: torch.Tensor, heads: Optional[int], dim: int, name: str):
     shape = x.shape
     if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
         raise ValueError(f"{name} must be [T, {'heads' if heads is None else heads}, {dim}], not {tuple(shape)}")
+    _no_gradient(x, name)
     token, head, one = x.stride()
     if one != 1:
         raise ValueError(f"{name} must have dense vectors")
@@ -255,6 +264,7 @@ def st_beam_select(logits: torch.Tensor, scores: torch.Tensor, keep: int, allow:
     kind = _DTYPES.get(logits.dtype)
     if kind is None or logits.dim() != 3:
         raise ValueError("logits must be [B, K, V] bfloat16, float16 or float32")
+    _no_gradient(logits, "logits")
     B, K, V = logits.shape
     request, beam, one = logits.stride()
     if V > 1 and one != 1:
@@ -263,6 +273,7 @@ def st_beam_select(logits: torch.Tensor, scores: torch.Tensor, keep: int, allow:
     if B > 1 and K > 1 and request != K * stride:
         raise ValueError("logits' beams must be evenly spaced")
     pscores = _array(scores, _F32, (B, K), "scores")
+    _no_gradient(scores, "scores")
     ex = out_finished = None
     if allow is not None or finished is not None:
         ex = _BeamExtras()
@@ -326,6 +337,7 @@ def st_beam_reorder(states: Sequence[torch.Tensor], parents: torch.Tensor, out: 
         shape = x.shape
         if len(shape) <= beam_dim or shape[beam_dim - 1] != B or shape[beam_dim] != K:
             raise ValueError(f"state {i} must have {B} requests of {K} beams at dimension {beam_dim}")
+        _no_gradient(x, f"state {i}")
         size = x.element_size()
         if out is None and beam_dim == 1 and stream is None and rows and x.is_contiguous():  # the usual case
             _on_gpu(x, f"state {i}")
@@ -344,6 +356,7 @@ def st_beam_reorder(states: Sequence[torch.Tensor], parents: torch.Tensor, out: 
             y = out[i]
             if y.shape != new or y.dtype != x.dtype:
                 raise ValueError(f"out {i} must be {tuple(new)} {x.dtype}")
+            _no_gradient(y, f"out {i}")
         layers = (shape[0], size * x.stride(0), size * y.stride(0)) if beam_dim == 2 else (1, 0, 0)
         words += (x.data_ptr(), y.data_ptr(), size * math.prod(shape[beam_dim + 1:]), size * step,
                   size * _rows(y, beam_dim, f"out {i}"), *layers)

@@ -140,10 +140,14 @@ def _ptr(t) -> Optional[int]:
     return int(t)
 
 
+# the current stream's handle alone: torch.cuda.current_stream() builds an object around it (private names: they may be missing)
+_raw_stream, _device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        if torch.cuda.is_initialized():  # the handle alone: torch.cuda.current_stream() builds an object around it
-            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        if _raw_stream and _device and torch.cuda.is_initialized():
+            return _raw_stream(_device())
         return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream

@@ -56,8 +56,12 @@ __device__ __forceinline__ float pow2_up(float big)
     return __uint_as_float(uint32_t(127 + e) << 23);
 }
 
-// A little above x, so that no product rounded to x exceeds it (and -inf for -inf).
-__device__ __forceinline__ float just_above(float x) { return fmaxf(x, fmaf(fabsf(x), 0x1p-22f, x)); }
+// Scores from here on are rounded before the maximum is taken off: the product that fma(s, factor, -max) holds exactly
+// may differ from its rounded value, and so from the maximum, by more than a weight may be off.
+constexpr float kScoreFar = 0x1p20f;
+__device__ __forceinline__ bool is_far(float m) { return fabsf(m) >= kScoreFar && m > -INFINITY; }
+// A little above x, so that no product rounded to x exceeds it (x itself for -inf and where scores are rounded).
+__device__ __forceinline__ float just_above(float x) { return fabsf(x) < kScoreFar ? fmaxf(x, fmaf(fabsf(x), 0x1p-22f, x)) : x; }
 
 // Bytes 128 + code (a code with its sign bit flipped) to fp16 codes, two per
 // register: 0x64 above a byte b is 1024 + b.

@@ -308,7 +308,7 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
                 sc[h][nt][1] = ks * mult[nt][1];
             }
         }
-        if (!whole) {  // scores now, those that the column does not see masked
+        if (!whole) {  // scores now (rounded), those that the column does not see masked
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int jj = jj0 + 16 * h;
@@ -317,7 +317,7 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
                 for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        s[h][nt][i] = !none && jj + g + 8 * (i >> 1) < seen[nt][i & 1] ? s[h][nt][i] * sc[h][nt][i & 1] : -INFINITY;
+                        s[h][nt][i] = !none && jj + g + 8 * (i >> 1) < seen[nt][i & 1] ? __fmul_rn(s[h][nt][i], sc[h][nt][i & 1]) : -INFINITY;
                     sc[h][nt][0] = sc[h][nt][1] = 1.f;
                 }
             }
@@ -339,6 +339,7 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
                 grew = grew || mx[nt][i] > m[nt][i];
             }
         if (__any_sync(0xffffffffu, grew)) {
+            bool some = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float shrink[2];
@@ -348,6 +349,7 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
                     shrink[i] = up > m[nt][i] ? ex2(m[nt][i] - up) : 1.f;
                     m[nt][i] = up;
                     l[nt][i] *= shrink[i];
+                    some = some || is_far(up);
                 }
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
@@ -356,6 +358,17 @@ kv_decode_kernel(AttendArgs a, int splits, int stretch, int col_blocks)
                     o[nt][i][2] *= shrink[0];
                     o[nt][i][3] *= shrink[1];
                 }
+            }
+            if (__any_sync(0xffffffffu, some)) {  // this step's scores are rounded now, later ones as those of a masked step
+                least_seen = 0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) s[h][nt][i] = __fmul_rn(s[h][nt][i], sc[h][nt][i & 1]);
+                        sc[h][nt][0] = sc[h][nt][1] = 1.f;
+                    }
             }
         }
         // weights, transposed to the B fragments of 16 tokens x 8 columns

@@ -236,7 +236,8 @@ __device__ __forceinline__ float step_weights(uint32_t ts, const float (&sc)[8],
     return total[0].x + total[0].y;
 }
 
-// Both for a step of which the column sees `see` tokens, without the hidden blocks' (negative factors).
+// Both for a step of which the column sees `see` tokens, without the hidden blocks' (negative factors), and for scores
+// that are rounded first.
 __device__ __noinline__ float step_max_masked(uint32_t ts, const float* ks, float mult, int see)
 {
     float top = -INFINITY;
@@ -255,8 +256,10 @@ __device__ __noinline__ float step_max_masked(uint32_t ts, const float* ks, floa
     }
     return top;
 }
-__device__ __noinline__ float step_weights_masked(uint32_t ts, const float* ks, const float* vs, float mult, float base, int see)
+__device__ __noinline__ float step_weights_masked(uint32_t ts, const float* ks, const float* vs, float mult, float base, int see, bool far)
 {
+    // (far: some column's maximum is)
+    const auto weight = [&](float s, float sc) { return ex2(far ? __fsub_rn(__fmul_rn(s, sc), base) : fmaf(s, sc, -base)); };
     float sum = 0.f;
 #pragma unroll 1
     for (int c = 0; c < 8; ++c) {
@@ -268,8 +271,8 @@ __device__ __noinline__ float step_weights_masked(uint32_t ts, const float* ks, 
         uint32_t w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float x = 2 * i < here ? ex2(fmaf(s[i].x, sc, -base)) : 0.f;
-            const float y = 2 * i + 1 < here ? ex2(fmaf(s[i].y, sc, -base)) : 0.f;
+            const float x = 2 * i < here ? weight(s[i].x, sc) : 0.f;
+            const float y = 2 * i + 1 < here ? weight(s[i].y, sc) : 0.f;
             sum += x + y;
             w[i] = pack_half2(x * vf, y * vf);
         }
@@ -278,12 +281,12 @@ __device__ __noinline__ float step_weights_masked(uint32_t ts, const float* ks, 
     return sum;
 }
 
-// Raise the column's reference m by `up` (>= 0): what has been summed with it, l and O, shrinks.
+// Raise the column's reference m to `top` (at least m): what has been summed with it, l and O, shrinks.
 template <int D>
-__device__ __noinline__ void raise(uint32_t to, float up, bool has_o, float& m, float& l)
+__device__ __noinline__ void raise(uint32_t to, float top, bool has_o, float& m, float& l)
 {
-    const float z = ex2(-up);
-    m += up;
+    const float z = top > m ? ex2(m - top) : 1.f;
+    m = top;
     l *= z;
     if (has_o) {
 #pragma unroll 1
@@ -675,7 +678,7 @@ kv_prefill_kernel(AttendArgs a, int splits, int stretch)
         int see = tokens;  // tokens of the stretch that this column sees
         if (mine && a.causal) see = int(max(int64_t(0), min(int64_t(tokens), len - n + col / G + 1 - j0)));
         const int least = __reduce_min_sync(0xffffffffu, see);
-        bool ok = true;
+        bool ok = true, far = false;  // far: some column's maximum is
         int i = 0;  // steps of this tile
         for (int j = turns ? tile : 0; j < steps && ok; j += turns ? 2 : 1, ++i) {
             const int left = see - j * kPreTile;
@@ -699,9 +702,10 @@ kv_prefill_kernel(AttendArgs a, int splits, int stretch)
             tc_fence_after();  // the products of the tile's step before are done too
             const float top = just_above(whole ? step_max(ts, sc) : step_max_masked(ts, ks, mult, left));
             if (m == -INFINITY) m = top;  // nothing seen before: l and O are 0
-            if (__any_sync(0xffffffffu, top > m + kPreRaise)) raise<D>(to, top > m + kPreRaise ? top - m : 0.f, i > 0, m, l);
+            if (__any_sync(0xffffffffu, top > m + kPreRaise)) raise<D>(to, top > m + kPreRaise ? top : m, i > 0, m, l);
+            far = __any_sync(0xffffffffu, is_far(m));
             const float base = m > -INFINITY ? m : 0.f;
-            l += whole ? step_weights(ts, sc, vf, base) : step_weights_masked(ts, ks, vs, mult, base, left);
+            l += whole && !far ? step_weights(ts, sc, vf, base) : step_weights_masked(ts, ks, vs, mult, base, left, far);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();

@@ -539,7 +539,8 @@ st_status st_kv_append(const st_kv_cache* cache, const void* k, const void* v, s
  * Products are taken in fp16 with fp32 sums: codes are exact there, a query is
  * scaled by a power of two to its largest element first, and a softmax weight times its
  * block's V scale carries 11 bits, or is off by 2^-32 of the largest; maxima, sums and
- * outputs are held in fp32 and rounded once.
+ * outputs are held in fp32 and rounded once. Scores, and scale times a query's largest element, are fp32 numbers (times log2 e): a score
+ * above their range makes its output NaN, one below it counts as not seen.
  *
  * Errors: INVALID_ARG (null or non-device pointer, misaligned arrays or strides,
  * q_heads not a multiple of kv_heads, sizes outside those above, a workspace that is too small, an out whose

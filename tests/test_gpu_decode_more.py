@@ -95,3 +95,59 @@ def test_rows_not_served_are_planned_again():
         q = torch.randn(4, 2 * H, D, generator=torch.Generator().manual_seed(61)).half().cuda()
         outs.append(st.st_kv_attend(cache, q, table[:4].contiguous(), torch.arange(5, **i32), have[:4].contiguous(), 1))
     assert torch.equal(*outs) and st.st_decode_check() == st.ST_OK
+
+
+@pytest.mark.parametrize("queries", [1, 3, 40, 300])
+@pytest.mark.parametrize("kind,power", [(kind, power) for kind in ("few", "most", "late", "near") for power in (10, 17, 24, 26, 40, 90)
+                                        if kind != "near" or power <= 26])
+def test_attend_scores_of_any_size(kind, power, queries):
+    """Every score is a multiple of 2^power, so that the softmax is the mean over the tokens of the largest: `few` (three
+    of 100 among 50s), `most` (the other way around, scores below zero), `late` (0 behind a long first part of large
+    negative scores), `near` (as late, but 32 instead of 0, by a part of the query that fp16 holds up to 2^26).
+    Tolerance: the output's half step, 2^-11 for the weights, 2^-20 for sums."""
+    S, H, D, n = 16, 1, 64, 1600
+    g = torch.Generator().manual_seed(power)
+    blocks = n // S
+    codes = [torch.zeros(blocks, H, S, D, dtype=torch.int8), torch.randint(-127, 128, (blocks, H, S, D), generator=g, dtype=torch.int8)]
+    level = torch.full((n,), 0 if kind in ("late", "near") else 50)
+    if kind in ("late", "near"):
+        level[:700] = -100
+    else:
+        level[[7, 800, 1290]] = 100
+    codes[0][..., 3] = level.view(blocks, H, S).to(torch.int8)
+    scales = [torch.full((blocks, H), 0.5), torch.full((blocks, H), 2.0 ** -6)]
+    q = torch.zeros(queries, 2, D)
+    q[..., 3] = 2.0 ** power * (-1 if kind == "most" else 1)
+    if kind == "near":
+        codes[0].view(n, D)[700:, 5] = 8
+        q[..., 5] = 8.0
+    best = level == {"few": 100, "most": 50}.get(kind, 0)
+    v = codes[1].view(n, D).double() * 2.0 ** -6
+    got = st.st_kv_attend(st.KvCache(*(x.cuda() for x in codes), *(x.cuda() for x in scales)), q.bfloat16().cuda(),
+                          torch.arange(blocks, dtype=torch.int32).view(1, -1).cuda(), torch.tensor([0, queries], dtype=torch.int32).cuda(),
+                          torch.tensor([n], dtype=torch.int32).cuda(), queries, scale=1.0).cpu().double()
+    for i in range(queries):
+        seen = best & (torch.arange(n) <= n - queries + i)
+        want, mass = v[seen].mean(0), v[seen].abs().mean(0)
+        assert bool(((got[i] - want).abs() <= want.abs() * 2.0 ** -8 + mass * (2.0 ** -11 + 2.0 ** -20) * (1 + 2.0 ** -8)).all())
+
+
+@pytest.mark.parametrize("queries", [1, 3, 40, 300])
+def test_attend_scores_beyond_fp32(queries):
+    """Above its range they give NaN, below it they count as not seen."""
+    S, D, n = 16, 64, 1600
+    codes = [torch.zeros(n // S, 1, S, D, dtype=torch.int8) for _ in range(2)]
+    codes[0].view(n, D)[700:900, 3] = 100
+    codes[1][:] = 64
+    codes[1].view(n, D)[700:900] = -64
+    scales = [torch.ones(n // S, 1), torch.full((n // S, 1), 2.0 ** -6)]
+    cache = st.KvCache(*(x.cuda() for x in codes), *(x.cuda() for x in scales))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    for sign in (1, -1):
+        q = torch.zeros(queries, 2, D, dtype=torch.bfloat16, device="cuda")
+        q[..., 3] = sign * 2.0 ** 125
+        got = st.st_kv_attend(cache, q, torch.arange(n // S, **i32).view(1, -1), torch.tensor([0, queries], **i32), torch.tensor([n], **i32), queries, scale=1.0)
+        assert bool(got.isnan().all() if sign > 0 else (got == 1).all())
+        alone = st.st_kv_attend(cache, q, torch.arange(44, 55, **i32).view(1, -1), torch.tensor([0, queries], **i32), torch.tensor([170], **i32), queries, scale=1.0)
+        seen = slice(max(0, queries - 170), queries)  # (queries before see nothing)
+        assert bool(alone[seen].isnan().all() if sign > 0 else (alone == 0).all())

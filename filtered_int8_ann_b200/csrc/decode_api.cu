@@ -47,6 +47,7 @@ cudaError_t decode_error_word(uint32_t* value)
 
 namespace {
 
+constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int64_t kLimit31 = int64_t(1) << 31;
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -280,7 +281,7 @@ st_status st_kv_attend(const st_kv_cache* cache, const void* q, st_dtype dtype, 
     return guarded([&]() -> st_status {
         const st_status s = attend_sizes(cache, T, q_heads, R, max_q, max_len);
         if (s == ST_ERR_INVALID_ARG) return s;
-        if ((dtype != ST_BF16 && dtype != ST_F16) || max_blocks < 1 || !std::isfinite(scale) ||
+        if ((dtype != ST_BF16 && dtype != ST_F16) || max_blocks < 1 || !std::isfinite(scale * kLog2e) ||
             !strides_ok(q_token_stride, q_head_stride) || !strides_ok(out_token_stride, out_head_stride) ||
             max_len > int64_t(max_blocks) * cache->block_size)
             return ST_ERR_INVALID_ARG;
@@ -304,7 +305,7 @@ st_status st_kv_attend(const st_kv_cache* cache, const void* q, st_dtype dtype, 
             return ST_ERR_INVALID_ARG;
         if (need > 0 && (workspace_bytes < need || !on_device(workspace, dev, 16))) return ST_ERR_INVALID_ARG;
         st::AttendArgs a{*cache, q, dtype, T, q_heads, q_token_stride, q_head_stride, table, max_blocks, row_start, lens,
-                         R, max_q, max_len, scale * 1.44269504088896340736f, causal, out, out_token_stride, out_head_stride,
+                         R, max_q, max_len, scale * kLog2e, causal, out, out_token_stride, out_head_stride,
                          workspace, nullptr};
         cudaError_t e = st::decode_error_address(&a.err);
         if (e == cudaSuccess) e = st::launch_kv_attend(a, stream);

@@ -532,7 +532,7 @@ st_status st_kv_append(const st_kv_cache* cache, const void* k, const void* v, s
  *   max_q      most query tokens of a row (1 to 2^20); max_len: most cached tokens of a
  *              row (1 to max_blocks * block_size). They size the launch: a row
  *              with more of either sets the decode error word, and its tokens get zeros.
- *   scale      finite
+ *   scale      finite, times log2 e too
  *   workspace  device, 16-byte aligned, of at least the bytes that
  *              st_kv_attend_workspace gives (NULL when that is 0)
  *

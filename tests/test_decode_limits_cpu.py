@@ -195,3 +195,12 @@ def test_reorder_arrays_that_share_memory(lib):
         assert through(call(**{a: base + parents})) and through(call(**{a: base - size}))
     assert through(call(dst2=base, bytes2=0))  # skipped
     assert call(dst=2 * base) == BAD and call(dst=4 * base) == BAD and call(dst2=3 * base) == BAD
+
+
+@pytest.mark.parametrize("scale,fine", [(2.35e38, True), (-2.35e38, True), (2.37e38, False), (-3.4e38, False), (float("inf"), False), (float("nan"), False)])
+def test_attend_scale_in_powers_of_two(lib, scale, fine):
+    """The scale times log2 e has to be an fp32 number too."""
+    base = 16 * 64 * MEG
+    c = st._KvCache(base, 2 * base, 3 * base, 4 * base, 8, 2, 16, 64)
+    status = lib.st_kv_attend(ctypes.byref(c), 5 * base, 0, 1, 2, 0, 64, 6 * base, 4, 7 * base, 8 * base, 1, 1, 64, scale, 1, 9 * base, 0, 64, None, 0, None)
+    assert through(status) if fine else status == BAD

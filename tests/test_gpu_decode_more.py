@@ -151,3 +151,41 @@ def test_attend_scores_beyond_fp32(queries):
         alone = st.st_kv_attend(cache, q, torch.arange(44, 55, **i32).view(1, -1), torch.tensor([0, queries], **i32), torch.tensor([170], **i32), queries, scale=1.0)
         seen = slice(max(0, queries - 170), queries)  # (queries before see nothing)
         assert bool(alone[seen].isnan().all() if sign > 0 else (alone == 0).all())
+
+
+@pytest.mark.parametrize("queries", [1, 2, 40, 300])
+@pytest.mark.parametrize("D,S,lens,extra", [
+    (64, 16, [9001], 0), (128, 128, [16391], 0), (64, 64, [40013], 0), (64, 32, [1023, 4097, 2560, 300], 0), (128, 16, [1025, 513, 7000], 0),
+    (128, 64, [5000, 1024, 3073], 60000)])
+@pytest.mark.parametrize("by", ["turns", "parts"])
+def test_attend_counts_every_token_once(by, D, S, lens, extra, queries):
+    """Equal scores: each dim holds the share of the tokens that are its own, by turns or one part of the row after the
+    other. A token that is left out or taken twice moves its dim by 1 / tokens of the dim, which is above the
+    tolerance: half a step of fp16 and of the weights (2^-11 each), 2^-20 for sums."""
+    H, R = 2, len(lens)
+    width = (max(lens) + extra) // S + 2
+    pages = [-(-n // S) for n in lens]
+    order = torch.randperm(sum(pages), generator=torch.Generator().manual_seed(D + S)).int()
+    table, codes, at = torch.full((R, width), -1, dtype=torch.int32), torch.zeros(sum(pages), H, S, D, dtype=torch.int8), 0
+    owners = []
+    for r, (n, p) in enumerate(zip(lens, pages)):
+        j = torch.arange(n)
+        own = j % D if by == "turns" else torch.clamp(j // -(-n // D), max=D - 1)
+        row = torch.zeros(p * S, D, dtype=torch.int8)
+        row[j, own] = 100
+        table[r, :p] = order[at:at + p]
+        codes[order[at:at + p].long()] = row.view(p, 1, S, D).expand(p, H, S, D)
+        at += p
+        owners.append(own)
+    ones = torch.full((sum(pages), H), 2.0 ** -5, device="cuda")
+    cache = st.KvCache(torch.randint(-127, 128, codes.shape, dtype=torch.int8, device="cuda"), codes.cuda(), ones, ones.clone())
+    start = torch.arange(R + 1, dtype=torch.int32) * queries
+    q = torch.zeros(R * queries, 2 * H, D, dtype=torch.float16, device="cuda")
+    got = st.st_kv_attend(cache, q, table.cuda(), start.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), queries,
+                          max_len=max(lens) + extra).cpu().double()
+    for r, n in enumerate(lens):
+        for i in {0, queries // 2, queries - 1}:
+            seen = n - queries + i + 1
+            want = torch.bincount(owners[r][:max(0, seen)], minlength=D).double() / max(1, seen) * 100 / 32
+            off = (got[r * queries + i] - want).abs()
+            assert bool((off <= want * (2.0 ** -10 + 2.0 ** -19)).all()), (r, i, float((off / want).max()))

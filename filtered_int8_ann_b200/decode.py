@@ -107,6 +107,12 @@ def _attend_workspace(kv_heads: int, size: int, dim: int, T: int, heads: int, R:
     return need.value
 
 
+def _room(workspace) -> int:
+    """Bytes of a workspace given: all of them behind its address."""
+    _need(isinstance(workspace, torch.Tensor) and workspace.is_contiguous(), "workspace must be a contiguous tensor")
+    return workspace.numel() * workspace.element_size()
+
+
 class KvCache:
     """An int8 paged cache over caller-owned tensors: k, v int8 [num_blocks,
     kv_heads, block_size, head_dim] and their scales float32 [num_blocks,
@@ -238,11 +244,9 @@ def st_kv_attend(cache: KvCache, q: torch.Tensor, table: torch.Tensor, row_start
         # tokens apart from each other, and heads: one inside the other either way
         _need((T <= 1 or ot >= dim) and (heads <= 1 or oh >= dim) and
               (T <= 1 or heads <= 1 or ot >= (heads - 1) * oh + dim or oh >= (T - 1) * ot + dim), "out's vectors must not overlap")
+    room = 0 if workspace is None else _room(workspace)
     need = _attend_workspace(kv_heads, size, dim, T, heads, R, max_q, max_len)
-    room = 0
-    if workspace is not None:
-        room = workspace.numel() * workspace.element_size()
-    elif need:
+    if workspace is None and need:
         workspace, room = _empty1(need, torch.uint8, stream), need
     status = lib().st_kv_attend(cache._ref, pq, _DTYPES[q.dtype], T, heads, qt, qh, pt, width, ps, pl, R, max_q, max_len,
                                 dim ** -0.5 if scale is None else scale, int(causal), po, ot, oh,
@@ -288,14 +292,12 @@ def st_beam_select(logits: torch.Tensor, scores: torch.Tensor, keep: int, allow:
             out_finished = _empty2(B, keep, torch.bool, stream)
             ex.finished, ex.out_finished = pf, out_finished.data_ptr()
             ex.end_token = end_token
+    room = 0 if workspace is None else _room(workspace)
     _on_gpu(logits, "logits")
     need = _select_workspace(B, K, V, keep)
     out_scores = _empty2(B, keep, torch.float32, stream)
     out_parents, out_tokens = _empty2(B, keep, _I32, stream), _empty2(B, keep, _I32, stream)
-    room = 0
-    if workspace is not None:
-        room = workspace.numel() * workspace.element_size()
-    elif need:
+    if workspace is None and need:
         workspace, room = _empty1(need, torch.uint8, stream), need
     _check(lib().st_beam_select(logits.data_ptr(), kind, stride, pscores, B, K, V, keep, out_scores.data_ptr(), out_parents.data_ptr(), out_tokens.data_ptr(),
                                 None if ex is None else ctypes.byref(ex),

@@ -1,0 +1,27 @@
+"""What the binding may not pass on: workspaces smaller than they look, numbers beyond 32 bits, views that conjugate or negate."""
+import pytest
+import torch
+
+import filtered_int8_ann_b200 as st
+
+I32 = torch.int32
+
+
+def cache():
+    k, sc = torch.zeros(4, 2, 16, 64, dtype=torch.int8), torch.zeros(4, 2)
+    return st.KvCache(k, k.clone(), sc, sc.clone())
+
+
+def attend(max_q=1, **k):
+    x = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    return st.st_kv_attend(cache(), x, torch.zeros(2, 4, dtype=I32), torch.zeros(3, dtype=I32), torch.zeros(2, dtype=I32), max_q, out=x.clone(), **k)
+
+
+@pytest.mark.parametrize("room", [torch.empty(1, dtype=torch.uint8).expand(1 << 40), torch.empty(1 << 16, dtype=torch.uint8)[::2],
+                                  torch.empty(1, 64, dtype=torch.uint8).expand(1 << 20, 64), 77])
+def test_workspaces_that_are_not_dense(room):
+    """Their elements times their size is not the memory behind their address."""
+    with pytest.raises(ValueError, match="workspace"):
+        attend(workspace=room)
+    with pytest.raises(ValueError, match="workspace"):
+        st.st_beam_select(torch.zeros(2, 3, 50), torch.zeros(2, 3), 4, workspace=room)

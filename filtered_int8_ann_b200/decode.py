@@ -72,6 +72,12 @@ def _empty(shape, dtype, stream):
         return _empty_strided_cuda(shape, strides, dtype)
 
 
+def _int32(*numbers):
+    """The calls' 32-bit numbers: the marshalling would cut larger ones."""
+    if max(numbers) > 0x7fffffff or min(numbers) < -0x80000000:
+        raise ValueError(f"sizes and numbers must be within 32 bits, not {max(numbers, key=abs)}")
+
+
 def _no_gradient(x: torch.Tensor, name: str):
     """What the calls write is not recorded: a gradient through it would be lost."""
     if x.requires_grad and torch.is_grad_enabled():
@@ -178,6 +184,7 @@ def st_kv_plan(table: torch.Tensor, have: torch.Tensor, add: torch.Tensor, num_b
     if table.dim() != 2 or T < 0:
         raise ValueError("table must be [R, max_blocks], and T not negative")
     R, width = table.shape
+    _int32(R, width, num_blocks, block_size)
     pt, ph, pa = _array(table, _I32, (R, width), "table"), _array(have, _I32, (R,), "have"), _array(add, _I32, (R,), "add")
     _on_gpu(table, "table")
 
@@ -229,6 +236,8 @@ def st_kv_attend(cache: KvCache, q: torch.Tensor, table: torch.Tensor, row_start
     R, width = table.shape
     if max_len is None:
         max_len = width * size
+    _int32(R, width, max_q, heads)
+    _need(abs(max_len) < 1 << 63, "max_len must be within 64 bits")
     pt = _array(table, _I32, (R, width), "table")
     ps, pl = _array(row_start, _I32, (R + 1,), "row_start"), _array(lens, _I32, (R,), "lens")
     if out is None:
@@ -270,6 +279,7 @@ def st_beam_select(logits: torch.Tensor, scores: torch.Tensor, keep: int, allow:
         raise ValueError("logits must be [B, K, V] bfloat16, float16 or float32")
     _no_gradient(logits, "logits")
     B, K, V = logits.shape
+    _int32(B, K, V, keep, end_token)
     request, beam, one = logits.stride()
     if V > 1 and one != 1:
         raise ValueError("logits must have a dense vocabulary")
@@ -332,6 +342,7 @@ def st_beam_reorder(states: Sequence[torch.Tensor], parents: torch.Tensor, out: 
         raise ValueError("parents must be [B, keep], beam_dim 1 or 2, and states not empty")
     B, keep = parents.shape
     K = states[0].shape[beam_dim] if states[0].dim() > beam_dim else -1
+    _int32(B, K, keep)
     pp = _array(parents, _I32, (B, keep), "parents")
     rows = B * K
     made, words = [], []  # words: the eight of each st_beam_state

@@ -25,3 +25,21 @@ def test_workspaces_that_are_not_dense(room):
         attend(workspace=room)
     with pytest.raises(ValueError, match="workspace"):
         st.st_beam_select(torch.zeros(2, 3, 50), torch.zeros(2, 3), 4, workspace=room)
+
+
+def test_numbers_beyond_32_bits():
+    """They would be cut to their low bits, which may be in range."""
+    far = 1 << 32
+    table, rows = torch.zeros(2, 4, dtype=I32), torch.zeros(2, dtype=I32)
+    given = dict(slots=torch.zeros(3, dtype=torch.int64), sources=torch.zeros(3, dtype=I32), row_start=torch.zeros(3, dtype=I32), lens=rows.clone(), report=torch.zeros(4, dtype=I32))
+    logits, scores = torch.zeros(2, 3, 50), torch.zeros(2, 3)
+    meta = lambda *shape, dtype=torch.bfloat16: torch.empty(*shape, dtype=dtype, device="meta")  # noqa: E731
+    for call in (lambda: st.st_kv_plan(table, rows, rows, far + 8, 16, 3, **given), lambda: st.st_kv_plan(table, rows, rows, 8, far + 16, 3, **given),
+                 lambda: st.st_kv_plan(table, rows, rows, 8 - far, 16, 3, **given),
+                 lambda: attend(max_q=far + 1), lambda: attend(max_q=1 - far), lambda: attend(max_len=(1 << 64) + 64),
+                 lambda: st.st_beam_select(logits, scores, far + 4), lambda: st.st_beam_select(logits, scores, 4 - far),
+                 lambda: st.st_beam_select(logits, scores, 4, finished=torch.zeros(2, 3, dtype=torch.bool), end_token=far),
+                 lambda: st.st_beam_select(meta(1, 1, far + 50), torch.zeros(1, 1), 4),
+                 lambda: st.st_beam_reorder([meta(2, far + 3, 4)], torch.zeros(2, 3, dtype=I32), out=[meta(2, 3, 4)])):
+        with pytest.raises(ValueError, match="(32|64) bits"):
+            call()

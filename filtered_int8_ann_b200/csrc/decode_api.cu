@@ -110,6 +110,7 @@ bool apart_in_turns(const Vectors& a, __int128 na, const Vectors& b, __int128 nb
 // projection), or with strides that are multiples of a length in which both have their place (every other head).
 bool apart(const Vectors& a, const Vectors& b)
 {
+    if (a.n0 <= 1 && a.n1 <= 1 && b.n0 <= 1 && b.n1 <= 1) return !overlap(a.p, a.bytes, b.p, b.bytes);
     if (a.span() <= 0 || b.span() <= 0 || a.at() >= b.at() + b.span() || b.at() >= a.at() + a.span()) return true;
     const auto outer = [](const Vectors& x, const Vectors& y) {
         return x.n0 > 1 && y.n0 > 1 && x.s0 == y.s0 && x.s0 > 0 && x.inner() <= x.s0 && y.inner() <= y.s0 &&

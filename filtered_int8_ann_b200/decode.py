@@ -48,6 +48,8 @@ def _array(x: torch.Tensor, dtype, shape, name: str) -> int:
     """The address of a dense tensor of this type and shape."""
     if not isinstance(x, torch.Tensor) or x.dtype is not dtype or x.shape != shape or not x.is_contiguous():
         _wrong(x, dtype, shape, name)
+    if dtype is _F32 and (x.requires_grad or x.is_neg()):
+        _not_plain(x, name)
     return x.data_ptr()
 
 
@@ -72,16 +74,19 @@ def _empty(shape, dtype, stream):
         return _empty_strided_cuda(shape, strides, dtype)
 
 
-def _int32(*numbers):
-    """The calls' 32-bit numbers: the marshalling would cut larger ones."""
-    if max(numbers) > 0x7fffffff or min(numbers) < -0x80000000:
-        raise ValueError(f"sizes and numbers must be within 32 bits, not {max(numbers, key=abs)}")
+_TOP, _FAR = (1 << 31) - 1, (1 << 63) - 1  # the marshalling would cut larger numbers to their low bits
 
 
-def _no_gradient(x: torch.Tensor, name: str):
-    """What the calls write is not recorded: a gradient through it would be lost."""
-    if x.requires_grad and torch.is_grad_enabled():
-        raise ValueError(f"{name} requires a gradient and the decode calls have none: make them under torch.no_grad()")
+def _too_far(*numbers):
+    _need(False, f"sizes and numbers must be within {64 if max(map(abs, numbers)) > _FAR else 32} bits, not {max(numbers, key=abs)}")
+
+
+def _not_plain(x: torch.Tensor, name: str):
+    """For a tensor that requires a gradient (what the calls write is not recorded, so that it would be lost) or whose
+    memory does not hold its values."""
+    _need(not (x.requires_grad and torch.is_grad_enabled()),
+          f"{name} requires a gradient and the decode calls have none: make them under torch.no_grad()")
+    _need(not (x.is_neg() or x.is_conj()), f"{name} is a view that negates or conjugates: resolve it first (resolve_neg, resolve_conj)")
 
 
 def _on_gpu(x: torch.Tensor, name: str):
@@ -162,7 +167,8 @@ def _vectors(x: torch.Tensor, heads: Optional[int], dim: int, name: str):
     shape = x.shape
     if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
         raise ValueError(f"{name} must be [T, {'heads' if heads is None else heads}, {dim}], not {tuple(shape)}")
-    _no_gradient(x, name)
+    if x.requires_grad or x.is_neg():
+        _not_plain(x, name)
     token, head, one = x.stride()
     if one != 1:
         raise ValueError(f"{name} must have dense vectors")
@@ -184,7 +190,8 @@ def st_kv_plan(table: torch.Tensor, have: torch.Tensor, add: torch.Tensor, num_b
     if table.dim() != 2 or T < 0:
         raise ValueError("table must be [R, max_blocks], and T not negative")
     R, width = table.shape
-    _int32(R, width, num_blocks, block_size)
+    if not (R <= _TOP and width <= _TOP and -_TOP <= num_blocks <= _TOP and -_TOP <= block_size <= _TOP):
+        _too_far(R, width, num_blocks, block_size)
     pt, ph, pa = _array(table, _I32, (R, width), "table"), _array(have, _I32, (R,), "have"), _array(add, _I32, (R,), "add")
     _on_gpu(table, "table")
 
@@ -236,8 +243,8 @@ def st_kv_attend(cache: KvCache, q: torch.Tensor, table: torch.Tensor, row_start
     R, width = table.shape
     if max_len is None:
         max_len = width * size
-    _int32(R, width, max_q, heads)
-    _need(abs(max_len) < 1 << 63, "max_len must be within 64 bits")
+    if not (R <= _TOP and width <= _TOP and heads <= _TOP and -_TOP <= max_q <= _TOP and -_FAR <= max_len <= _FAR):
+        _too_far(R, width, heads, max_q, max_len)
     pt = _array(table, _I32, (R, width), "table")
     ps, pl = _array(row_start, _I32, (R + 1,), "row_start"), _array(lens, _I32, (R,), "lens")
     if out is None:
@@ -277,9 +284,11 @@ def st_beam_select(logits: torch.Tensor, scores: torch.Tensor, keep: int, allow:
     kind = _DTYPES.get(logits.dtype)
     if kind is None or logits.dim() != 3:
         raise ValueError("logits must be [B, K, V] bfloat16, float16 or float32")
-    _no_gradient(logits, "logits")
+    if logits.requires_grad or logits.is_neg():
+        _not_plain(logits, "logits")
     B, K, V = logits.shape
-    _int32(B, K, V, keep, end_token)
+    if not (B <= _TOP and K <= _TOP and V <= _TOP and -_TOP <= keep <= _TOP and -_TOP <= end_token <= _TOP):
+        _too_far(B, K, V, keep, end_token)
     request, beam, one = logits.stride()
     if V > 1 and one != 1:
         raise ValueError("logits must have a dense vocabulary")
@@ -287,7 +296,6 @@ def st_beam_select(logits: torch.Tensor, scores: torch.Tensor, keep: int, allow:
     if B > 1 and K > 1 and request != K * stride:
         raise ValueError("logits' beams must be evenly spaced")
     pscores = _array(scores, _F32, (B, K), "scores")
-    _no_gradient(scores, "scores")
     ex = out_finished = None
     if allow is not None or finished is not None:
         ex = _BeamExtras()
@@ -342,7 +350,8 @@ def st_beam_reorder(states: Sequence[torch.Tensor], parents: torch.Tensor, out: 
         raise ValueError("parents must be [B, keep], beam_dim 1 or 2, and states not empty")
     B, keep = parents.shape
     K = states[0].shape[beam_dim] if states[0].dim() > beam_dim else -1
-    _int32(B, K, keep)
+    if not (B <= _TOP and K <= _TOP and keep <= _TOP):
+        _too_far(B, K, keep)
     pp = _array(parents, _I32, (B, keep), "parents")
     rows = B * K
     made, words = [], []  # words: the eight of each st_beam_state
@@ -350,7 +359,8 @@ def st_beam_reorder(states: Sequence[torch.Tensor], parents: torch.Tensor, out: 
         shape = x.shape
         if len(shape) <= beam_dim or shape[beam_dim - 1] != B or shape[beam_dim] != K:
             raise ValueError(f"state {i} must have {B} requests of {K} beams at dimension {beam_dim}")
-        _no_gradient(x, f"state {i}")
+        if x.requires_grad or x.is_neg() or x.is_conj():
+            _not_plain(x, f"state {i}")
         size = x.element_size()
         if out is None and beam_dim == 1 and stream is None and rows and x.is_contiguous():  # the usual case
             _on_gpu(x, f"state {i}")
@@ -369,7 +379,7 @@ def st_beam_reorder(states: Sequence[torch.Tensor], parents: torch.Tensor, out: 
             y = out[i]
             if y.shape != new or y.dtype != x.dtype:
                 raise ValueError(f"out {i} must be {tuple(new)} {x.dtype}")
-            _no_gradient(y, f"out {i}")
+            _not_plain(y, f"out {i}")
         layers = (shape[0], size * x.stride(0), size * y.stride(0)) if beam_dim == 2 else (1, 0, 0)
         words += (x.data_ptr(), y.data_ptr(), size * math.prod(shape[beam_dim + 1:]), size * step,
                   size * _rows(y, beam_dim, f"out {i}"), *layers)

@@ -43,3 +43,20 @@ def test_numbers_beyond_32_bits():
                  lambda: st.st_beam_reorder([meta(2, far + 3, 4)], torch.zeros(2, 3, dtype=I32), out=[meta(2, 3, 4)])):
         with pytest.raises(ValueError, match="(32|64) bits"):
             call()
+
+
+def test_states_that_are_conjugated_or_negated_lazily():
+    """Their memory does not hold their values."""
+    z = torch.complex(torch.ones(2, 3, 4), torch.ones(2, 3, 4))
+    parents = torch.zeros(2, 3, dtype=I32)
+    for x in (z.conj(), z.conj().imag, torch._neg_view(torch.ones(2, 3, 4))):
+        for out in (None, [torch.zeros(2, 3, 4, dtype=x.dtype)]):
+            with pytest.raises(ValueError, match="resolve"):
+                st.st_beam_reorder([x], parents, out=out)
+    with pytest.raises(ValueError, match="resolve"):
+        st.st_beam_reorder([z], parents, out=[torch.zeros_like(z).conj()])
+    for x, call in ((torch.zeros(3, 2, 64).bfloat16(), lambda y: st.st_kv_append(cache(), y, y, torch.zeros(3, dtype=torch.int64))),
+                    (torch.zeros(2, 3, 50), lambda y: st.st_beam_select(y, torch.zeros(2, 3), 4)),
+                    (torch.zeros(2, 3), lambda y: st.st_beam_select(torch.zeros(2, 3, 50), y, 4)), (torch.zeros(4, 2), lambda y: st.KvCache(cache().k, cache().v, y, y))):
+        with pytest.raises(ValueError, match="resolve"):
+            call(torch._neg_view(x))

@@ -7,7 +7,7 @@
 // sum of exp(x - max), and the stretch's best entries. The second, a CTA per
 // request, forms the beams' normalisers and picks among the entries.
 //
-// The order has to be that of the numbers themselves, so everything that
+// The order has to be that of the numbers themselves, up to a relative 2e-12 of the normalisers' sums, so everything that
 // decides between beams is held in 64 bits: with scores near -20 an error of one fp32 rounding
 // (2e-6) would swap neighbours of different beams once in a few hundred kept pairs. exp is
 //   exp(x) = 2^(n/32) * (1 + r + r^2/2 + r^3/6 + r^4/24),  n = rint(32 x / ln2), r = x - n ln2/32, |r| <= ln2/64
@@ -21,8 +21,9 @@
 // written. Where equal logits make them too many, a bisection over
 // (logit, index) finds the exact border.
 //
-// 1024 beams of 100003 bf16 logits, a fifth of the beams finished (160 MB are read): 117 us and 11 for the second launch,
-// which hides a part of its 20 behind the first; 24 us would be the bytes'. Bound by instructions: 28 per logit (six of
+// 1024 beams of 100003 bf16 logits, a fifth of the beams finished (160 MB are read): 128 us for both launches, of which the
+// second waits for the first to end (only its launch is hidden; profiled alone, with cold caches, they take 116 and 21); 24 us
+// would be the bytes'. With none finished 160 us, as f16 162, as f32 206. Bound by instructions: 28 per logit (six of
 // them in fp64), 60% of the issue slots busy; the exponentials are about half of the time. 128 beams of 1021
 // logits: 14.5 us, each launch's chain of barriers.
 #include <cfloat>

@@ -17,11 +17,11 @@
 //                  the tokens' bytes with byte permutes; B = P^T is S^T's accumulator transposed by movmatrix
 // Each warp copies its next 32 tokens (cp.async, 16 bytes a lane) while it works on
 // the last: 12 warps per SM keep 96 KB of codes under way, where loads to registers kept too
-// few (64 rows of up to 16384 tokens, 8 cache heads of 128, 4 query heads each: 404 us; 236 so). The 16-byte pieces of
+// few (64 rows of up to 16384 tokens, 8 cache heads of 128, 4 query heads each: 404 us; 240 so). The 16-byte pieces of
 // a 128-byte line are permuted by the token so that both kinds of loads are free of bank conflicts.
-// That case reads 1.33 GB at 5.6 TB/s, 86% of a plain copy's rate: blocks of 32 tokens are pieces of 4 KB anywhere in
+// That case reads 1.33 GB at 5.5 TB/s, 85% of a plain copy's rate: blocks of 32 tokens are pieces of 4 KB anywhere in
 // memory, which costs about 7% against neighbouring ones, and the last wave of CTAs is not full. One row of 100003
-// tokens (205 MB): 49 us against 31 at that rate; each CTA's way to its first product and the join are 12 of them.
+// tokens (205 MB): 50 us against 31 at that rate; each CTA's way to its first product and the join are 12 of them.
 // A code becomes fp16 exactly: with the sign bit flipped it is the low byte of 1024 + 128 + code.
 // A query is scaled by a power of two to below 2 (exact in fp16 down to 2^-24 of
 // its largest element). The V operand's weight is 2^15 p_j vs_j / max vs: p_j is at most 1, so that fp16 holds
@@ -33,8 +33,10 @@ namespace st {
 
 constexpr int kDecWarps = 4;
 constexpr int kDecBlock = 32 * kDecWarps;
-// Columns (query tokens x heads per cache head) up to which this kernel is taken, 16 at a time: with 24 to 32 it takes
-// 256 to 270 us for 32 rows of 8192 tokens and the prompts' kernel 340, with 40 it takes 380 and that one 297.
+// Columns (query tokens x heads per cache head) up to which this kernel is taken, 16 at a time: with 24 to 32 it took
+// 256 to 270 us for 32 rows of 8192 tokens and the prompts' kernel 340, with 40 it took 380 and that one 297. A block of 16
+// columns copies and converts the cache for itself: such rows (8 cache heads of 128, 4 query heads each) take 104 us with one
+// query token, 110 with 2, 151 with 4, 283 with 8 and 301 with 16; their bytes are 82.
 constexpr int kDecMaxCols = 32;
 constexpr int kDecGroup = 32;             // tokens a warp takes at a time
 constexpr int kDecSixteens = 4096 / 16 + 2 * kDecWarps * kDecGroup / 16;  // of the longest stretch, and of the stages copied past it
@@ -557,7 +559,8 @@ struct DecPlan {
     int64_t bytes;  // of the workspace: a multiple of 16, the prompts' kernel's part may follow
 };
 
-// Stretches, multiples of the longest block. One row fills the GPU's places (3 CTAs per SM) once, all with
+// Stretches, multiples of the longest block, from the bound that the host knows: rows much shorter than max_len use few of
+// the CTAs (one row of 32768 tokens 22 us, under a bound of 131072 30). One row fills the GPU's places (3 CTAs per SM) once, all with
 // the same work (100003 tokens: 49 us; in two to four turns 52 to 62). Several rows, which may be uneven, get about
 // three CTAs per place, of 256 to 1024 tokens, so that the long ones' stretches fill in behind the short ones.
 // A short row is one stretch, which needs no join.
@@ -616,7 +619,7 @@ template <typename T, int D>
 static cudaError_t launch_join(const AttendArgs& a, int splits, int stretch, int per_row, int64_t ctas, cudaStream_t s)
 {
     const dim3 grid{unsigned(ctas)};
-    // few stretches are joined faster by small CTAs, many heads at a time (2048 heads of up to 16: the call takes 236 us, by
+    // few stretches are joined faster by small CTAs, many heads at a time (2048 heads of up to 16: the call took 236 us, by
     // 512 threads 256), many by large ones (64 heads of 53: 49 us, by 128 threads 51)
     if (splits <= 16) return launch_dep(kv_join_kernel<T, D, 128>, grid, dim3(128), 0, s, a, splits, stretch, per_row);
     return launch_dep(kv_join_kernel<T, D, 512>, grid, dim3(512), 0, s, a, splits, stretch, per_row);

@@ -404,7 +404,8 @@ static cudaError_t launch_plan(const PlanArgs& a, bool all_slots, cudaStream_t s
 cudaError_t launch_kv_plan(const PlanArgs& a, cudaStream_t s)
 {
     // Few tokens per row need no second launch (64 rows of one token: 8.2 us, with it 13.1); many do (1024 rows of 1000:
-    // 20 us, without it 48).
+    // 20 us, without it 48). Few rows of many tokens would need it sooner than this rule gives it (one row of 1028 tokens 28 us,
+    // of 1029 7).
     const bool all_slots = a.T <= 4 * int64_t(a.R) + 1024;
     const bool small = a.R <= kPlanSmallRows && a.num_blocks <= kPlanSmallBlocks &&
                        int64_t(a.R) * a.max_blocks <= kPlanSmallEntries;

@@ -20,11 +20,12 @@
 // raised only when a score exceeds it by 8 (then O is rescaled in TMEM): p
 // is at most 2^8, and 2^7 times it and its V factor fits into fp16 and is held with 11 bits down to 2^-21.
 //
-// 4 rows of 2048 queries over up to 8192 tokens, 8 cache heads of 128 and 4 query heads each (0.28 PFLOP): 456 us, 0.62
-// PFLOP/s. A pair of tiles takes 4500 to 5600 cycles per 128 tokens, of which the products are 2570: a tile's S, its
+// Prompts of 1793 queries over 8192 tokens and of 722 over 6144, 8 cache heads of 128 and 4 query heads each (0.28 TFLOP):
+// 469 us, 0.60 PFLOP/s, two rows of one query in the same call and the join of their stretches included; 4 prompts of 2048 over
+// 8192 each (0.96 TFLOP) 1283 us, 0.75. A pair of tiles takes 4500 to 5600 cycles per 128 tokens, of which the products are 2570: a tile's S, its
 // softmax and its P V follow each other, and two tiles hide only a part of it (without any arithmetic in the softmax
-// and the conversions 335 us). The pairs that see most come first, yet the last ones leave a fifth of the
-// SMs' time unused; splitting them along the cache cost more (608 us) than it filled.
+// and the conversions 335 us). Every pair converts its row's K and V anew. The pairs that see most come first, yet the last
+// ones leave a fifth of the SMs' time unused; splitting them along the cache cost more (608 us) than it filled.
 //
 // Up to 128 columns stand in both tiles, which take the steps in turn, instead of leaving one tile empty: 32 rows of
 // 8192 tokens with 64 columns 298 us, 431 otherwise.
@@ -805,7 +806,9 @@ struct PrePlan {
 };
 
 // Stretches: one while the columns alone fill the GPU (a join would only add to the work), else enough for two CTAs
-// per SM, none longer than the table that fits, of at least 1024 tokens.
+// per SM, none longer than the table that fits, of at least 1024 tokens. Every row counts as work here, short ones that the
+// decode kernel takes too: few prompt columns beside many such rows get fewer stretches than they would alone (a prompt of 64
+// tokens over 16384, 4 query heads each, 53 us; beside 63 rows of one token, which alone take 370, both take 898).
 static PrePlan pre_plan(const st_kv_cache& c, int64_t T, int32_t q_heads, int32_t R, int64_t max_len)
 {
     PrePlan p;

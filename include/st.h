@@ -530,8 +530,8 @@ st_status st_kv_append(const st_kv_cache* cache, const void* k, const void* v, s
  *   table      device int32 [R][max_blocks], row_start device int32 [R+1] (nondecreasing,
  *              within [0, T]), lens device int32 [R]
  *   max_q      most query tokens of a row (1 to 2^20); max_len: most cached tokens of a
- *              row (1 to max_blocks * block_size). They size the launch: a row
- *              with more of either sets the decode error word, and its tokens get zeros.
+ *              row (1 to max_blocks * block_size). They size the launch and the workspace, and close bounds make
+ *              the call faster: a row with more of either sets the decode error word, and its tokens get zeros.
  *   scale      finite, times log2 e too
  *   workspace  device, 16-byte aligned, of at least the bytes that
  *              st_kv_attend_workspace gives (NULL when that is 0)
@@ -577,8 +577,9 @@ typedef struct {
 /*
  * The `keep` best pairs (beam i, token v) of each request by
  *   score(i, v) = scores[i] + logits[i][v] - ln(sum over allowed u of exp(logits[i][u]))
- * ordered by score descending, then i * V + v ascending. The order is that of the
- * numbers as they stand (the sum is taken in 64 bits), not of rounded scores.
+ * ordered by score descending, then i * V + v ascending. The order is that of the scores computed in
+ * 64 bits, not of rounded ones, with sums whose relative error is below 1e-11: pairs of different beams that are
+ * closer than that may stand in either order. Pairs of one beam, and of beams with equal logits and scores, do not depend on it.
  *
  *   logits      device bf16, f16 or f32 [B][K][V], consecutive beams logits_stride elements
  *               apart (at least V); aligned to the element only
